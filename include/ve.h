@@ -230,7 +230,13 @@ ve_status ve_dbuffer_group_op(const ve_plan* plan, int32_t rank, int32_t op, flo
  *   "wg_rows" (VE_WG_ROWS, 1): 0 = whole-row blocks of 2,048 or 4,096
  *       groups (rows of 8K or 16K elements) run one workgroup per block
  *       instead of persistent items of 4 or 2 consecutive blocks (same
- *       results, slower; needs "wg_dynamic" and no pinned shape).
+ *       results, slower; needs "wg_dynamic" and no pinned shape);
+ *   "linear_path" (VE_LINEAR_PATH, 0): pin the form of the linear layer's
+ *       products where it applies: 1 = register staged (any alignment), 2 /
+ *       3 = direct-to-LDS 128^2 / 256^2 tiles; 0 = chosen by shape;
+ *   "linear_split" (VE_LINEAR_SPLIT, 1): 0 = never cut their contraction
+ *       into slices (the options must not change between a workspace query
+ *       and the call it is for).
  * ve_set_option changes a value for every later call of the process
  * (calls already queued are unaffected); ve_get_option reads it.  Errors:
  * an unknown name or a NULL value pointer gives VE_ERR_INVALID_ARG. */
@@ -344,6 +350,113 @@ ve_status ve_muon_newton_schulz_noalloc(const uint16_t* G, uint16_t* out, int64_
 ve_status ve_gemm_bf16_nt(const uint16_t* P, int64_t ldp, const uint16_t* Q, int64_t ldq, const uint16_t* D,
                           int64_t ldd, uint16_t* C, int64_t ldc, uint16_t* CT, int64_t ldct, int64_t M, int64_t N,
                           int64_t K, float alpha, float beta, int32_t symmetric, void* stream);
+
+/* Activations saved in 8 bits: a matrix of int8 codes with one fp32 scale
+ * for each row and each run of `block` consecutive columns (the last run of
+ * a row may be shorter).  The rule is the step's: scale = amax / 127, code =
+ * clamp(rint(v * (127 / amax)), -127, 127), amax 0 gives scale 0 and codes 0;
+ * below amax 2^-100 both factors are first scaled by 2^64, so that the
+ * quotient stays finite.  A run that holds an infinity or NaN has scale NaN
+ * and codes 0, so that it restores to NaN.  The value a code stands for is
+ * bf16(code * scale), rounded once (nearest even). */
+typedef struct {
+    int8_t* codes;    /* device [rows x cols], row-major */
+    int64_t ld_codes; /* elements from one row of codes to the next, >= cols */
+    float* scales;    /* device [rows x ceil(cols / block)], row-major */
+    int64_t ld_scales;
+    int32_t block;    /* 32, 64 or 128 */
+} ve_act8;
+
+/* Save (pack) the bf16 rows x cols matrix x as codes and scales, or restore
+ * (unpack) it.  One pass over memory.  rows >= 0 (0: no-op), 1 <= cols <
+ * 2^31, leading dimensions at least the row; any alignment is correct, rows
+ * that start on 16 bytes (codes: 8) are faster.  Buffers may not overlap. */
+ve_status ve_act8_pack(const uint16_t* x, int64_t ldx, int64_t rows, int64_t cols, const ve_act8* out, void* stream);
+ve_status ve_act8_unpack(const ve_act8* in, int64_t rows, int64_t cols, uint16_t* x, int64_t ldx, void* stream);
+
+/* Activation functions of the linear layer. */
+typedef enum {
+    VE_ACT_NONE = 0,
+    VE_ACT_RELU = 1,      /* max(z, 0); slope 0 at 0 */
+    VE_ACT_GELU = 2,      /* z (1 + erf(z / sqrt 2)) / 2 */
+    VE_ACT_GELU_TANH = 3, /* z (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3))) / 2 */
+    VE_ACT_SILU = 4       /* z / (1 + exp(-z)) */
+} ve_activation;
+
+/* Forward pass of a linear layer, dense or grouped by expert:
+ *   z[t,n] = sum_k x[t,k] w[e,n,k] + bias[e,n],  y[t,n] = bf16(act(z[t,n]) + residual[t,n])
+ * where token t belongs to group e: rows [offsets[e], offsets[e + 1]) of x.
+ * Products of bf16 accumulate in fp32 on the MFMA units; bias, activation
+ * and residual are applied in fp32 and y is rounded once.  For the backward
+ * pass z can be written as bf16 (z) or in 8 bits (z8, from the fp32 values),
+ * in the same pass.
+ * All matrices are row-major bf16 on the device with the given leading
+ * dimensions (elements). */
+typedef struct {
+    int64_t tokens, in_features, out_features;  /* tokens >= 0 (0: no-op) */
+    int32_t groups;                             /* 1 .. 65536 */
+    int32_t activation;                         /* ve_activation */
+    const int64_t* offsets; /* device [groups + 1], non-decreasing in [0, tokens]; NULL only with one
+                               group: all tokens.  Groups may be empty; rows in no group are neither
+                               read nor written.  Offsets outside these rules give undefined values,
+                               but no access outside the buffers. */
+    const uint16_t* x; int64_t ldx;             /* [tokens x in_features] */
+    const uint16_t* w; int64_t ldw, w_group;    /* groups matrices [out_features x in_features], w_group
+                                                   elements from one to the next */
+    const uint16_t* bias; int64_t bias_group;   /* groups vectors [out_features], or NULL */
+    const uint16_t* residual; int64_t ldr;      /* [tokens x out_features] or NULL; may be y itself */
+    uint16_t* y; int64_t ldy;                   /* [tokens x out_features] */
+    uint16_t* z; int64_t ldz;                   /* out, or NULL */
+    ve_act8 z8;                                 /* out, or codes NULL */
+} ve_linear_forward_args;
+
+/* Backward pass of the same layer:
+ *   dz[t,n] = dy[t,n] act'(z[t,n])                        (fp32)
+ *   dx[t,k] = bf16(sum_n bf16(dz[t,n]) w[e,n,k] + dx_add[t,k])
+ *   dw[e,n,k] (+)= sum_{t in e} bf16(dz[t,n]) x[t,k]
+ *   dbias[e,n] (+)= sum_{t in e} dz[t,n]
+ * The MFMA units take bf16, so dz is rounded once before the two products
+ * (not with VE_ACT_NONE, where dz is dy); sums are fp32.  x and z come as
+ * bf16 or in 8 bits (then their restored values are what is computed with:
+ * the same results, bit for bit, as from ve_act8_unpack's output).  Any
+ * output may be NULL, and then what only it needs may be NULL too: w is read
+ * for dx, x for dw.  Empty groups get dw = dbias = 0 (or keep theirs with
+ * accumulate).  dx, dw and dbias of a call do not depend on anything but its
+ * inputs: no atomics, the same bits every call. */
+typedef struct {
+    int64_t tokens, in_features, out_features;
+    int32_t groups;
+    int32_t activation;
+    const int64_t* offsets;
+    const uint16_t* dy; int64_t lddy;           /* [tokens x out_features] */
+    const uint16_t* w; int64_t ldw, w_group;
+    const uint16_t* x; int64_t ldx;             /* exactly one of x and x8.codes with dw */
+    ve_act8 x8;
+    const uint16_t* z; int64_t ldz;             /* exactly one of z and z8.codes unless VE_ACT_NONE */
+    ve_act8 z8;
+    uint16_t* dx; int64_t lddx;                 /* [tokens x in_features], or NULL */
+    const uint16_t* dx_add; int64_t ld_add;     /* [tokens x in_features] or NULL; may be dx itself */
+    void* dw; int64_t lddw, dw_group;           /* groups matrices [out_features x in_features], or NULL:
+                                                   bf16, or fp32 with grad_fp32; e.g. where the tensor
+                                                   lies in a DBuffer bucket */
+    void* dbias; int64_t dbias_group;           /* groups vectors, of dw's type, or NULL */
+    int32_t grad_fp32;                          /* dw and dbias are fp32 */
+    int32_t accumulate;                         /* add to what dw and dbias hold */
+} ve_linear_backward_args;
+
+/* Device scratch a call needs (0 is common; the arguments' sizes and which of
+ * its pointers are NULL decide, nothing is read through them).  The caller
+ * owns the workspace, 256-byte aligned; its contents are scratch, and calls
+ * that may overlap must not share one.  Errors of all four: NULL arguments or
+ * needed pointers, sizes, groups or leading dimensions out of range (a
+ * leading dimension shorter than the row, groups > 1 without offsets), an
+ * unknown activation, a block other than 32, 64 or 128, a short or
+ * misaligned workspace: VE_ERR_INVALID_ARG; sizes beyond one launch:
+ * VE_ERR_UNSUPPORTED; launch failures: VE_ERR_DEVICE. */
+ve_status ve_linear_forward_workspace(const ve_linear_forward_args* a, int64_t* bytes);
+ve_status ve_linear_forward(const ve_linear_forward_args* a, void* workspace, int64_t workspace_bytes, void* stream);
+ve_status ve_linear_backward_workspace(const ve_linear_backward_args* a, int64_t* bytes);
+ve_status ve_linear_backward(const ve_linear_backward_args* a, void* workspace, int64_t workspace_bytes, void* stream);
 
 /* Thread-local message of this thread's last failing call ("" if none). */
 const char* ve_last_error(void);

@@ -33,10 +33,15 @@ _STATUS = {0: "VE_OK", 1: "VE_ERR_INVALID_ARG", 2: "VE_ERR_LAYOUT", 3: "VE_ERR_O
 EXPORTS = ("ve_plan_load", "ve_plan_free", "ve_plan_query", "ve_dbuffer_copy_in",
            "ve_shard_adam8bit_step", "ve_dbuffer_slice", "ve_dbuffer_group_op", "ve_plan_layout", "ve_plan_buckets",
            "ve_muon_workspace_bytes", "ve_muon_newton_schulz", "ve_muon_newton_schulz_noalloc",
-           "ve_gemm_bf16_nt", "ve_stream_copy", "ve_set_option", "ve_get_option", "ve_last_error")
+           "ve_gemm_bf16_nt", "ve_act8_pack", "ve_act8_unpack", "ve_linear_forward_workspace", "ve_linear_forward",
+           "ve_linear_backward_workspace", "ve_linear_backward",
+           "ve_stream_copy", "ve_set_option", "ve_get_option", "ve_last_error")
 
 # ve_group_op
 GROUP_ZERO, GROUP_SCALE, GROUP_ACCUMULATE = 0, 1, 2
+
+# ve_activation
+ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
 
 
 class VeError(RuntimeError):
@@ -53,6 +58,31 @@ class TensorSpec(C.Structure):
 class AdamHParams(C.Structure):
     _fields_ = [("lr", C.c_float), ("beta1", C.c_float), ("beta2", C.c_float), ("eps", C.c_float),
                 ("weight_decay", C.c_float)]
+
+
+class _Act8(C.Structure):
+    _fields_ = [("codes", C.c_void_p), ("ld_codes", C.c_int64), ("scales", C.c_void_p), ("ld_scales", C.c_int64),
+                ("block", C.c_int32)]
+
+
+_SHAPE_FIELDS = [("tokens", C.c_int64), ("in_features", C.c_int64), ("out_features", C.c_int64),
+                 ("groups", C.c_int32), ("activation", C.c_int32), ("offsets", C.c_void_p)]
+
+
+class _LinearForward(C.Structure):
+    _fields_ = _SHAPE_FIELDS + [
+        ("x", C.c_void_p), ("ldx", C.c_int64), ("w", C.c_void_p), ("ldw", C.c_int64), ("w_group", C.c_int64),
+        ("bias", C.c_void_p), ("bias_group", C.c_int64), ("residual", C.c_void_p), ("ldr", C.c_int64),
+        ("y", C.c_void_p), ("ldy", C.c_int64), ("z", C.c_void_p), ("ldz", C.c_int64), ("z8", _Act8)]
+
+
+class _LinearBackward(C.Structure):
+    _fields_ = _SHAPE_FIELDS + [
+        ("dy", C.c_void_p), ("lddy", C.c_int64), ("w", C.c_void_p), ("ldw", C.c_int64), ("w_group", C.c_int64),
+        ("x", C.c_void_p), ("ldx", C.c_int64), ("x8", _Act8), ("z", C.c_void_p), ("ldz", C.c_int64), ("z8", _Act8),
+        ("dx", C.c_void_p), ("lddx", C.c_int64), ("dx_add", C.c_void_p), ("ld_add", C.c_int64),
+        ("dw", C.c_void_p), ("lddw", C.c_int64), ("dw_group", C.c_int64),
+        ("dbias", C.c_void_p), ("dbias_group", C.c_int64), ("grad_fp32", C.c_int32), ("accumulate", C.c_int32)]
 
 
 # ve_shard_state: eight device pointers, in this order
@@ -83,6 +113,12 @@ def lib() -> C.CDLL:
         L.ve_muon_newton_schulz.argtypes = [P, P, C.c_int64, C.c_int64, C.c_int32, C.c_float, P, C.c_int64, P]
         L.ve_gemm_bf16_nt.argtypes = [P, C.c_int64, P, C.c_int64, P, C.c_int64, P, C.c_int64, P, C.c_int64,
                                       C.c_int64, C.c_int64, C.c_int64, C.c_float, C.c_float, C.c_int32, P]
+        L.ve_act8_pack.argtypes = [P, C.c_int64, C.c_int64, C.c_int64, P, P]
+        L.ve_act8_unpack.argtypes = [P, C.c_int64, C.c_int64, P, C.c_int64, P]
+        L.ve_linear_forward_workspace.argtypes = [P, P]
+        L.ve_linear_forward.argtypes = [P, P, C.c_int64, P]
+        L.ve_linear_backward_workspace.argtypes = [P, P]
+        L.ve_linear_backward.argtypes = [P, P, C.c_int64, P]
         L.ve_stream_copy.argtypes = [P, P, C.c_int64, P]
         L.ve_set_option.argtypes = [C.c_char_p, C.c_int64]
         L.ve_get_option.argtypes = [C.c_char_p, P]
@@ -333,6 +369,295 @@ def gemm_bf16_nt(P, Q, C=None, CT=None, D=None, alpha: float = 1.0, beta: float 
     _require_buffer(Q, N * K, 2, "Q")
     _check(lib().ve_gemm_bf16_nt(_ptr_of(P), K, _ptr_of(Q), K, _ptr_of(D), N, _ptr_of(C), N, _ptr_of(CT), M,
                                  M, N, K, float(alpha), float(beta), int(bool(symmetric)), _stream_handle(stream)))
+
+
+# ---------------------------------------------------------------------------
+# linear layers and 8-bit saved activations
+
+def _matrix(t, rows, cols, name, device, itemsize=2):
+    """(pointer, leading dimension) of a rows x cols device matrix whose rows
+    are contiguous (any stride between them)."""
+    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols:
+        raise ValueError(f"{name}: shape {tuple(t.shape)} != {(rows, cols)}")
+    if t.device != device or not t.is_cuda:
+        raise ValueError(f"{name}: must be a device tensor on {device}")
+    return t.data_ptr(), _lead(t, rows, cols, name, itemsize)
+
+
+def _lead(t, rows, cols, name, itemsize):
+    _elements(t, name, itemsize)
+    ld, inner = t.stride()[-2:]
+    if inner != 1 and cols > 1:
+        raise ValueError(f"{name}: rows must be contiguous")
+    return ld if rows > 1 else max(ld, cols)
+
+
+def _elements(t, name, itemsize):
+    if t.element_size() != itemsize or (itemsize == 2 and "float16" == str(t.dtype)[6:]):
+        raise ValueError(f"{name}: need {itemsize}-byte elements" + (" (bf16 bits)" if itemsize == 2 else ""))
+
+
+def _groups_of(t, groups, rows, cols, name, device, itemsize=2):
+    """(pointer, leading dimension, group stride) of [rows, cols] (no groups)
+    or [groups, rows, cols]."""
+    if groups is None:
+        ptr, ld = _matrix(t, rows, cols, name, device, itemsize)
+        return ptr, ld, 0
+    if tuple(t.shape) != (groups, rows, cols):
+        raise ValueError(f"{name}: shape {tuple(t.shape)} != {(groups, rows, cols)}")
+    if t.device != device or not t.is_cuda:
+        raise ValueError(f"{name}: must be a device tensor on {device}")
+    return t.data_ptr(), _lead(t, rows, cols, name, itemsize), t.stride(0)
+
+
+def _vectors_of(t, groups, n, name, device, itemsize=2):
+    """(pointer, group stride) of [n] or [groups, n]."""
+    want = (n,) if groups is None else (groups, n)
+    if tuple(t.shape) != want:
+        raise ValueError(f"{name}: shape {tuple(t.shape)} != {want}")
+    if t.device != device or not t.is_cuda:
+        raise ValueError(f"{name}: must be a device tensor on {device}")
+    _elements(t, name, itemsize)
+    if t.stride(-1) != 1 and n > 1:
+        raise ValueError(f"{name}: must be contiguous")
+    return t.data_ptr(), 0 if groups is None else t.stride(0)
+
+
+class Act8:
+    """An activation matrix saved in 8 bits (``ve_act8``): int8 ``codes``
+    [rows, cols] and fp32 ``scales`` [rows, ceil(cols / block)], device
+    tensors with contiguous rows."""
+
+    __slots__ = ("codes", "scales", "block")
+
+    def __init__(self, codes, scales, block: int = 128):
+        self.codes, self.scales, self.block = codes, scales, int(block)
+
+    def _fill(self, rows, cols, name, device):
+        b = self.block
+        if b not in (32, 64, 128):
+            raise ValueError(f"{name}: block {b} is not 32, 64 or 128")
+        c, ldc = _matrix(self.codes, rows, cols, f"{name}.codes", device, 1)
+        s, lds = _matrix(self.scales, rows, -(-cols // b), f"{name}.scales", device, 4)
+        return _Act8(c, ldc, s, lds, b)
+
+
+def new_act8(rows: int, cols: int, block: int = 128, device="cuda") -> Act8:
+    """Allocate an :class:`Act8` for a rows x cols matrix."""
+    import torch
+    return Act8(torch.empty(rows, cols, dtype=torch.int8, device=device),
+                torch.empty(rows, -(-cols // block), dtype=torch.float32, device=device), block)
+
+
+class _On:
+    """The stream of a call whose tensors live on ``device`` (the device's
+    current stream if None), with that device current while it launches."""
+
+    __slots__ = ("device", "stream", "handle", "before")
+
+    def __init__(self, device, stream):
+        import torch
+        self.device, self.stream = device, stream
+        if stream is None:
+            self.handle = torch.cuda.current_stream(device).cuda_stream
+        else:
+            self.handle = stream if isinstance(stream, int) else stream.cuda_stream
+            if not isinstance(stream, int) and stream.device != device:
+                raise ValueError(f"stream on {stream.device}, tensors on {device}")
+
+    def __enter__(self):
+        import torch
+        now = torch.cuda.current_device()
+        self.before = now if now != self.device.index else None
+        if self.before is not None:
+            torch.cuda.set_device(self.device)
+        return self
+
+    def __exit__(self, *exc):
+        if self.before is not None:
+            import torch
+            torch.cuda.set_device(self.before)
+        return False
+
+    def workspace(self, need: int, given):
+        """(pointer, bytes) of the call's scratch.  Where it is allocated here
+        it belongs to the call's stream, so the allocator hands it out again
+        only behind the call."""
+        if given is not None:
+            if given.device != self.device:
+                raise ValueError("workspace: must be on the tensors' device")
+            _require_buffer(given, need, 1, "workspace")
+            return given.data_ptr(), given.numel()
+        if need == 0:
+            return None, 0
+        import torch
+        if self.stream is None:
+            return torch.empty(need, dtype=torch.uint8, device=self.device)
+        st = torch.cuda.ExternalStream(self.stream, self.device) if isinstance(self.stream, int) else self.stream
+        with torch.cuda.stream(st):
+            return torch.empty(need, dtype=torch.uint8, device=self.device)
+
+
+def _run(call, args, query, device, stream, workspace):
+    with _On(device, stream) as on:
+        need = C.c_int64()
+        _check(query(C.byref(args), C.byref(need)))
+        ws = on.workspace(need.value, workspace)
+        ptr, size = ws if isinstance(ws, tuple) else (ws.data_ptr(), need.value)
+        _check(call(C.byref(args), ptr, size, on.handle))
+
+
+def act8_pack(x, out: Act8, stream=None) -> Act8:
+    """``ve_act8_pack``: save the 2-D bf16 matrix ``x`` in 8 bits."""
+    rows, cols = x.shape
+    ptr, ld = _matrix(x, rows, cols, "x", x.device)
+    q = out._fill(rows, cols, "out", x.device)
+    with _On(x.device, stream) as on:
+        _check(lib().ve_act8_pack(ptr, ld, rows, cols, C.byref(q), on.handle))
+    return out
+
+
+def act8_unpack(q: Act8, out, stream=None):
+    """``ve_act8_unpack``: restore a saved matrix as bf16 into ``out``."""
+    rows, cols = out.shape
+    ptr, ld = _matrix(out, rows, cols, "out", out.device)
+    s = q._fill(rows, cols, "q", out.device)
+    with _On(out.device, stream) as on:
+        _check(lib().ve_act8_unpack(C.byref(s), rows, cols, ptr, ld, on.handle))
+    return out
+
+
+def _shape(a, tokens, w, offsets, activation, device, wname="w"):
+    """Fill the shape of an argument record; returns groups (None without offsets)."""
+    groups = None
+    if offsets is not None:
+        if offsets.dim() != 1 or offsets.shape[0] < 2 or str(offsets.dtype) != "torch.int64":
+            raise ValueError("offsets: a 1-D int64 tensor of groups + 1 elements")
+        if offsets.device != device or not offsets.is_contiguous():
+            raise ValueError(f"offsets: must be contiguous on {device}")
+        groups = offsets.shape[0] - 1
+        a.offsets = offsets.data_ptr()
+    if w.dim() != (2 if groups is None else 3):
+        raise ValueError(f"{wname}: [out, in] features, or [groups, out, in] with offsets")
+    a.tokens, a.in_features, a.out_features = tokens, w.shape[-1], w.shape[-2]
+    a.groups = 1 if groups is None else groups
+    act = ACTIVATIONS.get(activation, activation)
+    if not isinstance(act, int):
+        raise ValueError(f"unknown activation {activation!r}; one of {sorted(ACTIVATIONS)}")
+    a.activation = act
+    return groups
+
+
+def linear_forward(x, w, y, bias=None, activation="none", residual=None, z=None, z8=None, offsets=None,
+                   workspace=None, stream=None):
+    """``ve_linear_forward``: y = act(x w^T + bias) + residual.
+
+    ``x`` [tokens, in], ``w`` [out, in], ``y`` / ``residual`` / ``z``
+    [tokens, out], ``bias`` [out]: bf16 device tensors with contiguous rows.
+    With ``offsets`` (int64 on the device, [groups + 1]), rows
+    [offsets[e], offsets[e + 1]) belong to expert e, and ``w`` is [groups,
+    out, in], ``bias`` [groups, out].  ``z`` (bf16) or ``z8`` (:class:`Act8`)
+    receives the input of the activation for the backward pass.
+    ``residual`` may be ``y``.  ``workspace``: uint8, at least
+    :func:`linear_forward_workspace` bytes (allocated here if None)."""
+    return _forward(x, w, y, bias, activation, residual, z, z8, offsets, workspace, stream, False)
+
+
+def linear_forward_workspace(x, w, y, bias=None, activation="none", residual=None, z=None, z8=None,
+                             offsets=None) -> int:
+    """``ve_linear_forward_workspace`` of the same call (bytes)."""
+    return _forward(x, w, y, bias, activation, residual, z, z8, offsets, None, None, True)
+
+
+def _forward(x, w, y, bias, activation, residual, z, z8, offsets, workspace, stream, query):
+    a, dev = _LinearForward(), x.device
+    if x.dim() != 2:
+        raise ValueError("x: [tokens, in] features")
+    g = _shape(a, x.shape[0], w, offsets, activation, dev)
+    T, K, N = a.tokens, a.in_features, a.out_features
+    a.x, a.ldx = _matrix(x, T, K, "x", dev)
+    a.w, a.ldw, a.w_group = _groups_of(w, g, N, K, "w", dev)
+    a.y, a.ldy = _matrix(y, T, N, "y", dev)
+    if bias is not None:
+        a.bias, a.bias_group = _vectors_of(bias, g, N, "bias", dev)
+    if residual is not None:
+        a.residual, a.ldr = _matrix(residual, T, N, "residual", dev)
+    if z is not None:
+        a.z, a.ldz = _matrix(z, T, N, "z", dev)
+    if z8 is not None:
+        a.z8 = z8._fill(T, N, "z8", dev)
+    L = lib()
+    if query:
+        need = C.c_int64()
+        _check(L.ve_linear_forward_workspace(C.byref(a), C.byref(need)))
+        return need.value
+    _run(L.ve_linear_forward, a, L.ve_linear_forward_workspace, dev, stream, workspace)
+    return y
+
+
+def linear_backward(dy, w, x=None, z=None, activation="none", dx=None, dx_add=None, dw=None, dbias=None,
+                    accumulate=False, offsets=None, workspace=None, stream=None):
+    """``ve_linear_backward``: the gradients ``dx`` (bf16, plus ``dx_add``),
+    ``dw`` and ``dbias`` (both bf16, or both fp32; added to what they hold
+    with ``accumulate``); each may be None.
+
+    ``x`` (needed for ``dw``) and ``z`` (needed unless the activation is
+    "none") are bf16 tensors or :class:`Act8`.  ``dw`` may be any tensor of
+    w's shape with contiguous rows, e.g. a view of a DBuffer bucket at the
+    tensor's offset.  ``dx_add`` may be ``dx``."""
+    _backward(dy, w, x, z, activation, dx, dx_add, dw, dbias, accumulate, offsets, workspace, stream, False)
+
+
+def linear_backward_workspace(dy, w, x=None, z=None, activation="none", dx=None, dx_add=None, dw=None, dbias=None,
+                              accumulate=False, offsets=None) -> int:
+    """``ve_linear_backward_workspace`` of the same call (bytes)."""
+    return _backward(dy, w, x, z, activation, dx, dx_add, dw, dbias, accumulate, offsets, None, None, True)
+
+
+def _backward(dy, w, x, z, activation, dx, dx_add, dw, dbias, accumulate, offsets, workspace, stream, query):
+    a, dev = _LinearBackward(), dy.device
+    if dy.dim() != 2:
+        raise ValueError("dy: [tokens, out] features")
+    g = _shape(a, dy.shape[0], w, offsets, activation, dev)
+    T, K, N = a.tokens, a.in_features, a.out_features
+    a.dy, a.lddy = _matrix(dy, T, N, "dy", dev)
+    a.w, a.ldw, a.w_group = _groups_of(w, g, N, K, "w", dev)
+    if isinstance(x, Act8):
+        a.x8 = x._fill(T, K, "x", dev)
+    elif x is not None:
+        a.x, a.ldx = _matrix(x, T, K, "x", dev)
+    elif dw is not None:
+        raise ValueError("dw needs x")
+    if isinstance(z, Act8):
+        a.z8 = z._fill(T, N, "z", dev)
+    elif z is not None:
+        a.z, a.ldz = _matrix(z, T, N, "z", dev)
+    elif a.activation:
+        raise ValueError("the activation's gradient needs z")
+    if dx is not None:
+        a.dx, a.lddx = _matrix(dx, T, K, "dx", dev)
+        if dx_add is not None:
+            a.dx_add, a.ld_add = _matrix(dx_add, T, K, "dx_add", dev)
+    elif dx_add is not None:
+        raise ValueError("dx_add without dx")
+    sizes = {t.element_size() for t in (dw, dbias) if t is not None}
+    if len(sizes) > 1 or not sizes <= {2, 4}:
+        raise ValueError("dw and dbias: both bf16 or both fp32")
+    item = sizes.pop() if sizes else 2
+    for t, name in ((dw, "dw"), (dbias, "dbias")):
+        if t is not None and item == 4 and str(t.dtype) != "torch.float32":
+            raise ValueError(f"{name}: need bf16 or fp32")
+    a.grad_fp32, a.accumulate = int(item == 4), int(bool(accumulate))
+    if dw is not None:
+        a.dw, a.lddw, a.dw_group = _groups_of(dw, g, N, K, "dw", dev, item)
+    if dbias is not None:
+        a.dbias, a.dbias_group = _vectors_of(dbias, g, N, "dbias", dev, item)
+    L = lib()
+    if query:
+        need = C.c_int64()
+        _check(L.ve_linear_backward_workspace(C.byref(a), C.byref(need)))
+        return need.value
+    _run(L.ve_linear_backward, a, L.ve_linear_backward_workspace, dev, stream, workspace)
 
 
 def stream_copy(dst, src, stream=None):

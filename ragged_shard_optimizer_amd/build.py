@@ -23,7 +23,8 @@ CSRC = os.path.join(PKG, "csrc")
 OUT = os.path.join(PKG, "_build", "libve.so")
 SOURCES = [os.path.join(CSRC, f) for f in ("ve_host.cpp", "ve_planner.cpp", "ve_muon_host.cpp", "ve_kernels.hip", "ve_group.hip",
                                            "ve_muon.hip", "ve_stream.hip",
-                                           "ve_muon_static.hip")]
+                                           "ve_muon_static.hip",
+                                           "ve_linear_host.cpp", "ve_linear.hip", "ve_act8.hip")]
 ARCH = "gfx950"
 
 HIPCC_FLAGS = [

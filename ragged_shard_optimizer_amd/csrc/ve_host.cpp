@@ -38,7 +38,7 @@ struct OptionDef {
 constexpr OptionDef kOptionDefs[kNumOptions] = {
     {"wg_threads", "VE_WG_THREADS", 0}, {"wg_gpt", "VE_WG_GPT", 0}, {"gemm_split", "VE_GEMM_SPLIT", 1},
     {"gemm_cfg", "VE_GEMM_CFG", -1},    {"gemm_xcd", "VE_GEMM_XCD", 1},     {"wg_dynamic", "VE_WG_DYNAMIC", 1},
-    {"wg_rows", "VE_WG_ROWS", 1},
+    {"wg_rows", "VE_WG_ROWS", 1},       {"linear_path", "VE_LINEAR_PATH", 0}, {"linear_split", "VE_LINEAR_SPLIT", 1},
 };
 std::atomic<int64_t> g_options[kNumOptions];
 std::once_flag g_options_once;

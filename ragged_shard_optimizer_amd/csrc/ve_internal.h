@@ -183,6 +183,8 @@ enum Option : int {
     kOptWgDynamic,      // "wg_dynamic" (VE_WG_DYNAMIC): 0 = one-shot launches only; 1 = persistent forms where a
                         // launch has enough work; 2 = persistent forms whatever the work
     kOptWgRows,         // "wg_rows" (VE_WG_ROWS): 0 = no multi-block items for blocks of 2,048 / 4,096 groups
+    kOptLinearPath,     // "linear_path" (VE_LINEAR_PATH): form of the linear layer's products, 0 = by shape
+    kOptLinearSplit,    // "linear_split" (VE_LINEAR_SPLIT): 0 = never split their contraction
     kNumOptions
 };
 int64_t option(Option o);

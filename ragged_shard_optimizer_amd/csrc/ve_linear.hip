@@ -1,0 +1,548 @@
+// ve_linear.hip -- the three products of a linear layer, dense or grouped by
+// expert, on the MFMA units:
+//
+//   forward   z[t,n]  = sum_k x[t,k] w[e,n,k]     (+ bias, act, residual, saving)
+//   dx        dx[t,k] = sum_n dz[t,n] w[e,n,k]    (+ addend)
+//   dw        dw[e,n,k] = sum_{t in e} dz[t,n] x[t,k]   (+ what dw holds)
+//
+// e is the group (expert) token t belongs to: rows [offsets[e],
+// offsets[e+1]).  The offsets stay on the device: a launch covers the most
+// tiles that any offsets could need, and each workgroup finds its group with
+// a wave-wide prefix sum over the groups' tile counts.
+//
+// Operands and LDS.  A contraction step is 64 deep.  An operand whose
+// contraction index is contiguous in memory ("KC": x and w of the forward
+// product, dz of dx) sits in LDS as rows of 64 elements; its fragments are
+// 16-byte reads.  An operand whose contraction index is the row ("KS": w of
+// dx, both operands of dw) sits in LDS as it lies in memory, 64 rows of the
+// tile's width, and its fragments come from the transposing read
+// ds_read_b64_tr_b16 (16 lanes read 4 rows x 16 columns; lane i gets column
+// i), so no operand is ever transposed in memory.  Both layouts permute the
+// 16- or 32-byte pieces of a row by XOR so that the lanes of one read hit
+// distinct banks.
+//
+// MFMA 32x32x16 bf16, operands swapped (output columns as the first operand):
+// accumulator register r of lane l holds row l % 32 and column
+// 8 (r / 4) + 4 (l / 32) + r % 4 of a 32 x 32 block, so four registers are
+// four consecutive columns and leave as one 16-byte LDS write.
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include <algorithm>
+
+#include "ve_linear_device.h"
+
+namespace ve {
+namespace {
+
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+#define VE_LDS __attribute__((address_space(3)))
+
+constexpr int kCUs = 256;
+constexpr int BK = 64;          // contraction step
+
+// Workgroup tile BM x BN of waves of WM x WN; two LDS stages.
+template <int BM_, int BN_, int WM_, int WN_>
+struct LinCfg {
+    static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_;
+    static constexpr int WAVES_M = BM / WM, WAVES_N = BN / WN, WAVES = WAVES_M * WAVES_N;
+    static constexpr int THREADS = 64 * WAVES;
+    static constexpr int TM = WM / 32, TN = WN / 32;
+    static constexpr int A_ELEMS = BM * BK, B_ELEMS = BN * BK, STAGE_ELEMS = A_ELEMS + B_ELEMS;
+    static constexpr int LDC = BN + 4;
+    static constexpr int OP_BYTES = 2 * STAGE_ELEMS * 2, C_BYTES = WM * LDC * 4;
+    static constexpr int SMEM = OP_BYTES > C_BYTES ? OP_BYTES : C_BYTES;
+    static_assert(SMEM <= 160 * 1024, "LDS");
+    static constexpr int PER_CU = 160 * 1024 / SMEM;
+};
+using Cfg256 = LinCfg<256, 256, 128, 64>;
+using Cfg128 = LinCfg<128, 128, 64, 64>;
+
+// s_waitcnt operand: at most n vector-memory operations outstanding
+// (lgkm: also every LDS operation complete).
+constexpr int wait_vm(int n, bool lgkm) { return (lgkm ? 0x0070 : 0x0F70) | (n & 15) | (((n >> 4) & 3) << 14); }
+
+// One operand of the workgroup's tile: ROWS tile rows (KC) or columns (KS)
+// over the contraction.  The tile of one step is ROWS * 128 bytes, filled in
+// pieces of 1 KiB by one wave instruction each (lane l: 16 bytes at 16 l).
+template <bool KS, int ROWS, int WAVES, bool DMA>
+struct Operand {
+    static constexpr int PIECES = ROWS * BK * 2 / 1024 / WAVES;  // per wave and step
+    static constexpr int SLOTS = KS ? ROWS / 8 : 8;              // 16-byte slots of an LDS row
+    static constexpr int LROWS = 64 / SLOTS;                     // LDS rows of one piece
+    static_assert(PIECES * WAVES * 1024 == ROWS * BK * 2, "pieces must divide evenly");
+    static_assert(WAVES % 2 == 0, "a lane's slot must not depend on the piece");
+    const uint16_t* base;  // KC: row 0, contraction index 0 of the tile; KS: contraction row 0, column 0
+    int64_t ld;
+    int valid;             // KC: rows; KS: columns (from the tile's first on)
+    int64_t kc;            // contraction length
+    bool vec;              // !DMA: rows allow 16-byte loads
+    int lrow, chunk, wave;
+    uint32_t voff;
+    u32x4 reg[DMA ? 1 : PIECES];
+
+    // swizzle of KC rows: consecutive rows of one bank line get distinct slots
+    __device__ static __forceinline__ int swz(int r) { return (r & 7) ^ ((r >> 3) & 1); }
+    // KS: 32-byte piece s of contraction row k lies at piece place(s) ^ (k & 3)
+    // of its LDS row.  A transposing read touches pieces s, s + 1 (s even) of
+    // rows k .. k + 3: eight distinct pieces modulo 256 bytes, and four
+    // distinct ones modulo 128 bytes for either s alone.
+    __device__ static __forceinline__ int place(int s) { return (s & ~7) | ((s & 1) << 2) | ((s >> 1) & 3); }
+    __device__ static __forceinline__ int unplace(int f) { return (f & ~7) | ((f & 3) << 1) | ((f >> 2) & 1); }
+
+    __device__ __forceinline__ void init(const uint16_t* base_, int64_t ld_, int valid_, int64_t kc_, bool vec_, int lane,
+                                         int wave_) {
+        base = base_; ld = ld_; valid = valid_; kc = kc_; vec = vec_; wave = wave_;
+        const int slot = lane % SLOTS, row0 = wave * LROWS + lane / SLOTS;  // row of piece 0
+        lrow = row0;
+        if constexpr (KS) {
+            const int f = (slot >> 1) ^ (row0 & 3);
+            chunk = unplace(f) * 2 + (slot & 1);
+        } else {
+            chunk = slot ^ swz(row0);
+        }
+        voff = (uint32_t)((lrow * ld + chunk * 8) * 2);
+    }
+    // Bring step kt's tile in: by direct loads into the LDS stage at `st`, or
+    // into registers (then put() writes them to LDS).
+    __device__ __forceinline__ void get(uint16_t* st, int64_t kt) {
+        const int64_t k0 = kt * BK;
+        if constexpr (DMA) {
+            // A buffer resource from this step's first element on: reads past
+            // the last valid row return 0, and so do those of a KC row past
+            // the contraction (sent past the end by hand).
+            const uint16_t* p = KS ? base + k0 * ld : base + k0;
+            const int64_t rows = KS ? (kc - k0 < BK ? kc - k0 : BK) : valid;
+            const uint32_t bytes = (uint32_t)(((rows - 1) * ld + (KS ? valid : kc - k0)) * 2);
+            const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc((void*)p, (short)0, (int)bytes, 0x00020000);
+            const bool in = KS || k0 + chunk * 8 < kc;
+#pragma unroll
+            for (int q = 0; q < PIECES; ++q) {
+                uint32_t v = voff + (uint32_t)(q * WAVES * LROWS * (int)ld * 2);
+                if (!KS) v = in ? v : 0x80000000u;
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (void VE_LDS*)(st + (WAVES * q + wave) * 512), 16, (int)v, 0,
+                                                         0, 0);
+            }
+        } else {
+#pragma unroll
+            for (int q = 0; q < PIECES; ++q) {
+                const int row = lrow + q * WAVES * LROWS;
+                const uint16_t* p;
+                int64_t cnt;
+                if constexpr (KS) {
+                    p = base + (k0 + row) * ld + chunk * 8;
+                    cnt = k0 + row < kc ? valid - chunk * 8 : 0;
+                } else {
+                    p = base + row * ld + k0 + chunk * 8;
+                    cnt = row < valid ? kc - (k0 + chunk * 8) : 0;
+                }
+                reg[q] = cnt > 0 ? load_bf16x8(p, (int)(cnt < 8 ? cnt : 8), vec) : u32x4{0, 0, 0, 0};
+            }
+        }
+    }
+    __device__ __forceinline__ void put(uint16_t* st, int lane) {
+        if constexpr (!DMA) {
+#pragma unroll
+            for (int q = 0; q < PIECES; ++q) *(u32x4*)(st + (WAVES * q + wave) * 512 + lane * 8) = reg[q];
+        }
+    }
+    // LDS byte offsets of a lane's fragment of the 32 rows (columns) from r0
+    // on, 16-deep sub-step 0; KC sub-steps differ in the slot, KS ones by
+    // 16 rows.
+    __device__ static __forceinline__ bf16x8 frag(const uint16_t* st, int r0, int kk, int lane) {
+        if constexpr (KS) {
+            const int g = lane >> 4, i = lane & 15;
+            const int k = kk * 16 + (g >> 1) * 8 + (i >> 2);
+            const int s = r0 / 16 + (g & 1);
+            const uint16_t* p = st + k * ROWS + (place(s) ^ (i >> 2)) * 16 + (i & 3) * 4;
+            const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((s16x4 VE_LDS*)p);
+            const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((s16x4 VE_LDS*)(p + 4 * ROWS));
+            return __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+        } else {
+            const int row = r0 + (lane & 31), slot = (2 * kk + (lane >> 5)) ^ swz(row & 15);
+            return __builtin_bit_cast(bf16x8, *(const u32x4*)(st + row * BK + slot * 8));
+        }
+    }
+};
+
+// Where a workgroup's tile lies.
+struct TileAt {
+    int e;
+    int64_t row0, rows;     // first output row (a token, or a dw row), rows of the tile that exist
+    int64_t col0;
+    int64_t begin, len;     // the group's tokens
+};
+
+// Tile t of the sequence (group by group; inside a group in bands of 8 tile
+// rows, column by column, so that consecutive tiles share panels).
+template <class CF, int KIND>
+__device__ __forceinline__ bool tile_of(const LinArgs& g, int64_t t, TileAt& at) {
+    int64_t in;  // index inside the group
+    int tm;
+    if constexpr (KIND == kLinDw) {
+        tm = (int)((g.M + CF::BM - 1) / CF::BM);
+        const int64_t per = (int64_t)tm * g.tiles_n;
+        at.e = (int)(t / per);
+        in = t - at.e * per;
+        at.begin = 0;
+        at.len = g.T;
+        if (g.offsets) {
+            group_rows(g.offsets, at.e, g.T, at.begin, at.len);
+            at.begin = uniform64(at.begin);
+            at.len = uniform64(at.len);
+        }
+    } else {
+        if (g.offsets) {
+            RaggedGroup r;
+            if (!ragged_find(g.offsets, g.E, g.T, CF::BM, t, g.tiles_n, r)) return false;
+            at.e = r.e;
+            at.begin = r.begin;
+            at.len = r.len;
+            tm = r.tiles;
+            in = t - (int64_t)r.before * g.tiles_n;
+        } else {
+            at.e = 0;
+            at.begin = 0;
+            at.len = g.T;
+            tm = (int)((g.T + CF::BM - 1) / CF::BM);
+            in = t;
+            if (t >= (int64_t)tm * g.tiles_n) return false;
+        }
+    }
+    constexpr int kBand = 8;
+    const int i = (int)in, per_band = kBand * g.tiles_n;
+    const int first = (i / per_band) * kBand, rows = min(tm - first, kBand), r = i % per_band;
+    const int ti = first + r % rows, tj = r / rows;
+    at.col0 = (int64_t)tj * CF::BN;
+    const int64_t i0 = (int64_t)ti * CF::BM, all = KIND == kLinDw ? g.M : at.len;
+    at.rows = all - i0 < CF::BM ? all - i0 : CF::BM;
+    at.row0 = KIND == kLinDw ? i0 : at.begin + i0;
+    return true;
+}
+
+// Epilogue of 8 consecutive columns of one output row: `row` the token (or
+// the row of dw[e]), col the first column, cnt of the 8 that exist (0: none;
+// such lanes still take part in the runs' maxima).
+template <int KIND>
+__device__ __forceinline__ void finish8(const LinArgs& g, int e, int64_t row, int64_t col, int cnt, float* v) {
+    if constexpr (KIND == kLinDw) {
+        if (cnt <= 0) return;
+        const int64_t at = (int64_t)e * g.dw_group + row * g.lddw + col;
+        if (g.wide) {
+            VE_GLOBAL float* p = (VE_GLOBAL float*)((float*)g.dw + at);
+            if (cnt == 8 && g.vec_dw) {
+                f32x4 a = {v[0], v[1], v[2], v[3]}, b = {v[4], v[5], v[6], v[7]};
+                if (g.accumulate) {
+                    a += *(VE_GLOBAL f32x4*)p;
+                    b += *(VE_GLOBAL f32x4*)(p + 4);
+                }
+                *(VE_GLOBAL f32x4*)p = a;
+                *(VE_GLOBAL f32x4*)(p + 4) = b;
+            } else {
+#pragma unroll
+                for (int t = 0; t < 8; ++t)
+                    if (t < cnt) p[t] = g.accumulate ? p[t] + v[t] : v[t];
+            }
+        } else {
+            uint16_t* p = (uint16_t*)g.dw + at;
+            if (g.accumulate) {
+                float o[8];
+                widen8(load_bf16x8(p, cnt, g.vec_dw), o);
+#pragma unroll
+                for (int t = 0; t < 8; ++t) v[t] += o[t];
+            }
+            store_bf16x8(p, narrow8(v), cnt, g.vec_dw);
+        }
+    } else {
+        if (g.bias && cnt > 0) {
+            float o[8];
+            widen8(load_bf16x8(g.bias + (int64_t)e * g.bias_group + col, cnt, g.vec_bias), o);
+#pragma unroll
+            for (int t = 0; t < 8; ++t) v[t] += o[t];
+        }
+        if constexpr (KIND == kLinFwd) {
+            if (g.z && cnt > 0) store_bf16x8(g.z + row * g.ldz + col, narrow8(v), cnt, g.vec_z);
+            if (g.z8.codes) {
+                uint32_t m = 0;
+#pragma unroll
+                for (int t = 0; t < 8; ++t) m = t < cnt ? amax_of(m, v[t]) : m;
+                m = amax_lanes(m, g.z8.block / 8);
+                const RunCode c = run_code(__uint_as_float(m));
+                if (cnt > 0) {
+                    store_codes8(g.z8.codes + row * g.z8.ld_codes + col, encode8(c, v), cnt, g.vec_z8);
+                    const uint32_t run = (uint32_t)col >> __builtin_ctz(g.z8.block);
+                    if (((uint32_t)col & (g.z8.block - 1)) == 0) g.z8.scales[row * g.z8.ld_scales + run] = c.scale;
+                }
+            }
+            if (g.act != VE_ACT_NONE) {
+#pragma unroll
+                for (int t = 0; t < 8; ++t) v[t] = activate(g.act, v[t]);
+            }
+        }
+        if (cnt <= 0) return;
+        if (g.res) {
+            float o[8];
+            widen8(load_bf16x8(g.res + row * g.ldr + col, cnt, g.vec_res), o);
+#pragma unroll
+            for (int t = 0; t < 8; ++t) v[t] += o[t];
+        }
+        store_bf16x8(g.y + row * g.ldy + col, narrow8(v), cnt, g.vec_y);
+    }
+}
+
+// One tile (and slice of the contraction).  DMA: operands go straight from
+// memory to LDS (16-byte rows, no ragged ends inside 16 bytes); else through
+// registers, from any alignment.
+template <class CF, int KIND, bool DMA>
+__global__ void __launch_bounds__(CF::THREADS) k_product(LinArgs g) {
+    constexpr int TM = CF::TM, TN = CF::TN, WM = CF::WM, WN = CF::WN;
+    constexpr bool AKS = KIND == kLinDw, BKS = KIND != kLinFwd;
+    __shared__ __attribute__((aligned(1024))) unsigned char smem[CF::SMEM];
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wr = wave / CF::WAVES_N, wc = wave % CF::WAVES_N;
+
+    // tile and slice: workgroups go round-robin over the 8 XCDs, each with
+    // its own L2, so each XCD takes a contiguous run of the tile sequence
+    int64_t t = blockIdx.x;
+    int slice = 0;
+    if (g.ksplit > 1) {
+        slice = (int)(t % g.ksplit);
+        t /= g.ksplit;
+    } else {
+        int64_t total = g.tiles;
+        if (KIND != kLinDw && g.offsets)
+            total = min(total, (int64_t)ragged_total(g.offsets, g.E, g.T, CF::BM) * g.tiles_n);
+        const int64_t per = (total + 7) / 8;
+        if (t / 8 >= per) return;
+        t = (t % 8) * per + t / 8;
+        if (t >= total) return;
+    }
+    TileAt at;
+    if (!tile_of<CF, KIND>(g, t, at)) return;
+
+    uint16_t* ops = (uint16_t*)smem;
+    Operand<AKS, CF::BM, CF::WAVES, DMA> A;
+    Operand<BKS, CF::BN, CF::WAVES, DMA> B;
+    const int64_t K = KIND == kLinDw ? at.len : g.K;
+    const int cols = (int)(g.N - at.col0 < CF::BN ? g.N - at.col0 : CF::BN);
+    if constexpr (AKS) A.init(g.A + at.begin * g.lda + at.row0, g.lda, (int)at.rows, K, g.lda % 8 == 0 && ((uintptr_t)g.A & 15) == 0, lane, wave);
+    else A.init(g.A + at.row0 * g.lda, g.lda, (int)at.rows, K, g.lda % 8 == 0 && ((uintptr_t)g.A & 15) == 0, lane, wave);
+    const bool vb = g.ldb % 8 == 0 && ((uintptr_t)g.B & 15) == 0 && g.b_group % 8 == 0;
+    if constexpr (KIND == kLinFwd) B.init(g.B + at.e * g.b_group + at.col0 * g.ldb, g.ldb, cols, K, vb, lane, wave);
+    else if constexpr (KIND == kLinDx) B.init(g.B + at.e * g.b_group + at.col0, g.ldb, cols, K, vb, lane, wave);
+    else B.init(g.B + at.begin * g.ldb + at.col0, g.ldb, cols, K, vb, lane, wave);
+
+    f32x16 acc[TM][TN];
+#pragma unroll
+    for (int a = 0; a < TM; ++a)
+#pragma unroll
+        for (int b = 0; b < TN; ++b)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) acc[a][b][r] = 0.f;
+
+    int64_t kbeg = 0, nk = (K + BK - 1) / BK;
+    if (g.ksplit > 1) {
+        const int64_t per = (nk + g.ksplit - 1) / g.ksplit;
+        kbeg = min(slice * per, nk);
+        nk = min(per, nk - kbeg);
+    }
+    auto stage = [&](int64_t kt) { return ops + (int)(kt & 1) * CF::STAGE_ELEMS; };
+    auto get = [&](int64_t kt) {
+        A.get(stage(kt), kbeg + kt);
+        B.get(stage(kt) + CF::A_ELEMS, kbeg + kt);
+    };
+    auto put = [&](int64_t kt) {
+        A.put(stage(kt), lane);
+        B.put(stage(kt) + CF::A_ELEMS, lane);
+    };
+    // this wave's loads (and LDS writes) of the next stage are complete, then
+    // everyone's: a bare barrier, with the LDS accesses pinned around it
+    auto ready = [&]() {
+        __builtin_amdgcn_s_waitcnt(wait_vm(0, !DMA));
+        asm volatile("" ::: "memory");
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+    };
+    bf16x8 fa[2][TM], fb[2][TN];
+    auto frag = [&](int buf, int kk, int64_t kt) {
+        const uint16_t* st = stage(kt);
+#pragma unroll
+        for (int a = 0; a < TM; ++a) fa[buf][a] = A.frag(st, wr * WM + a * 32, kk, lane);
+#pragma unroll
+        for (int b = 0; b < TN; ++b) fb[buf][b] = B.frag(st + CF::A_ELEMS, wc * WN + b * 32, kk, lane);
+    };
+    auto mfma = [&](int buf, int a, int b) {
+        acc[a][b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fb[buf][b], fa[buf][a], acc[a][b], 0, 0, 0);
+    };
+    if (nk > 0) {
+        get(0);
+        put(0);
+        ready();
+        frag(0, 0, 0);
+        for (int64_t kt = 0; kt < nk; ++kt) {
+            // every wave's reads of the other stage were complete before the
+            // barrier inside step kt - 1
+            if (kt + 1 < nk) get(kt + 1);
+#pragma unroll
+            for (int kk = 0; kk < BK / 16; ++kk) {
+                if (kk + 1 < BK / 16) {
+                    frag((kk + 1) & 1, kk + 1, kt);
+#pragma unroll
+                    for (int a = 0; a < TM; ++a)
+#pragma unroll
+                        for (int b = 0; b < TN; ++b) mfma(kk & 1, a, b);
+                    if (!DMA && kk == 1 && kt + 1 < nk) put(kt + 1);
+                } else {
+                    // last sub-step: all reads of this stage are complete.
+                    // Half of its MFMAs, the barrier, the next step's first
+                    // reads (on the last step they fetch an unused stage),
+                    // the other half.
+#pragma unroll
+                    for (int i = 0; i < TM * TN / 2; ++i) mfma(kk & 1, i / TN, i % TN);
+                    ready();
+                    frag(0, 0, kt + 1);
+#pragma unroll
+                    for (int i = TM * TN / 2; i < TM * TN; ++i) mfma(kk & 1, i / TN, i % TN);
+                }
+            }
+        }
+    }
+    __syncthreads();
+
+    // epilogue, one row of waves at a time through fp32 rows in LDS
+    float* sC = (float*)smem;
+    constexpr int LDC = CF::LDC, CPR = CF::BN / 8;
+#pragma unroll 1
+    for (int pass = 0; pass < CF::WAVES_M; ++pass) {
+        if (wr == pass) {
+#pragma unroll
+            for (int a = 0; a < TM; ++a)
+#pragma unroll
+                for (int b = 0; b < TN; ++b)
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const f32x4 v = {acc[a][b][4 * q], acc[a][b][4 * q + 1], acc[a][b][4 * q + 2], acc[a][b][4 * q + 3]};
+                        *(f32x4*)&sC[(a * 32 + (lane & 31)) * LDC + wc * WN + b * 32 + 8 * q + 4 * (lane >> 5)] = v;
+                    }
+        }
+        __syncthreads();
+        const int rows = (int)at.rows - pass * WM;  // rows of this pass that exist
+#pragma unroll 1
+        for (int q = 0; q < WM * CPR / CF::THREADS; ++q) {
+            const int id = tid + CF::THREADS * q, row = id / CPR, c8 = (id % CPR) * 8;
+            float v[8];
+            *(f32x4*)&v[0] = *(const f32x4*)&sC[row * LDC + c8];
+            *(f32x4*)&v[4] = *(const f32x4*)&sC[row * LDC + c8 + 4];
+            if (g.ksplit > 1) {
+                float* out = g.partial + ((int64_t)slice * g.tiles + t) * (CF::BM * CF::BN) +
+                             (pass * WM + row) * CF::BN + c8;
+                *(f32x4*)out = *(const f32x4*)&v[0];
+                *(f32x4*)(out + 4) = *(const f32x4*)&v[4];
+            } else {
+                finish8<KIND>(g, at.e, at.row0 + pass * WM + row, at.col0 + c8, row < rows ? min(cols - c8, 8) : 0, v);
+            }
+        }
+        __syncthreads();
+    }
+}
+
+// Slices of split tiles summed in slice order, then the epilogue: one thread
+// for 8 columns of a tile row.
+template <class CF, int KIND>
+__global__ void __launch_bounds__(256) k_join(LinArgs g) {
+    constexpr int CPR = CF::BN / 8, PER = CF::BM * CPR / 256;  // workgroups of one tile
+    const int64_t t = blockIdx.x / PER;
+    TileAt at;
+    if (!tile_of<CF, KIND>(g, t, at)) return;
+    const int id = (int)(blockIdx.x % PER) * 256 + (int)threadIdx.x, row = id / CPR, c8 = (id % CPR) * 8;
+    const float* p = g.partial + t * (CF::BM * CF::BN) + row * CF::BN + c8;
+    float v[8];
+    *(f32x4*)&v[0] = *(const f32x4*)p;
+    *(f32x4*)&v[4] = *(const f32x4*)(p + 4);
+    for (int s = 1; s < g.ksplit; ++s) {
+        p += g.tiles * (CF::BM * CF::BN);
+        const f32x4 a = *(const f32x4*)p, b = *(const f32x4*)(p + 4);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            v[i] += a[i];
+            v[4 + i] += b[i];
+        }
+    }
+    const int cols = (int)(g.N - at.col0 < CF::BN ? g.N - at.col0 : CF::BN);
+    finish8<KIND>(g, at.e, at.row0 + row, at.col0 + c8, row < at.rows ? min(cols - c8, 8) : 0, v);
+}
+
+template <class CF>
+int64_t tiles_of(const LinArgs& g, LinKind kind) {
+    const int64_t tn = (g.N + CF::BN - 1) / CF::BN;
+    if (kind == kLinDw) return (int64_t)g.E * ((g.M + CF::BM - 1) / CF::BM) * tn;
+    return ((g.T + CF::BM - 1) / CF::BM + (g.offsets ? g.E : 0)) * tn;
+}
+
+template <class CF, int KIND, bool DMA>
+hipError_t launch_kind(LinArgs g, int ksplit, hipStream_t s) {
+    g.tiles_n = (int)((g.N + CF::BN - 1) / CF::BN);
+    g.ksplit = ksplit;
+    g.tiles = tiles_of<CF>(g, (LinKind)KIND);
+    if (g.tiles == 0) return hipSuccess;
+    // whole tiles: 8 runs of equal length, one for each XCD
+    const int64_t grid = ksplit > 1 ? g.tiles * ksplit : (g.tiles + 7) / 8 * 8;
+    hipLaunchKernelGGL((k_product<CF, KIND, DMA>), dim3((unsigned)grid), dim3(CF::THREADS), 0, s, g);
+    if (ksplit > 1)
+        hipLaunchKernelGGL((k_join<CF, KIND>), dim3((unsigned)(g.tiles * (CF::BM * (CF::BN / 8) / 256))), dim3(256), 0, s, g);
+    return hipGetLastError();
+}
+
+bool aligned16(const void* p) { return ((uintptr_t)p & 15) == 0; }
+
+// Direct loads: 16-byte operand rows, the contiguous dimensions whole 16-byte
+// groups, and a tile's rows within 32-bit byte offsets.
+bool dma_ok(const LinArgs& g, LinKind kind) {
+    const int64_t kMaxLd = int64_t(1) << 21;
+    if (!aligned16(g.A) || !aligned16(g.B) || g.lda % 8 || g.ldb % 8 || g.lda > kMaxLd || g.ldb > kMaxLd) return false;
+    if (kind != kLinDw && g.b_group % 8) return false;
+    if (kind == kLinDw) return g.M % 8 == 0 && g.N % 8 == 0;
+    return g.K % 8 == 0 && (kind == kLinFwd || g.N % 8 == 0);
+}
+
+template <int KIND>
+hipError_t launch_path(const LinArgs& g, const LinPlan& p, hipStream_t s) {
+    switch (p.path) {
+    case kPath256: return launch_kind<Cfg256, KIND, true>(g, p.ksplit, s);
+    case kPath128: return launch_kind<Cfg128, KIND, true>(g, p.ksplit, s);
+    default: return launch_kind<Cfg128, KIND, false>(g, p.ksplit, s);
+    }
+}
+
+}  // namespace
+
+LinPlan plan_product(const LinArgs& g, LinKind kind) {
+    LinPlan p{kPathGeneral, 1, 0};
+    const int64_t pin = option(kOptLinearPath);
+    const int64_t t256 = tiles_of<Cfg256>(g, kind), t128 = tiles_of<Cfg128>(g, kind);
+    const int64_t K = kind == kLinDw ? g.T / std::max(1, g.E) : g.K, nk = (K + BK - 1) / BK;
+    auto split = [&](int64_t tiles, int64_t slots) -> int {
+        if (g.offsets || option(kOptLinearSplit) == 0 || tiles * 2 > slots || nk < 16) return 1;
+        return (int)std::min<int64_t>(std::min(slots / std::max<int64_t>(tiles, 1), nk / 8), 32);
+    };
+    if (dma_ok(g, kind) && pin != kPathGeneral) p.path = t256 >= 2 * kCUs ? kPath256 : kPath128;
+    if (p.path != kPathGeneral && (pin == kPath128 || pin == kPath256)) p.path = (int)pin;
+    const int64_t tiles = p.path == kPath256 ? t256 : t128;
+    const int64_t area = p.path == kPath256 ? 256 * 256 : 128 * 128;
+    p.ksplit = std::max(1, split(tiles, kCUs * (p.path == kPath256 ? Cfg256::PER_CU : Cfg128::PER_CU)));
+    p.partial_bytes = p.ksplit > 1 ? p.ksplit * tiles * area * 4 : 0;
+    return p;
+}
+
+hipError_t launch_product(LinArgs g, LinKind kind, const LinPlan& p, hipStream_t s) {
+    switch (kind) {
+    case kLinFwd: return launch_path<kLinFwd>(g, p, s);
+    case kLinDx: return launch_path<kLinDx>(g, p, s);
+    default: return launch_path<kLinDw>(g, p, s);
+    }
+}
+
+}  // namespace ve

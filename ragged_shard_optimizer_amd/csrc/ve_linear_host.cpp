@@ -1,0 +1,285 @@
+// ve_linear_host.cpp -- C entry points of the linear layer and of 8-bit saved
+// activations: argument checks, workspace sizing and the launch sequences
+// (kernels in ve_linear.hip and ve_act8.hip).
+//
+// Backward sequence:
+//   1. dz = bf16(dy act'(z)) into the workspace, with the column sums by
+//      token tile (no activation: the sums only, and dz is dy);
+//   2. dbias from the sums;
+//   3. dx = dz w;
+//   4. x restored into the workspace if it comes in 8 bits, then dw = dz^T x.
+
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <cstdint>
+
+#include "ve.h"
+#include "ve_linear.h"
+
+using namespace ve;
+
+namespace {
+
+constexpr int64_t kMaxDim = (int64_t(1) << 31) - 1;
+constexpr int64_t kMaxWorkgroups = kMaxGridItems / 512;  // of at most 512 threads
+
+int64_t round256(int64_t x) { return (x + 255) / 256 * 256; }
+bool aligned(const void* p, uintptr_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
+bool vec16(const void* p, int64_t ld) { return aligned(p, 16) && ld % 8 == 0; }
+
+ve_status status_of(hipError_t e, const char* what) {
+    if (e == hipSuccess) return VE_OK;
+    return fail(VE_ERR_DEVICE, "%s: %s", what, hipGetErrorString(e));
+}
+
+ve_status check_act8(const ve_act8& q, int64_t cols, const char* name) {
+    if (!q.codes || !q.scales) return fail(VE_ERR_INVALID_ARG, "%s: codes or scales is NULL", name);
+    if (q.block != 32 && q.block != 64 && q.block != 128)
+        return fail(VE_ERR_INVALID_ARG, "%s: block %d is not 32, 64 or 128", name, q.block);
+    if (q.ld_codes < cols || q.ld_scales < (cols + q.block - 1) / q.block)
+        return fail(VE_ERR_INVALID_ARG, "%s: leading dimension smaller than the row", name);
+    return VE_OK;
+}
+
+ve_status check_shape(int64_t tokens, int64_t in, int64_t out, int32_t groups, const int64_t* offsets, int32_t act) {
+    if (tokens < 0 || in < 1 || out < 1)
+        return fail(VE_ERR_INVALID_ARG, "shape: %lld tokens, %lld -> %lld features", (long long)tokens, (long long)in,
+                    (long long)out);
+    if (groups < 1 || groups > 65536) return fail(VE_ERR_INVALID_ARG, "groups %d outside [1, 65536]", groups);
+    if (!offsets && groups != 1) return fail(VE_ERR_INVALID_ARG, "%d groups need offsets", groups);
+    if (act < VE_ACT_NONE || act > VE_ACT_SILU) return fail(VE_ERR_INVALID_ARG, "unknown activation %d", act);
+    if (tokens > kMaxDim || in > kMaxDim || out > kMaxDim)
+        return fail(VE_ERR_UNSUPPORTED, "a dimension of 2^31 or more");
+    return VE_OK;
+}
+
+// The workgroups of every launch over a rows x cols matrix fit one grid.
+// Tiles are at least 64 x 64 or 128 x 128; `extra` row tiles more come from
+// ragged groups, and `times` matrices from grouped weights.
+bool launchable(int64_t rows, int64_t cols, int64_t extra, int64_t times) {
+    const int64_t tm = (rows + 63) / 64 + extra, tn = (cols + 63) / 64;
+    return tm <= kMaxWorkgroups / tn / times;
+}
+
+ve_status check_forward(const ve_linear_forward_args& a) {
+    ve_status st = check_shape(a.tokens, a.in_features, a.out_features, a.groups, a.offsets, a.activation);
+    if (st != VE_OK) return st;
+    if (!a.w) return fail(VE_ERR_INVALID_ARG, "w is NULL");
+    if (a.tokens > 0 && (!a.x || !a.y)) return fail(VE_ERR_INVALID_ARG, "x or y is NULL");
+    const int64_t K = a.in_features, N = a.out_features;
+    if (a.ldx < K || a.ldw < K || a.ldy < N || (a.residual && a.ldr < N) || (a.z && a.ldz < N))
+        return fail(VE_ERR_INVALID_ARG, "leading dimension smaller than the row");
+    if (a.groups > 1 && (a.w_group < (N - 1) * a.ldw + K || (a.bias && a.bias_group < N)))
+        return fail(VE_ERR_INVALID_ARG, "group stride smaller than a group");
+    if (a.z8.codes && (st = check_act8(a.z8, N, "z8")) != VE_OK) return st;
+    if (!launchable(a.tokens, N, a.groups, 1)) return fail(VE_ERR_UNSUPPORTED, "product too large for one launch");
+    return VE_OK;
+}
+
+LinArgs forward_product(const ve_linear_forward_args& a) {
+    LinArgs g{};
+    g.A = a.x; g.lda = a.ldx;
+    g.B = a.w; g.ldb = a.ldw; g.b_group = a.groups > 1 ? a.w_group : 0;
+    g.T = a.tokens; g.N = a.out_features; g.K = a.in_features;
+    g.E = a.groups; g.offsets = a.offsets;
+    g.bias = a.bias; g.bias_group = a.groups > 1 ? a.bias_group : 0;
+    g.res = a.residual; g.ldr = a.ldr;
+    g.y = a.y; g.ldy = a.ldy;
+    g.z = a.z; g.ldz = a.ldz;
+    g.z8 = a.z8; g.act = a.activation;
+    g.vec_bias = vec16(a.bias, g.bias_group);
+    g.vec_res = vec16(a.residual, a.ldr);
+    g.vec_y = vec16(a.y, a.ldy);
+    g.vec_z = vec16(a.z, a.ldz);
+    g.vec_z8 = aligned(a.z8.codes, 8) && a.z8.ld_codes % 8 == 0;
+    return g;
+}
+
+ve_status check_backward(const ve_linear_backward_args& a) {
+    ve_status st = check_shape(a.tokens, a.in_features, a.out_features, a.groups, a.offsets, a.activation);
+    if (st != VE_OK) return st;
+    const int64_t K = a.in_features, N = a.out_features;
+    const bool some = a.tokens > 0, need_z = a.activation != VE_ACT_NONE && (a.dx || a.dw || a.dbias);
+    if (some && !a.dy) return fail(VE_ERR_INVALID_ARG, "dy is NULL");
+    if (a.lddy < N) return fail(VE_ERR_INVALID_ARG, "leading dimension smaller than the row");
+    if (a.dx && (a.lddx < K || (a.dx_add && a.ld_add < K)))
+        return fail(VE_ERR_INVALID_ARG, "leading dimension smaller than the row");
+    if (a.dx && !a.w) return fail(VE_ERR_INVALID_ARG, "dx needs w");
+    if (a.dx && a.ldw < K) return fail(VE_ERR_INVALID_ARG, "leading dimension smaller than the row");
+    if (a.dx && a.groups > 1 && a.w_group < (N - 1) * a.ldw + K)
+        return fail(VE_ERR_INVALID_ARG, "group stride smaller than a group");
+    if (a.dw) {
+        if (some && (a.x != nullptr) == (a.x8.codes != nullptr))
+            return fail(VE_ERR_INVALID_ARG, "dw needs exactly one of x and x8");
+        if (a.lddw < K || (a.x && a.ldx < K)) return fail(VE_ERR_INVALID_ARG, "leading dimension smaller than the row");
+        if (a.x8.codes && (st = check_act8(a.x8, K, "x8")) != VE_OK) return st;
+        if (a.groups > 1 && a.dw_group < (N - 1) * a.lddw + K)
+            return fail(VE_ERR_INVALID_ARG, "group stride smaller than a group");
+    }
+    if (a.dbias && a.groups > 1 && a.dbias_group < N)
+        return fail(VE_ERR_INVALID_ARG, "group stride smaller than a group");
+    if (need_z) {
+        if (some && (a.z != nullptr) == (a.z8.codes != nullptr))
+            return fail(VE_ERR_INVALID_ARG, "the activation needs exactly one of z and z8");
+        if (a.z && a.ldz < N) return fail(VE_ERR_INVALID_ARG, "leading dimension smaller than the row");
+        if (a.z8.codes && (st = check_act8(a.z8, N, "z8")) != VE_OK) return st;
+    }
+    if (!launchable(a.tokens, K, a.groups, 1) || !launchable(a.tokens, N, a.groups, 1) || !launchable(N, K, 0, a.groups))
+        return fail(VE_ERR_UNSUPPORTED, "product too large for one launch");
+    return VE_OK;
+}
+
+// What a backward call launches, and where its scratch lies.
+struct Backward {
+    DzArgs dz;
+    LinArgs dx, dw;
+    LinPlan pdx, pdw;
+    int64_t dz_at, sums_at, x_at, partial_at, total;
+};
+
+void plan_backward(const ve_linear_backward_args& a, char* ws, Backward& b) {
+    const int64_t T = a.tokens, K = a.in_features, N = a.out_features;
+    const bool act = a.activation != VE_ACT_NONE;
+    // rows of the scratch matrices start on 16 bytes
+    const int64_t ldz = (N + 7) / 8 * 8, ldx = (K + 7) / 8 * 8;
+    int64_t at = 0;
+    auto carve = [&](bool need, int64_t bytes) {
+        const int64_t here = at;
+        if (need) at += round256(bytes);
+        return here;
+    };
+    b.dz_at = carve(act, T * ldz * 2);
+    b.sums_at = carve(a.dbias != nullptr, dz_tiles(T, a.groups, a.offsets != nullptr) * N * 4);
+    const bool restore = a.dw && a.x8.codes;
+    b.x_at = carve(restore, T * ldx * 2);
+    auto in_ws = [&](int64_t off) { return ws ? (uint16_t*)(ws + off) : (uint16_t*)(uintptr_t)256; };
+
+    b.dz = DzArgs{};
+    b.dz.dy = a.dy; b.dz.lddy = a.lddy;
+    b.dz.z = a.z; b.dz.ldz = a.ldz; b.dz.z8 = a.z8;
+    b.dz.dz = act ? in_ws(b.dz_at) : nullptr; b.dz.lddz = ldz;
+    b.dz.sums = a.dbias ? (float*)in_ws(b.sums_at) : nullptr;
+    b.dz.T = T; b.dz.N = N; b.dz.E = a.groups; b.dz.act = a.activation; b.dz.offsets = a.offsets;
+    b.dz.vec = N % 8 == 0 && vec16(a.dy, a.lddy);
+    if (act) b.dz.vec = b.dz.vec && (a.z8.codes ? aligned(a.z8.codes, 8) && a.z8.ld_codes % 8 == 0 : vec16(a.z, a.ldz));
+
+    const uint16_t* dz = act ? b.dz.dz : a.dy;
+    const int64_t lddz = act ? ldz : a.lddy;
+    LinArgs g{};
+    g.A = dz; g.lda = lddz;
+    g.B = a.w; g.ldb = a.ldw; g.b_group = a.groups > 1 ? a.w_group : 0;
+    g.T = T; g.N = K; g.K = N; g.E = a.groups; g.offsets = a.offsets;
+    g.res = a.dx_add; g.ldr = a.ld_add;
+    g.y = a.dx; g.ldy = a.lddx;
+    g.vec_res = vec16(a.dx_add, a.ld_add);
+    g.vec_y = vec16(a.dx, a.lddx);
+    b.dx = g;
+    g = LinArgs{};
+    g.A = dz; g.lda = lddz;
+    g.B = restore ? in_ws(b.x_at) : a.x; g.ldb = restore ? ldx : a.ldx;
+    g.T = T; g.M = N; g.N = K; g.E = a.groups; g.offsets = a.offsets;
+    g.dw = a.dw; g.lddw = a.lddw; g.dw_group = a.groups > 1 ? a.dw_group : 0;
+    g.wide = a.grad_fp32 != 0; g.accumulate = a.accumulate != 0;
+    g.vec_dw = aligned(a.dw, 16) && a.lddw % 8 == 0 && g.dw_group % 8 == 0;
+    b.dw = g;
+    b.pdx = a.dx && T > 0 ? plan_product(b.dx, kLinDx) : LinPlan{kPathGeneral, 1, 0};
+    b.pdw = a.dw ? plan_product(b.dw, kLinDw) : LinPlan{kPathGeneral, 1, 0};
+    const int64_t partial = std::max(b.pdx.partial_bytes, b.pdw.partial_bytes);
+    b.partial_at = carve(partial > 0, partial);
+    b.dx.partial = b.dw.partial = (float*)in_ws(b.partial_at);
+    b.total = at;
+}
+
+ve_status check_workspace(void* ws, int64_t have, int64_t need) {
+    if (need == 0) return VE_OK;
+    if (!ws || have < need) return fail(VE_ERR_INVALID_ARG, "workspace of %lld bytes needed", (long long)need);
+    if (!aligned(ws, 256)) return fail(VE_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
+    return VE_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+ve_status ve_act8_pack(const uint16_t* x, int64_t ldx, int64_t rows, int64_t cols, const ve_act8* out, void* stream) {
+    if (!out) return fail(VE_ERR_INVALID_ARG, "out is NULL");
+    if (rows < 0 || cols < 1) return fail(VE_ERR_INVALID_ARG, "shape %lld x %lld", (long long)rows, (long long)cols);
+    if (ldx < cols) return fail(VE_ERR_INVALID_ARG, "leading dimension smaller than the row");
+    if (rows == 0) return VE_OK;
+    if (!x) return fail(VE_ERR_INVALID_ARG, "x is NULL");
+    if (const ve_status st = check_act8(*out, cols, "out"); st != VE_OK) return st;
+    if (cols > kMaxDim || rows > kMaxWorkgroups * 8192 / (cols + 128))
+        return fail(VE_ERR_UNSUPPORTED, "matrix too large for one launch");
+    (void)hipGetLastError();
+    return status_of(launch_act8_pack(x, ldx, rows, cols, *out, (hipStream_t)stream), "pack");
+}
+
+ve_status ve_act8_unpack(const ve_act8* in, int64_t rows, int64_t cols, uint16_t* x, int64_t ldx, void* stream) {
+    if (!in) return fail(VE_ERR_INVALID_ARG, "in is NULL");
+    if (rows < 0 || cols < 1) return fail(VE_ERR_INVALID_ARG, "shape %lld x %lld", (long long)rows, (long long)cols);
+    if (ldx < cols) return fail(VE_ERR_INVALID_ARG, "leading dimension smaller than the row");
+    if (rows == 0) return VE_OK;
+    if (!x) return fail(VE_ERR_INVALID_ARG, "x is NULL");
+    if (const ve_status st = check_act8(*in, cols, "in"); st != VE_OK) return st;
+    if (cols > kMaxDim || rows > kMaxWorkgroups * 8192 / (cols + 128))
+        return fail(VE_ERR_UNSUPPORTED, "matrix too large for one launch");
+    (void)hipGetLastError();
+    return status_of(launch_act8_unpack(*in, rows, cols, x, ldx, (hipStream_t)stream), "unpack");
+}
+
+ve_status ve_linear_forward_workspace(const ve_linear_forward_args* a, int64_t* bytes) {
+    if (!a || !bytes) return fail(VE_ERR_INVALID_ARG, "arguments or bytes is NULL");
+    if (const ve_status st = check_forward(*a); st != VE_OK) return st;
+    *bytes = a->tokens > 0 ? plan_product(forward_product(*a), kLinFwd).partial_bytes : 0;
+    return VE_OK;
+}
+
+ve_status ve_linear_forward(const ve_linear_forward_args* a, void* workspace, int64_t workspace_bytes, void* stream) {
+    if (!a) return fail(VE_ERR_INVALID_ARG, "arguments are NULL");
+    if (const ve_status st = check_forward(*a); st != VE_OK) return st;
+    if (a->tokens == 0) return VE_OK;
+    LinArgs g = forward_product(*a);
+    const LinPlan p = plan_product(g, kLinFwd);
+    if (const ve_status st = check_workspace(workspace, workspace_bytes, p.partial_bytes); st != VE_OK) return st;
+    g.partial = (float*)workspace;
+    (void)hipGetLastError();
+    return status_of(launch_product(g, kLinFwd, p, (hipStream_t)stream), "forward product");
+}
+
+ve_status ve_linear_backward_workspace(const ve_linear_backward_args* a, int64_t* bytes) {
+    if (!a || !bytes) return fail(VE_ERR_INVALID_ARG, "arguments or bytes is NULL");
+    if (const ve_status st = check_backward(*a); st != VE_OK) return st;
+    Backward b;
+    plan_backward(*a, nullptr, b);
+    *bytes = b.total;
+    return VE_OK;
+}
+
+ve_status ve_linear_backward(const ve_linear_backward_args* a, void* workspace, int64_t workspace_bytes, void* stream) {
+    if (!a) return fail(VE_ERR_INVALID_ARG, "arguments are NULL");
+    ve_status st = check_backward(*a);
+    if (st != VE_OK) return st;
+    Backward b;
+    plan_backward(*a, (char*)workspace, b);
+    if ((st = check_workspace(workspace, workspace_bytes, b.total)) != VE_OK) return st;
+    hipStream_t s = (hipStream_t)stream;
+    (void)hipGetLastError();
+    if (a->tokens > 0 && (a->dbias || (b.dz.dz && (a->dx || a->dw))) &&
+        (st = status_of(launch_dz(b.dz, s), "dz")) != VE_OK)
+        return st;
+    if (a->dbias && (st = status_of(launch_dbias(b.dz, a->dbias, a->groups > 1 ? a->dbias_group : 0, a->grad_fp32 != 0,
+                                                 a->accumulate != 0, s),
+                                    "dbias")) != VE_OK)
+        return st;
+    if (a->dx && a->tokens > 0 && (st = status_of(launch_product(b.dx, kLinDx, b.pdx, s), "dx product")) != VE_OK)
+        return st;
+    if (!a->dw) return VE_OK;
+    if (a->tokens > 0 && a->x8.codes &&
+        (st = status_of(launch_act8_unpack(a->x8, a->tokens, a->in_features, (uint16_t*)b.dw.B, b.dw.ldb, s),
+                        "restore")) != VE_OK)
+        return st;
+    return status_of(launch_product(b.dw, kLinDw, b.pdw, s), "dw product");
+}
+
+}  // extern "C"

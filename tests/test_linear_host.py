@@ -1,0 +1,139 @@
+"""Refusals of the linear layer's and the 8-bit code's entry points, on the
+C ABI without a GPU: every call here is rejected before anything reaches a
+device, or has nothing to launch."""
+
+from __future__ import annotations
+
+import ctypes as C
+
+import pytest
+
+import ragged_shard_optimizer_amd as ve
+
+P = 4096  # never dereferenced
+BAD, OK, UNSUP = ve.VE_ERR_INVALID_ARG, ve.VE_OK, ve.VE_ERR_UNSUPPORTED
+
+
+def _fwd(**kw):
+    a = ve._LinearForward(tokens=8, in_features=16, out_features=24, groups=1, activation=0, x=P, ldx=16, w=P, ldw=16,
+                          y=P, ldy=24)
+    for k, v in kw.items():
+        setattr(a, k, v)
+    return a
+
+
+def _bwd(**kw):
+    a = ve._LinearBackward(tokens=8, in_features=16, out_features=24, groups=1, activation=0, dy=P, lddy=24, w=P,
+                           ldw=16, x=P, ldx=16, dx=P, lddx=16, dw=P, lddw=16)
+    for k, v in kw.items():
+        setattr(a, k, v)
+    return a
+
+
+def _q(a, fn):
+    n = C.c_int64(-1)
+    rc = fn(C.byref(a), C.byref(n))
+    return rc, n.value
+
+
+@pytest.mark.parametrize("kw,rc", [
+    ({}, OK),
+    (dict(x=None), BAD), (dict(w=None), BAD), (dict(y=None), BAD),
+    (dict(tokens=0, x=None, y=None), OK),
+    (dict(tokens=-1), BAD), (dict(in_features=0), BAD), (dict(out_features=0), BAD),
+    (dict(tokens=1 << 31), UNSUP),
+    (dict(tokens=(1 << 31) - 1, out_features=(1 << 31) - 1, ldy=1 << 31), UNSUP),
+    (dict(ldx=15), BAD), (dict(ldw=15), BAD), (dict(ldy=23), BAD), (dict(residual=P, ldr=23), BAD),
+    (dict(z=P, ldz=23), BAD),
+    (dict(groups=0), BAD), (dict(groups=2), BAD), (dict(groups=65537, offsets=P, w_group=400), BAD),
+    (dict(groups=2, offsets=P, w_group=383), BAD), (dict(groups=2, offsets=P, w_group=384), OK),
+    (dict(groups=2, offsets=P, w_group=384, bias=P, bias_group=23), BAD),
+    (dict(activation=-1), BAD), (dict(activation=5), BAD),
+    (dict(z8=ve._Act8(P, 24, None, 1, 32)), BAD), (dict(z8=ve._Act8(P, 24, P, 1, 16)), BAD),
+    (dict(z8=ve._Act8(P, 23, P, 1, 32)), BAD), (dict(z8=ve._Act8(P, 24, P, 0, 32)), BAD),
+    (dict(z8=ve._Act8(P, 24, P, 1, 32)), OK),
+])
+def test_forward_checks(kw, rc):
+    got, need = _q(_fwd(**kw), ve.lib().ve_linear_forward_workspace)
+    assert got == rc
+    if rc != OK:
+        assert ve.lib().ve_last_error()
+        assert ve.lib().ve_linear_forward(C.byref(_fwd(**kw)), None, 0, None) == rc
+    else:
+        assert need >= 0
+
+
+@pytest.mark.parametrize("kw,rc", [
+    ({}, OK),
+    (dict(dy=None), BAD), (dict(w=None), BAD), (dict(w=None, dx=None), OK), (dict(x=None), BAD),
+    (dict(x=None, dw=None), OK), (dict(x8=ve._Act8(P, 16, P, 1, 32)), BAD),
+    (dict(x=None, x8=ve._Act8(P, 16, P, 1, 32)), OK), (dict(x=None, x8=ve._Act8(P, 16, P, 1, 48)), BAD),
+    (dict(activation=4), BAD), (dict(activation=4, z=P, ldz=24), OK), (dict(activation=4, z=P, ldz=23), BAD),
+    (dict(activation=4, z=P, ldz=24, z8=ve._Act8(P, 24, P, 1, 32)), BAD),
+    (dict(activation=4, z8=ve._Act8(P, 24, P, 1, 32)), OK),
+    (dict(lddy=23), BAD), (dict(ldw=15), BAD), (dict(lddx=15), BAD), (dict(lddw=15), BAD), (dict(ldx=15), BAD),
+    (dict(dx_add=P, ld_add=15), BAD),
+    (dict(groups=3, offsets=P, w_group=384, dw_group=383), BAD),
+    (dict(groups=3, offsets=P, w_group=383, dw_group=384), BAD),
+    (dict(groups=3, offsets=P, w_group=384, dw_group=384, dbias=P, dbias_group=23), BAD),
+    (dict(groups=3, offsets=P, w_group=384, dw_group=384), OK),
+    (dict(activation=7, z=P, ldz=24), BAD),
+])
+def test_backward_checks(kw, rc):
+    got, need = _q(_bwd(**kw), ve.lib().ve_linear_backward_workspace)
+    assert got == rc
+    if rc != OK:
+        assert ve.lib().ve_last_error()
+        assert ve.lib().ve_linear_backward(C.byref(_bwd(**kw)), None, 0, None) == rc
+    else:
+        assert need >= 0
+
+
+def test_null_records_and_workspace():
+    L = ve.lib()
+    n = C.c_int64()
+    assert L.ve_linear_forward(None, None, 0, None) == BAD
+    assert L.ve_linear_backward(None, None, 0, None) == BAD
+    assert L.ve_linear_forward_workspace(C.byref(_fwd()), None) == BAD
+    assert L.ve_linear_backward_workspace(None, C.byref(n)) == BAD
+    a = _bwd(activation=4, z=P, ldz=24)       # dz lives in the workspace
+    rc, need = _q(a, L.ve_linear_backward_workspace)
+    assert rc == OK and need >= 8 * 24 * 2
+    assert L.ve_linear_backward(C.byref(a), None, 0, None) == BAD
+    assert L.ve_linear_backward(C.byref(a), P, need - 1, None) == BAD
+    assert b"workspace" in L.ve_last_error()
+    assert L.ve_linear_backward(C.byref(a), P + 16, need, None) == BAD
+    assert b"aligned" in L.ve_last_error()
+    assert L.ve_linear_forward(C.byref(_fwd(tokens=0, x=None, y=None)), None, 0, None) == OK
+
+
+def test_act8_checks():
+    L = ve.lib()
+    q = ve._Act8(P, 100, P, 4, 32)
+    for f in (lambda rows, cols, x, ld, q: L.ve_act8_pack(x, ld, rows, cols, q, None),
+              lambda rows, cols, x, ld, q: L.ve_act8_unpack(q, rows, cols, x, ld, None)):
+        assert f(0, 100, None, 100, C.byref(q)) == OK
+        assert f(4, 100, P, 100, None) == BAD
+        assert f(4, 100, None, 100, C.byref(q)) == BAD
+        assert f(-1, 100, P, 100, C.byref(q)) == BAD
+        assert f(4, 0, P, 100, C.byref(q)) == BAD
+        assert f(4, 100, P, 99, C.byref(q)) == BAD
+        assert f(4, 101, P, 101, C.byref(q)) == BAD           # codes rows too short
+        assert f(4, 100, P, 100, C.byref(ve._Act8(P, 100, P, 3, 32))) == BAD
+        assert f(4, 100, P, 100, C.byref(ve._Act8(P, 100, P, 4, 33))) == BAD
+        assert f(4, 100, P, 100, C.byref(ve._Act8(None, 100, P, 4, 32))) == BAD
+        assert f(1 << 40, 100, P, 100, C.byref(q)) == UNSUP
+    assert L.ve_last_error()
+
+
+def test_binding_refuses_host_tensors_and_bad_names():
+    import torch
+    x, w, y = (torch.zeros(s, dtype=torch.bfloat16) for s in ((4, 8), (16, 8), (4, 16)))
+    with pytest.raises(ValueError, match="device tensor"):
+        ve.linear_forward(x, w, y)
+    with pytest.raises(ValueError, match="unknown activation"):
+        ve.linear_forward(x, w, y, activation="tanh")
+    with pytest.raises(ValueError, match="device tensor"):
+        ve.act8_pack(x, ve.new_act8(4, 8, device="cpu"))
+    with pytest.raises(ValueError, match="1-D int64"):
+        ve.linear_forward(x, w, y, offsets=torch.zeros(2, dtype=torch.int32))
