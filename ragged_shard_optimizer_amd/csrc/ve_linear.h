@@ -18,7 +18,7 @@ namespace ve {
 enum LinKind : int { kLinFwd = 0, kLinDx = 1, kLinDw = 2 };
 
 // Tile forms of the product kernel (option "linear_path" pins one).
-enum LinPath : int { kPathAuto = 0, kPathGeneral = 1, kPath128 = 2, kPath256 = 3, kPathFew = 4 };
+enum LinPath : int { kPathAuto = 0, kPathGeneral = 1, kPath128 = 2, kPathMid = 3, kPath256 = 4, kPathFew = 5 };
 
 struct LinArgs {
     const uint16_t* A; int64_t lda;           // x, dz, dz

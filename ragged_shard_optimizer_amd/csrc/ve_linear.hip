@@ -23,8 +23,8 @@
 //
 // MFMA 32x32x16 bf16, operands swapped (output columns as the first operand):
 // accumulator register r of lane l holds row l % 32 and column
-// 8 (r / 4) + 4 (l / 32) + r % 4 of a 32 x 32 block, so four registers are
-// four consecutive columns and leave as one 16-byte LDS write.
+// 8 (r / 4) + 4 (l / 32) + r % 4 of a 32 x 32 block: a lane's registers run
+// along a row.
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -44,7 +44,7 @@ typedef float f32x16 __attribute__((ext_vector_type(16)));
 constexpr int kCUs = 256;
 constexpr int BK = 64;          // contraction step
 
-// Workgroup tile BM x BN of waves of WM x WN; two LDS stages.
+// Workgroup tile BM x BN of four waves of WM x WN; two LDS stages.
 template <int BM_, int BN_, int WM_, int WN_>
 struct LinCfg {
     static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_;
@@ -52,18 +52,26 @@ struct LinCfg {
     static constexpr int THREADS = 64 * WAVES;
     static constexpr int TM = WM / 32, TN = WN / 32;
     static constexpr int A_ELEMS = BM * BK, B_ELEMS = BN * BK, STAGE_ELEMS = A_ELEMS + B_ELEMS;
-    static constexpr int LDC = BN + 4;
-    static constexpr int OP_BYTES = 2 * STAGE_ELEMS * 2, C_BYTES = WM * LDC * 4;
-    static constexpr int SMEM = OP_BYTES > C_BYTES ? OP_BYTES : C_BYTES;
+    static constexpr int SMEM = 2 * STAGE_ELEMS * 2;
     static_assert(SMEM <= 160 * 1024, "LDS");
     static constexpr int PER_CU = 160 * 1024 / SMEM;
 };
-using Cfg256 = LinCfg<256, 256, 128, 64>;
+using Cfg256 = LinCfg<256, 256, 128, 128>;
+using CfgMid = LinCfg<128, 256, 64, 128>;
 using Cfg128 = LinCfg<128, 128, 64, 64>;
+using CfgGen = LinCfg<128, 128, 32, 128>;
 
-// s_waitcnt operand: at most n vector-memory operations outstanding
-// (lgkm: also every LDS operation complete).
-constexpr int wait_vm(int n, bool lgkm) { return (lgkm ? 0x0070 : 0x0F70) | (n & 15) | (((n >> 4) & 3) << 14); }
+// s_waitcnt operands: at most n vector-memory operations outstanding; every
+// vector-memory and LDS operation complete.
+constexpr int wait_vm(int n) { return 0x0F70 | (n & 15) | (((n >> 4) & 3) << 14); }
+constexpr int kWaitAll = 0x0070;
+
+// Transposing read.  The restricted pointer carries that no store touches
+// these bytes while they are read; without it the compiler waits for every
+// direct load in flight (which fill the other stage) before the read.
+__device__ __forceinline__ s16x4 read_tr(const VE_LDS uint16_t* __restrict__ p) {
+    return __builtin_amdgcn_ds_read_tr16_b64_v4i16((s16x4 VE_LDS*)p);
+}
 
 // One operand of the workgroup's tile: ROWS tile rows (KC) or columns (KS)
 // over the contraction.  The tile of one step is ROWS * 128 bytes, filled in
@@ -81,7 +89,8 @@ struct Operand {
     int64_t kc;            // contraction length
     bool vec;              // !DMA: rows allow 16-byte loads
     int lrow, chunk, wave;
-    uint32_t voff;
+    uint32_t voff, step_off;
+    __amdgpu_buffer_rsrc_t rs;
     u32x4 reg[DMA ? 1 : PIECES];
 
     // swizzle of KC rows: consecutive rows of one bank line get distinct slots
@@ -106,27 +115,27 @@ struct Operand {
         }
         voff = (uint32_t)((lrow * ld + chunk * 8) * 2);
     }
-    // Bring step kt's tile in: by direct loads into the LDS stage at `st`, or
-    // into registers (then put() writes them to LDS).
-    __device__ __forceinline__ void get(uint16_t* st, int64_t kt) {
+    // Direct loads of step kt's tile into the LDS stage at `st`: begin() for
+    // the step, then piece() for each piece.  A buffer resource from the
+    // step's first element on: reads past the last valid row return 0, and so
+    // do those of a KC row past the contraction (sent past the end by hand)
+    // and every read of a step past the last (kt >= nk).
+    __device__ __forceinline__ void begin(int64_t kt, bool live) {
         const int64_t k0 = kt * BK;
-        if constexpr (DMA) {
-            // A buffer resource from this step's first element on: reads past
-            // the last valid row return 0, and so do those of a KC row past
-            // the contraction (sent past the end by hand).
-            const uint16_t* p = KS ? base + k0 * ld : base + k0;
-            const int64_t rows = KS ? (kc - k0 < BK ? kc - k0 : BK) : valid;
-            const uint32_t bytes = (uint32_t)(((rows - 1) * ld + (KS ? valid : kc - k0)) * 2);
-            const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc((void*)p, (short)0, (int)bytes, 0x00020000);
-            const bool in = KS || k0 + chunk * 8 < kc;
-#pragma unroll
-            for (int q = 0; q < PIECES; ++q) {
-                uint32_t v = voff + (uint32_t)(q * WAVES * LROWS * (int)ld * 2);
-                if (!KS) v = in ? v : 0x80000000u;
-                __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (void VE_LDS*)(st + (WAVES * q + wave) * 512), 16, (int)v, 0,
-                                                         0, 0);
-            }
-        } else {
+        const uint16_t* p = KS ? base + k0 * ld : base + k0;
+        const int64_t rows = KS ? (kc - k0 < BK ? kc - k0 : BK) : valid;
+        const uint32_t bytes = live ? (uint32_t)(((rows - 1) * ld + (KS ? valid : kc - k0)) * 2) : 0u;
+        rs = __builtin_amdgcn_make_buffer_rsrc((void*)p, (short)0, (int)bytes, 0x00020000);
+        step_off = KS || k0 + chunk * 8 < kc ? voff : 0x80000000u;
+    }
+    __device__ __forceinline__ void piece(uint16_t* st, int q) {
+        const uint32_t v = step_off + (uint32_t)(q * WAVES * LROWS * (int)ld * 2);
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (void VE_LDS*)(st + (WAVES * q + wave) * 512), 16, (int)v, 0, 0, 0);
+    }
+    // Step kt's tile into registers (put() then writes them to LDS).
+    __device__ __forceinline__ void get(int64_t kt) {
+        const int64_t k0 = kt * BK;
+        if constexpr (!DMA) {
 #pragma unroll
             for (int q = 0; q < PIECES; ++q) {
                 const int row = lrow + q * WAVES * LROWS;
@@ -149,18 +158,15 @@ struct Operand {
             for (int q = 0; q < PIECES; ++q) *(u32x4*)(st + (WAVES * q + wave) * 512 + lane * 8) = reg[q];
         }
     }
-    // LDS byte offsets of a lane's fragment of the 32 rows (columns) from r0
-    // on, 16-deep sub-step 0; KC sub-steps differ in the slot, KS ones by
-    // 16 rows.
+    // A lane's fragment of the 32 rows (columns) from r0 on, sub-step kk.
     __device__ static __forceinline__ bf16x8 frag(const uint16_t* st, int r0, int kk, int lane) {
         if constexpr (KS) {
             const int g = lane >> 4, i = lane & 15;
-            const int k = kk * 16 + (g >> 1) * 8 + (i >> 2);
-            const int s = r0 / 16 + (g & 1);
+            const int k = kk * 16 + (g >> 1) * 8 + (i >> 2), s = r0 / 16 + (g & 1);
             const uint16_t* p = st + k * ROWS + (place(s) ^ (i >> 2)) * 16 + (i & 3) * 4;
-            const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((s16x4 VE_LDS*)p);
-            const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((s16x4 VE_LDS*)(p + 4 * ROWS));
-            return __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+            return __builtin_bit_cast(bf16x8, __builtin_shufflevector(read_tr((const VE_LDS uint16_t*)p),
+                                                                      read_tr((const VE_LDS uint16_t*)(p + 4 * ROWS)), 0, 1,
+                                                                      2, 3, 4, 5, 6, 7));
         } else {
             const int row = r0 + (lane & 31), slot = (2 * kk + (lane >> 5)) ^ swz(row & 15);
             return __builtin_bit_cast(bf16x8, *(const u32x4*)(st + row * BK + slot * 8));
@@ -224,12 +230,32 @@ __device__ __forceinline__ bool tile_of(const LinArgs& g, int64_t t, TileAt& at)
 }
 
 // Epilogue of 8 consecutive columns of one output row: `row` the token (or
-// the row of dw[e]), col the first column, cnt of the 8 that exist (0: none;
-// such lanes still take part in the runs' maxima).
+// the row of dw[e]), col the first column, cnt of the 8 that exist (0: none).
+// First the bias (rows of tokens), then, where z is saved in 8 bits, the
+// largest magnitude of the run the columns lie in, which the caller finds
+// across its lanes, then the rest.
 template <int KIND>
-__device__ __forceinline__ void finish8(const LinArgs& g, int e, int64_t row, int64_t col, int cnt, float* v) {
+__device__ __forceinline__ void bias8(const LinArgs& g, int e, int64_t col, int cnt, float* v) {
+    if constexpr (KIND == kLinFwd) {
+        if (!g.bias || cnt <= 0) return;
+        float o[8];
+        widen8(load_bf16x8(g.bias + (int64_t)e * g.bias_group + col, cnt, g.vec_bias), o);
+#pragma unroll
+        for (int t = 0; t < 8; ++t) v[t] += o[t];
+    }
+}
+
+__device__ __forceinline__ uint32_t amax8(const float* v, int cnt) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int t = 0; t < 8; ++t) m = t < cnt ? amax_of(m, v[t]) : m;
+    return m;
+}
+
+template <int KIND>
+__device__ __forceinline__ void finish8(const LinArgs& g, int e, int64_t row, int64_t col, int cnt, float* v, uint32_t amax) {
+    if (cnt <= 0) return;
     if constexpr (KIND == kLinDw) {
-        if (cnt <= 0) return;
         const int64_t at = (int64_t)e * g.dw_group + row * g.lddw + col;
         if (g.wide) {
             VE_GLOBAL float* p = (VE_GLOBAL float*)((float*)g.dw + at);
@@ -257,32 +283,19 @@ __device__ __forceinline__ void finish8(const LinArgs& g, int e, int64_t row, in
             store_bf16x8(p, narrow8(v), cnt, g.vec_dw);
         }
     } else {
-        if (g.bias && cnt > 0) {
-            float o[8];
-            widen8(load_bf16x8(g.bias + (int64_t)e * g.bias_group + col, cnt, g.vec_bias), o);
-#pragma unroll
-            for (int t = 0; t < 8; ++t) v[t] += o[t];
-        }
         if constexpr (KIND == kLinFwd) {
-            if (g.z && cnt > 0) store_bf16x8(g.z + row * g.ldz + col, narrow8(v), cnt, g.vec_z);
+            if (g.z) store_bf16x8(g.z + row * g.ldz + col, narrow8(v), cnt, g.vec_z);
             if (g.z8.codes) {
-                uint32_t m = 0;
-#pragma unroll
-                for (int t = 0; t < 8; ++t) m = t < cnt ? amax_of(m, v[t]) : m;
-                m = amax_lanes(m, g.z8.block / 8);
-                const RunCode c = run_code(__uint_as_float(m));
-                if (cnt > 0) {
-                    store_codes8(g.z8.codes + row * g.z8.ld_codes + col, encode8(c, v), cnt, g.vec_z8);
-                    const uint32_t run = (uint32_t)col >> __builtin_ctz(g.z8.block);
-                    if (((uint32_t)col & (g.z8.block - 1)) == 0) g.z8.scales[row * g.z8.ld_scales + run] = c.scale;
-                }
+                const RunCode c = run_code(__uint_as_float(amax));
+                store_codes8(g.z8.codes + row * g.z8.ld_codes + col, encode8(c, v), cnt, g.vec_z8);
+                const uint32_t run = (uint32_t)col >> __builtin_ctz(g.z8.block);
+                if (((uint32_t)col & (g.z8.block - 1)) == 0) g.z8.scales[row * g.z8.ld_scales + run] = c.scale;
             }
             if (g.act != VE_ACT_NONE) {
 #pragma unroll
                 for (int t = 0; t < 8; ++t) v[t] = activate(g.act, v[t]);
             }
         }
-        if (cnt <= 0) return;
         if (g.res) {
             float o[8];
             widen8(load_bf16x8(g.res + row * g.ldr + col, cnt, g.vec_res), o);
@@ -297,7 +310,7 @@ __device__ __forceinline__ void finish8(const LinArgs& g, int e, int64_t row, in
 // memory to LDS (16-byte rows, no ragged ends inside 16 bytes); else through
 // registers, from any alignment.
 template <class CF, int KIND, bool DMA>
-__global__ void __launch_bounds__(CF::THREADS) k_product(LinArgs g) {
+__global__ void __launch_bounds__(CF::THREADS, CF::PER_CU) k_product(LinArgs g) {
     constexpr int TM = CF::TM, TN = CF::TN, WM = CF::WM, WN = CF::WN;
     constexpr bool AKS = KIND == kLinDw, BKS = KIND != kLinFwd;
     __shared__ __attribute__((aligned(1024))) unsigned char smem[CF::SMEM];
@@ -350,102 +363,170 @@ __global__ void __launch_bounds__(CF::THREADS) k_product(LinArgs g) {
         nk = min(per, nk - kbeg);
     }
     auto stage = [&](int64_t kt) { return ops + (int)(kt & 1) * CF::STAGE_ELEMS; };
-    auto get = [&](int64_t kt) {
-        A.get(stage(kt), kbeg + kt);
-        B.get(stage(kt) + CF::A_ELEMS, kbeg + kt);
-    };
-    auto put = [&](int64_t kt) {
-        A.put(stage(kt), lane);
-        B.put(stage(kt) + CF::A_ELEMS, lane);
-    };
-    // this wave's loads (and LDS writes) of the next stage are complete, then
-    // everyone's: a bare barrier, with the LDS accesses pinned around it
+    // this wave's loads and LDS accesses are complete, then everyone's: a
+    // bare barrier, with the LDS accesses pinned around it
     auto ready = [&]() {
-        __builtin_amdgcn_s_waitcnt(wait_vm(0, !DMA));
+        __builtin_amdgcn_s_waitcnt(kWaitAll);
         asm volatile("" ::: "memory");
         __builtin_amdgcn_s_barrier();
         asm volatile("" ::: "memory");
     };
     bf16x8 fa[2][TM], fb[2][TN];
-    auto frag = [&](int buf, int kk, int64_t kt) {
+    constexpr int NF = TM + TN, MM = TM * TN, H = MM / 2;
+    // fragment f of sub-step kk in the order the MFMAs need them: A0, all B, the other A
+    auto frag1 = [&](int buf, int f, int kk, int64_t kt) {
         const uint16_t* st = stage(kt);
-#pragma unroll
-        for (int a = 0; a < TM; ++a) fa[buf][a] = A.frag(st, wr * WM + a * 32, kk, lane);
-#pragma unroll
-        for (int b = 0; b < TN; ++b) fb[buf][b] = B.frag(st + CF::A_ELEMS, wc * WN + b * 32, kk, lane);
+        if (f == 0 || f > TN) {
+            const int a = f == 0 ? 0 : f - TN;
+            fa[buf][a] = A.frag(st, wr * WM + a * 32, kk, lane);
+        } else {
+            fb[buf][f - 1] = B.frag(st + CF::A_ELEMS, wc * WN + (f - 1) * 32, kk, lane);
+        }
     };
-    auto mfma = [&](int buf, int a, int b) {
+    auto mfma = [&](int buf, int m) {
+        const int a = m / TN, b = m % TN;
         acc[a][b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fb[buf][b], fa[buf][a], acc[a][b], 0, 0, 0);
     };
-    if (nk > 0) {
+    if constexpr (DMA) {
+        // Every MFMA is followed by its share of what feeds the later ones,
+        // in this order (the scheduling barriers keep it): the fragment
+        // reads of the next sub-step, and direct loads.  In the middle of a
+        // step's last sub-step all its reads are complete: the barrier there
+        // frees its stage and makes the next one visible, and A's loads of
+        // step kt + 2 go out in the freed stage at once, B's at the start of
+        // the next step: they have at least two and a half sub-steps to land.
+        auto A_st = [&](int64_t kt) { return stage(kt); };
+        auto B_st = [&](int64_t kt) { return stage(kt) + CF::A_ELEMS; };
+        using OpA = decltype(A);
+        using OpB = decltype(B);
+        constexpr int PA = OpA::PIECES, PB = OpB::PIECES;
+        if (nk > 0) {
+            A.begin(kbeg, true);
+            B.begin(kbeg, true);
+#pragma unroll
+            for (int q = 0; q < PA; ++q) A.piece(A_st(0), q);
+#pragma unroll
+            for (int q = 0; q < PB; ++q) B.piece(B_st(0), q);
+            A.begin(kbeg + 1, nk > 1);
+#pragma unroll
+            for (int q = 0; q < PA; ++q) A.piece(A_st(1), q);
+            __builtin_amdgcn_s_waitcnt(wait_vm(PA));
+            asm volatile("" ::: "memory");
+            __builtin_amdgcn_s_barrier();
+            asm volatile("" ::: "memory");
+#pragma unroll
+            for (int f = 0; f < NF; ++f) frag1(0, f, 0, 0);
+            for (int64_t kt = 0; kt < nk; ++kt) {
+                B.begin(kbeg + kt + 1, kt + 1 < nk);
+#pragma unroll
+                for (int kk = 0; kk < BK / 16 - 1; ++kk) {
+#pragma unroll
+                    for (int m = 0; m < MM; ++m) {
+                        mfma(kk & 1, m);
+#pragma unroll
+                        for (int f = m * NF / MM; f < (m + 1) * NF / MM; ++f) frag1((kk + 1) & 1, f, kk + 1, kt);
+                        if (kk == 0) {
+#pragma unroll
+                            for (int q = m * PB / MM; q < (m + 1) * PB / MM; ++q) B.piece(B_st(kt + 1), q);
+                        }
+                        __builtin_amdgcn_sched_barrier(0);
+                    }
+                }
+                A.begin(kbeg + kt + 2, kt + 2 < nk);
+#pragma unroll
+                for (int m = 0; m < H; ++m) mfma(1, m);
+                __builtin_amdgcn_sched_barrier(0);
+                ready();
+#pragma unroll
+                for (int m = H; m < MM; ++m) {
+                    mfma(1, m);
+#pragma unroll
+                    for (int f = (m - H) * NF / H; f < (m - H + 1) * NF / H; ++f) frag1(0, f, 0, kt + 1);
+#pragma unroll
+                    for (int q = (m - H) * PA / H; q < (m - H + 1) * PA / H; ++q) A.piece(A_st(kt + 2), q);
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+            }
+            // the loads past the last step (of nothing) land before the end
+            __builtin_amdgcn_s_waitcnt(kWaitAll);
+        }
+    } else if (nk > 0) {
+        auto get = [&](int64_t kt) {
+            A.get(kbeg + kt);
+            B.get(kbeg + kt);
+        };
+        auto put = [&](int64_t kt) {
+            A.put(stage(kt), lane);
+            B.put(stage(kt) + CF::A_ELEMS, lane);
+        };
         get(0);
         put(0);
         ready();
-        frag(0, 0, 0);
         for (int64_t kt = 0; kt < nk; ++kt) {
-            // every wave's reads of the other stage were complete before the
-            // barrier inside step kt - 1
+            // the next step's registers are loaded while this one computes,
+            // and written to the other stage, which everyone's reads left
+            // before the last barrier
             if (kt + 1 < nk) get(kt + 1);
 #pragma unroll
             for (int kk = 0; kk < BK / 16; ++kk) {
-                if (kk + 1 < BK / 16) {
-                    frag((kk + 1) & 1, kk + 1, kt);
 #pragma unroll
-                    for (int a = 0; a < TM; ++a)
+                for (int f = 0; f < NF; ++f) frag1(kk & 1, f, kk, kt);
 #pragma unroll
-                        for (int b = 0; b < TN; ++b) mfma(kk & 1, a, b);
-                    if (!DMA && kk == 1 && kt + 1 < nk) put(kt + 1);
-                } else {
-                    // last sub-step: all reads of this stage are complete.
-                    // Half of its MFMAs, the barrier, the next step's first
-                    // reads (on the last step they fetch an unused stage),
-                    // the other half.
-#pragma unroll
-                    for (int i = 0; i < TM * TN / 2; ++i) mfma(kk & 1, i / TN, i % TN);
-                    ready();
-                    frag(0, 0, kt + 1);
-#pragma unroll
-                    for (int i = TM * TN / 2; i < TM * TN; ++i) mfma(kk & 1, i / TN, i % TN);
-                }
+                for (int m = 0; m < MM; ++m) mfma(kk & 1, m);
             }
+            if (kt + 1 < nk) put(kt + 1);
+            ready();
         }
     }
-    __syncthreads();
 
-    // epilogue, one row of waves at a time through fp32 rows in LDS
-    float* sC = (float*)smem;
-    constexpr int LDC = CF::LDC, CPR = CF::BN / 8;
+    // Epilogue: each wave passes its accumulators through its own share of
+    // LDS (no barrier between the waves), PA rows of 32 at a time, so that a
+    // lane gets 8 consecutive columns and WN / 8 lanes a whole row of the
+    // wave's tile: 16-byte accesses, and runs saved in 8 bits are
+    // neighbouring lanes.  A row's 16-byte chunks lie even ones first, then
+    // odd ones, permuted by the row: a write (32 rows of one chunk) and a read
+    // (the even, then the odd chunks of a row) touch distinct banks.
+    __syncthreads();
+    constexpr int CPR = WN / 8, ROWB = WN * 4, PASS = (CF::SMEM / CF::WAVES) / (32 * ROWB);
+    constexpr int PAS = PASS < TM ? PASS : TM;  // rows of 32 in one pass
+    static_assert(PAS >= 1 && TM % PAS == 0, "epilogue passes");
+    unsigned char* sw = smem + wave * (CF::SMEM / CF::WAVES);
 #pragma unroll 1
-    for (int pass = 0; pass < CF::WAVES_M; ++pass) {
-        if (wr == pass) {
+    for (int pass = 0; pass < TM / PAS; ++pass) {
 #pragma unroll
-            for (int a = 0; a < TM; ++a)
+        for (int a = 0; a < TM; ++a)
+            if (a / PAS == pass) {
 #pragma unroll
                 for (int b = 0; b < TN; ++b)
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
-                        const f32x4 v = {acc[a][b][4 * q], acc[a][b][4 * q + 1], acc[a][b][4 * q + 2], acc[a][b][4 * q + 3]};
-                        *(f32x4*)&sC[(a * 32 + (lane & 31)) * LDC + wc * WN + b * 32 + 8 * q + 4 * (lane >> 5)] = v;
+                        const int r = (a % PAS) * 32 + (lane & 31), c = ((4 * b + q) ^ (r & (CPR - 1))) + CPR * (lane >> 5);
+                        *(f32x4*)(sw + r * ROWB + c * 16) =
+                            f32x4{acc[a][b][4 * q], acc[a][b][4 * q + 1], acc[a][b][4 * q + 2], acc[a][b][4 * q + 3]};
                     }
-        }
-        __syncthreads();
-        const int rows = (int)at.rows - pass * WM;  // rows of this pass that exist
-#pragma unroll 1
-        for (int q = 0; q < WM * CPR / CF::THREADS; ++q) {
-            const int id = tid + CF::THREADS * q, row = id / CPR, c8 = (id % CPR) * 8;
+            }
+        __builtin_amdgcn_wave_barrier();
+#pragma unroll 2
+        for (int i = 0; i < PAS * 32 * CPR / 64; ++i) {
+            const int id = lane + 64 * i, r = id / CPR, c8 = id % CPR;
             float v[8];
-            *(f32x4*)&v[0] = *(const f32x4*)&sC[row * LDC + c8];
-            *(f32x4*)&v[4] = *(const f32x4*)&sC[row * LDC + c8 + 4];
+            const unsigned char* src = sw + r * ROWB + (c8 ^ (r & (CPR - 1))) * 16;
+            *(f32x4*)&v[0] = *(const f32x4*)src;
+            *(f32x4*)&v[4] = *(const f32x4*)(src + CPR * 16);
+            const int rr = wr * WM + pass * (PAS * 32) + r, cc = wc * WN + c8 * 8;  // in the workgroup's tile
             if (g.ksplit > 1) {
-                float* out = g.partial + ((int64_t)slice * g.tiles + t) * (CF::BM * CF::BN) +
-                             (pass * WM + row) * CF::BN + c8;
+                float* out = g.partial + ((int64_t)slice * g.tiles + t) * (CF::BM * CF::BN) + rr * CF::BN + cc;
                 *(f32x4*)out = *(const f32x4*)&v[0];
                 *(f32x4*)(out + 4) = *(const f32x4*)&v[4];
-            } else {
-                finish8<KIND>(g, at.e, at.row0 + pass * WM + row, at.col0 + c8, row < rows ? min(cols - c8, 8) : 0, v);
+                continue;
             }
+            const int cnt = rr < at.rows ? min(max(cols - cc, 0), 8) : 0;
+            bias8<KIND>(g, at.e, at.col0 + cc, cnt, v);
+            uint32_t m = 0;
+            if (KIND == kLinFwd && g.z8.codes) m = amax_lanes(amax8(v, cnt), g.z8.block / 8);
+            finish8<KIND>(g, at.e, at.row0 + rr, at.col0 + cc, cnt, v, m);
         }
-        __syncthreads();
+        __builtin_amdgcn_wave_barrier();
     }
 }
 
@@ -472,7 +553,11 @@ __global__ void __launch_bounds__(256) k_join(LinArgs g) {
         }
     }
     const int cols = (int)(g.N - at.col0 < CF::BN ? g.N - at.col0 : CF::BN);
-    finish8<KIND>(g, at.e, at.row0 + row, at.col0 + c8, row < at.rows ? min(cols - c8, 8) : 0, v);
+    const int cnt = row < at.rows ? min(max(cols - c8, 0), 8) : 0;
+    bias8<KIND>(g, at.e, at.col0 + c8, cnt, v);
+    uint32_t m = 0;
+    if (KIND == kLinFwd && g.z8.codes) m = amax_lanes(amax8(v, cnt), g.z8.block / 8);
+    finish8<KIND>(g, at.e, at.row0 + row, at.col0 + c8, cnt, v, m);
 }
 
 template <class CF>
@@ -512,8 +597,9 @@ template <int KIND>
 hipError_t launch_path(const LinArgs& g, const LinPlan& p, hipStream_t s) {
     switch (p.path) {
     case kPath256: return launch_kind<Cfg256, KIND, true>(g, p.ksplit, s);
+    case kPathMid: return launch_kind<CfgMid, KIND, true>(g, p.ksplit, s);
     case kPath128: return launch_kind<Cfg128, KIND, true>(g, p.ksplit, s);
-    default: return launch_kind<Cfg128, KIND, false>(g, p.ksplit, s);
+    default: return launch_kind<CfgGen, KIND, false>(g, p.ksplit, s);
     }
 }
 
@@ -528,11 +614,15 @@ LinPlan plan_product(const LinArgs& g, LinKind kind) {
         if (g.offsets || option(kOptLinearSplit) == 0 || tiles * 2 > slots || nk < 16) return 1;
         return (int)std::min<int64_t>(std::min(slots / std::max<int64_t>(tiles, 1), nk / 8), 32);
     };
-    if (dma_ok(g, kind) && pin != kPathGeneral) p.path = t256 >= 2 * kCUs ? kPath256 : kPath128;
-    if (p.path != kPathGeneral && (pin == kPath128 || pin == kPath256)) p.path = (int)pin;
-    const int64_t tiles = p.path == kPath256 ? t256 : t128;
-    const int64_t area = p.path == kPath256 ? 256 * 256 : 128 * 128;
-    p.ksplit = std::max(1, split(tiles, kCUs * (p.path == kPath256 ? Cfg256::PER_CU : Cfg128::PER_CU)));
+    const int64_t tmid = tiles_of<CfgMid>(g, kind);
+    if (dma_ok(g, kind) && pin != kPathGeneral) p.path = t256 >= 2 * kCUs ? kPath256 : tmid >= kCUs ? kPathMid : kPath128;
+    if (p.path != kPathGeneral && (pin == kPath128 || pin == kPathMid || pin == kPath256)) p.path = (int)pin;
+    // a wave of the 128 x 128 tile has 64 columns, half a run of 128
+    const bool wide_runs = kind == kLinFwd && g.z8.codes && g.z8.block > Cfg128::WN;
+    if (p.path == kPath128 && wide_runs) p.path = kPathMid;
+    const int64_t tiles = p.path == kPath256 ? t256 : p.path == kPathMid ? tmid : t128;
+    const int64_t area = p.path == kPath256 ? 256 * 256 : p.path == kPathMid ? 128 * 256 : 128 * 128;
+    p.ksplit = std::max(1, split(tiles, kCUs * (p.path == kPath256 || p.path == kPathMid ? 1 : Cfg128::PER_CU)));
     p.partial_bytes = p.ksplit > 1 ? p.ksplit * tiles * area * 4 : 0;
     return p;
 }
