@@ -42,6 +42,7 @@ typedef float f32x16 __attribute__((ext_vector_type(16)));
 #define VE_LDS __attribute__((address_space(3)))
 
 constexpr int kCUs = 256;
+constexpr int kFewTokens = 16;  // rows of the few-token form
 constexpr int BK = 64;          // contraction step
 
 // Workgroup tile BM x BN of four waves of WM x WN; two LDS stages.
@@ -392,32 +393,45 @@ __global__ void __launch_bounds__(CF::THREADS, CF::PER_CU) k_product(LinArgs g) 
         // in this order (the scheduling barriers keep it): the fragment
         // reads of the next sub-step, and direct loads.  In the middle of a
         // step's last sub-step all its reads are complete: the barrier there
-        // frees its stage and makes the next one visible, and A's loads of
-        // step kt + 2 go out in the freed stage at once, B's at the start of
-        // the next step: they have at least two and a half sub-steps to land.
-        auto A_st = [&](int64_t kt) { return stage(kt); };
-        auto B_st = [&](int64_t kt) { return stage(kt) + CF::A_ELEMS; };
+        // frees its stage and makes the next one visible, and from there on
+        // the loads of step kt + 2 go out into the freed stage, spread evenly
+        // over two sub-steps: issued faster they stall the wave (all within
+        // half a sub-step: 1,207 TFLOP/s forward at 8192^3, one sub-step:
+        // 1,260), later they have less time to land (two and a half: 1,283;
+        // two: 1,306).
         using OpA = decltype(A);
         using OpB = decltype(B);
-        constexpr int PA = OpA::PIECES, PB = OpB::PIECES;
+        constexpr int PA = OpA::PIECES, PB = OpB::PIECES, P = PA + PB, SPAN = 2 * MM;
+        static_assert(SPAN <= H + 3 * MM, "loads of a step must be issued before its barrier");
+        auto begin = [&](int64_t kt) {
+            A.begin(kbeg + kt, kt < nk);
+            B.begin(kbeg + kt, kt < nk);
+        };
+        // the pieces of slot s (s MFMAs behind the barrier)
+        auto pieces = [&](int s, int64_t kt) {
+#pragma unroll
+            for (int p = 0; p < P; ++p)
+                if (p * SPAN / P == s) {
+                    if (p < PA) A.piece(stage(kt), p);
+                    else B.piece(stage(kt) + CF::A_ELEMS, p - PA);
+                }
+        };
         if (nk > 0) {
-            A.begin(kbeg, true);
-            B.begin(kbeg, true);
+            begin(0);
 #pragma unroll
-            for (int q = 0; q < PA; ++q) A.piece(A_st(0), q);
+            for (int q = 0; q < PA; ++q) A.piece(stage(0), q);
 #pragma unroll
-            for (int q = 0; q < PB; ++q) B.piece(B_st(0), q);
-            A.begin(kbeg + 1, nk > 1);
+            for (int q = 0; q < PB; ++q) B.piece(stage(0) + CF::A_ELEMS, q);
+            __builtin_amdgcn_s_waitcnt(kWaitAll);
+            begin(1);
 #pragma unroll
-            for (int q = 0; q < PA; ++q) A.piece(A_st(1), q);
-            __builtin_amdgcn_s_waitcnt(wait_vm(PA));
+            for (int s = 0; s < H; ++s) pieces(s, 1);
             asm volatile("" ::: "memory");
             __builtin_amdgcn_s_barrier();
             asm volatile("" ::: "memory");
 #pragma unroll
             for (int f = 0; f < NF; ++f) frag1(0, f, 0, 0);
             for (int64_t kt = 0; kt < nk; ++kt) {
-                B.begin(kbeg + kt + 1, kt + 1 < nk);
 #pragma unroll
                 for (int kk = 0; kk < BK / 16 - 1; ++kk) {
 #pragma unroll
@@ -425,25 +439,21 @@ __global__ void __launch_bounds__(CF::THREADS, CF::PER_CU) k_product(LinArgs g) 
                         mfma(kk & 1, m);
 #pragma unroll
                         for (int f = m * NF / MM; f < (m + 1) * NF / MM; ++f) frag1((kk + 1) & 1, f, kk + 1, kt);
-                        if (kk == 0) {
-#pragma unroll
-                            for (int q = m * PB / MM; q < (m + 1) * PB / MM; ++q) B.piece(B_st(kt + 1), q);
-                        }
+                        pieces(H + kk * MM + m, kt + 1);
                         __builtin_amdgcn_sched_barrier(0);
                     }
                 }
-                A.begin(kbeg + kt + 2, kt + 2 < nk);
 #pragma unroll
                 for (int m = 0; m < H; ++m) mfma(1, m);
                 __builtin_amdgcn_sched_barrier(0);
                 ready();
+                begin(kt + 2);
 #pragma unroll
                 for (int m = H; m < MM; ++m) {
                     mfma(1, m);
 #pragma unroll
                     for (int f = (m - H) * NF / H; f < (m - H + 1) * NF / H; ++f) frag1(0, f, 0, kt + 1);
-#pragma unroll
-                    for (int q = (m - H) * PA / H; q < (m - H + 1) * PA / H; ++q) A.piece(A_st(kt + 2), q);
+                    pieces(m - H, kt + 2);
                     __builtin_amdgcn_sched_barrier(0);
                 }
             }
@@ -560,6 +570,84 @@ __global__ void __launch_bounds__(256) k_join(LinArgs g) {
     finish8<KIND>(g, at.e, at.row0 + row, at.col0 + c8, cnt, v, m);
 }
 
+// Few tokens (forward, one group): bound by reading the weights, so the
+// contraction is what is split.  A workgroup takes 16 output columns (rows of
+// w); its waves take turns of 128 along the contraction, straight from memory
+// into MFMA fragments (no element of w is read twice, so LDS would only add a
+// copy), with the next turn's loads in flight.  The waves' sums are joined in
+// LDS in wave order, and 8 columns of a token go through the epilogue
+// together.  One token, 8192 -> 28672: 89 us, 5.3 TB/s (128 x 128 tiles: 131);
+// 32 columns a workgroup 104, 4 waves instead of 8 95.
+//
+// MFMA 16x16x32 bf16, w as the first operand: lane l reads 8 consecutive k
+// (8 (l / 16) + 0 .. 7) of row l % 16; accumulator register r of lane l holds
+// column 4 (l / 16) + r of token l % 16.
+template <int WAVES>
+__global__ void __launch_bounds__(64 * WAVES) k_few(LinArgs g) {
+    constexpr int U = 4, MT = kFewTokens, NR = 16, LDN = NR + 4;  // LDS rows of NR columns, padded
+    __shared__ __attribute__((aligned(16))) float part[WAVES][MT][LDN];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+    const int64_t n0 = (int64_t)blockIdx.x * NR;
+    const int wrows = (int)min(g.N - n0, (int64_t)NR), toks = (int)g.T, row = lane & 15, k8 = (lane >> 4) * 8;
+    const __amdgpu_buffer_rsrc_t wr = __builtin_amdgcn_make_buffer_rsrc(
+        (void*)(g.B + n0 * g.ldb), (short)0, (int)(uint32_t)(((wrows - 1) * g.ldb + g.K) * 2), 0x00020000);
+    const __amdgpu_buffer_rsrc_t xr = __builtin_amdgcn_make_buffer_rsrc(
+        (void*)g.A, (short)0, (int)(uint32_t)(((toks - 1) * g.lda + g.K) * 2), 0x00020000);
+    const int K = (int)g.K;
+    // byte offsets of the lane's rows; reads past the last row or the
+    // contraction are sent out of the buffers and return 0
+    const uint32_t wrow = row < wrows ? (uint32_t)(row * g.ldb * 2) : 0x80000000u;
+    const uint32_t xrow = row < toks ? (uint32_t)(row * g.lda * 2) : 0x80000000u;
+    f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+    u32x4 w[2][U], x[2][U];
+    auto load = [&](int buf, int k0) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int k = k0 + 32 * u + k8;
+            const uint32_t off = k < K ? (uint32_t)k * 2 : 0x40000000u;
+            w[buf][u] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(wr, (int)(wrow + off), 0, 0));
+            x[buf][u] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(xr, (int)(xrow + off), 0, 0));
+        }
+    };
+    auto compute = [&](int buf) {
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, w[buf][u]),
+                                                          __builtin_bit_cast(bf16x8, x[buf][u]), acc, 0, 0, 0);
+    };
+    constexpr int STEP = 32 * U * WAVES;
+    int k0 = 32 * U * wave;
+    load(0, k0);
+    for (; k0 < K; k0 += 2 * STEP) {
+        load(1, k0 + STEP);
+        compute(0);
+        load(0, k0 + 2 * STEP);
+        compute(1);
+    }
+    *(f32x4*)&part[wave][row][4 * (lane >> 4)] = acc;
+    __syncthreads();
+    const int t = threadIdx.x / (NR / 8), c8 = (threadIdx.x % (NR / 8)) * 8;
+    if (t >= toks) return;
+    float v[8];
+#pragma unroll
+    for (int c = 0; c < 8; ++c) v[c] = part[0][t][c8 + c];
+#pragma unroll
+    for (int s = 1; s < WAVES; ++s)
+#pragma unroll
+        for (int c = 0; c < 8; ++c) v[c] += part[s][t][c8 + c];
+    const int cnt = min(max(wrows - c8, 0), 8);
+    bias8<kLinFwd>(g, 0, n0 + c8, cnt, v);
+    finish8<kLinFwd>(g, 0, t, n0 + c8, cnt, v, 0);
+}
+
+hipError_t launch_few(const LinArgs& g, hipStream_t s) {
+    // 8 waves a workgroup; 16 where there are too few workgroups to fill the CUs
+    const unsigned grid = (unsigned)((g.N + 15) / 16);
+    if (grid <= 4 * kCUs) hipLaunchKernelGGL(k_few<16>, dim3(grid), dim3(1024), 0, s, g);
+    else hipLaunchKernelGGL(k_few<8>, dim3(grid), dim3(512), 0, s, g);
+    return hipGetLastError();
+}
+
 template <class CF>
 int64_t tiles_of(const LinArgs& g, LinKind kind) {
     const int64_t tn = (g.N + CF::BN - 1) / CF::BN;
@@ -596,6 +684,7 @@ bool dma_ok(const LinArgs& g, LinKind kind) {
 template <int KIND>
 hipError_t launch_path(const LinArgs& g, const LinPlan& p, hipStream_t s) {
     switch (p.path) {
+    case kPathFew: return launch_few(g, s);
     case kPath256: return launch_kind<Cfg256, KIND, true>(g, p.ksplit, s);
     case kPathMid: return launch_kind<CfgMid, KIND, true>(g, p.ksplit, s);
     case kPath128: return launch_kind<Cfg128, KIND, true>(g, p.ksplit, s);
@@ -614,6 +703,16 @@ LinPlan plan_product(const LinArgs& g, LinKind kind) {
         if (g.offsets || option(kOptLinearSplit) == 0 || tiles * 2 > slots || nk < 16) return 1;
         return (int)std::min<int64_t>(std::min(slots / std::max<int64_t>(tiles, 1), nk / 8), 32);
     };
+    // Up to 8 tokens the few-token form is faster (us, 8192 -> 28672 one token
+    // 89 against 131 of the tiles; 8192 -> 1024 14 against 19), at 16 the
+    // tiles split along the contraction are (8192 -> 8192: 35 against 37).
+    // Ragged groups stay with the tiles, which stream 32 groups' weights at
+    // 5.6 TB/s with one token or 16 in each.
+    const bool few = kind == kLinFwd && !g.offsets && !g.z8.codes && dma_ok(g, kind);
+    if (few && ((pin == kPathAuto && g.T <= 8) || (pin == kPathFew && g.T <= kFewTokens))) {
+        p.path = kPathFew;
+        return p;
+    }
     const int64_t tmid = tiles_of<CfgMid>(g, kind);
     if (dma_ok(g, kind) && pin != kPathGeneral) p.path = t256 >= 2 * kCUs ? kPath256 : tmid >= kCUs ? kPathMid : kPath128;
     if (p.path != kPathGeneral && (pin == kPath128 || pin == kPathMid || pin == kPath256)) p.path = (int)pin;

@@ -227,6 +227,21 @@ def test_forward_forms(case, path, split):
         _forward_case(*case)
 
 
+@pytest.mark.parametrize("case", [
+    (1, 8, 8, None, "none", True, True, True, 0, 0, 0),
+    (9, 2056, 24, None, "gelu", True, False, False, 0, 8, 8),
+    (13, 1000, 1032, None, "silu", True, True, True, 0, 0, 0),
+    (16, 4104, 40, None, "relu", True, True, False, 0, 0, 0),
+    (8, 136, 16400, None, "none", False, False, False, 0, 0, 0),
+    (5, 99, 75, None, "silu", True, True, True, 0, 3, 1),       # not 16-byte rows: another form takes it
+], ids=lambda c: "-".join(map(str, c)))
+def test_forward_of_few_tokens(case):
+    ve = _ve()
+    print(f"[gpu] forward of few tokens {case}", flush=True)
+    with ve.options(linear_path=5):
+        _forward_case(*case)
+
+
 def test_forward_residual_in_place_and_repeat():
     import torch
     ve = _ve()
