@@ -233,8 +233,8 @@ ve_status ve_dbuffer_group_op(const ve_plan* plan, int32_t rank, int32_t op, flo
  *       results, slower; needs "wg_dynamic" and no pinned shape);
  *   "linear_path" (VE_LINEAR_PATH, 0): pin the form of the linear layer's
  *       products where it applies: 1 = register staged (any alignment), 2 /
- *       3 / 4 = direct-to-LDS tiles of 128 x 128, 128 x 256, 256 x 256, 5 =
- *       the forward form for few tokens; 0 = chosen by shape;
+ *       3 = direct-to-LDS tiles of 128 x 128 / 256 x 256, 4 = the forward
+ *       form for few tokens; 0 = chosen by shape;
  *   "linear_split" (VE_LINEAR_SPLIT, 1): 0 = never cut their contraction
  *       into slices (the options must not change between a workspace query
  *       and the call it is for).

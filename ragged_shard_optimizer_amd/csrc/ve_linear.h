@@ -18,7 +18,7 @@ namespace ve {
 enum LinKind : int { kLinFwd = 0, kLinDx = 1, kLinDw = 2 };
 
 // Tile forms of the product kernel (option "linear_path" pins one).
-enum LinPath : int { kPathAuto = 0, kPathGeneral = 1, kPath128 = 2, kPathMid = 3, kPath256 = 4, kPathFew = 5 };
+enum LinPath : int { kPathAuto = 0, kPathGeneral = 1, kPath128 = 2, kPath256 = 3, kPathFew = 4 };
 
 struct LinArgs {
     const uint16_t* A; int64_t lda;           // x, dz, dz
@@ -40,6 +40,7 @@ struct LinArgs {
     // 16-byte accesses allowed on rows of these
     bool vec_bias, vec_res, vec_y, vec_z, vec_z8, vec_dw;
     // set by the launcher
+    int32_t finish;                           // which epilogue
     int32_t tiles_n, ksplit;
     int64_t tiles;                            // tiles of the launch (an upper bound when the rows are ragged)
     float* partial;                           // [slice][tile][BM x BN] fp32 when ksplit > 1

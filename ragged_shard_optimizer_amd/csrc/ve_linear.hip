@@ -45,7 +45,8 @@ constexpr int kCUs = 256;
 constexpr int kFewTokens = 16;  // rows of the few-token form
 constexpr int BK = 64;          // contraction step
 
-// Workgroup tile BM x BN of four waves of WM x WN; two LDS stages.
+// Workgroup tile BM x BN of four waves of WM x WN; two LDS stages of operands
+// and 16 rows of output a wave.
 template <int BM_, int BN_, int WM_, int WN_>
 struct LinCfg {
     static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_;
@@ -53,14 +54,15 @@ struct LinCfg {
     static constexpr int THREADS = 64 * WAVES;
     static constexpr int TM = WM / 32, TN = WN / 32;
     static constexpr int A_ELEMS = BM * BK, B_ELEMS = BN * BK, STAGE_ELEMS = A_ELEMS + B_ELEMS;
-    static constexpr int SMEM = 2 * STAGE_ELEMS * 2;
+    static constexpr int STAGES_BYTES = 2 * STAGE_ELEMS * 2;
+    static constexpr int OUT_BYTES = 16 * WN * 4;  // a wave's 16 output rows, fp32
+    static constexpr int SMEM = STAGES_BYTES + WAVES * OUT_BYTES;
     static_assert(SMEM <= 160 * 1024, "LDS");
     static constexpr int PER_CU = 160 * 1024 / SMEM;
 };
 using Cfg256 = LinCfg<256, 256, 128, 128>;
-using CfgMid = LinCfg<128, 256, 64, 128>;
 using Cfg128 = LinCfg<128, 128, 64, 64>;
-using CfgGen = LinCfg<128, 128, 32, 128>;
+using Cfg128W = LinCfg<128, 128, 32, 128>;  // a wave holds whole runs of 128 columns
 
 // s_waitcnt operands: at most n vector-memory operations outstanding; every
 // vector-memory and LDS operation complete.
@@ -73,6 +75,13 @@ constexpr int kWaitAll = 0x0070;
 __device__ __forceinline__ s16x4 read_tr(const VE_LDS uint16_t* __restrict__ p) {
     return __builtin_amdgcn_ds_read_tr16_b64_v4i16((s16x4 VE_LDS*)p);
 }
+
+// A scalar in lane `at` of a vector register.
+__device__ __forceinline__ void put_lane(uint32_t& v, int at, uint32_t x) { v = (int)(threadIdx.x & 63) == at ? x : v; }
+
+// ... and back (unsigned: the builtin's signed result would fill the upper
+// half of an address with its sign).
+__device__ __forceinline__ uint32_t get_lane(uint32_t v, int at) { return (uint32_t)__builtin_amdgcn_readlane((int)v, at); }
 
 // One operand of the workgroup's tile: ROWS tile rows (KC) or columns (KS)
 // over the contraction.  The tile of one step is ROWS * 128 bytes, filled in
@@ -87,7 +96,7 @@ struct Operand {
     const uint16_t* base;  // KC: row 0, contraction index 0 of the tile; KS: contraction row 0, column 0
     int64_t ld;
     int valid;             // KC: rows; KS: columns (from the tile's first on)
-    int64_t kc;            // contraction length
+    int kc;                // contraction length
     bool vec;              // !DMA: rows allow 16-byte loads
     int lrow, chunk, wave;
     uint32_t voff, step_off;
@@ -103,7 +112,7 @@ struct Operand {
     __device__ static __forceinline__ int place(int s) { return (s & ~7) | ((s & 1) << 2) | ((s >> 1) & 3); }
     __device__ static __forceinline__ int unplace(int f) { return (f & ~7) | ((f & 3) << 1) | ((f >> 2) & 1); }
 
-    __device__ __forceinline__ void init(const uint16_t* base_, int64_t ld_, int valid_, int64_t kc_, bool vec_, int lane,
+    __device__ __forceinline__ void init(const uint16_t* base_, int64_t ld_, int valid_, int kc_, bool vec_, int lane,
                                          int wave_) {
         base = base_; ld = ld_; valid = valid_; kc = kc_; vec = vec_; wave = wave_;
         const int slot = lane % SLOTS, row0 = wave * LROWS + lane / SLOTS;  // row of piece 0
@@ -121,12 +130,33 @@ struct Operand {
     // step's first element on: reads past the last valid row return 0, and so
     // do those of a KC row past the contraction (sent past the end by hand)
     // and every read of a step past the last (kt >= nk).
-    __device__ __forceinline__ void begin(int64_t kt, bool live) {
-        const int64_t k0 = kt * BK;
-        const uint16_t* p = KS ? base + k0 * ld : base + k0;
-        const int64_t rows = KS ? (kc - k0 < BK ? kc - k0 : BK) : valid;
-        const uint32_t bytes = live ? (uint32_t)(((rows - 1) * ld + (KS ? valid : kc - k0)) * 2) : 0u;
-        rs = __builtin_amdgcn_make_buffer_rsrc((void*)p, (short)0, (int)bytes, 0x00020000);
+    // base, valid and kc in five lanes of a vector register, and back
+    __device__ __forceinline__ void stash(uint32_t& keep, int at) const {
+        put_lane(keep, at, (uint32_t)(uintptr_t)base);
+        put_lane(keep, at + 1, (uint32_t)((uintptr_t)base >> 32));
+        put_lane(keep, at + 2, (uint32_t)valid);
+        put_lane(keep, at + 3, (uint32_t)kc);
+        put_lane(keep, at + 4, (uint32_t)ld);
+    }
+    __device__ __forceinline__ void unstash(uint32_t keep, int at) {
+        const uint64_t lo = get_lane(keep, at), hi = get_lane(keep, at + 1);
+        base = (const uint16_t*)(uintptr_t)((hi << 32) | lo);
+        valid = (int)get_lane(keep, at + 2);
+        kc = (int)get_lane(keep, at + 3);
+        ld = (int)get_lane(keep, at + 4);
+    }
+    __device__ __forceinline__ void make_uniform() {
+        base = (const uint16_t*)uniform64((int64_t)base);
+        ld = __builtin_amdgcn_readfirstlane((int)ld);
+        valid = __builtin_amdgcn_readfirstlane(valid);
+        kc = __builtin_amdgcn_readfirstlane(kc);
+    }
+    __device__ __forceinline__ void begin(int kt, bool live) {
+        const int k0 = kt * BK, l = (int)ld;
+        const uint16_t* p = KS ? base + (int64_t)k0 * l : base + k0;
+        const int rows = KS ? min(kc - k0, BK) : valid;
+        const int bytes = live ? ((rows - 1) * l + (KS ? valid : kc - k0)) * 2 : 0;
+        rs = __builtin_amdgcn_make_buffer_rsrc((void*)p, (short)0, bytes, 0x00020000);
         step_off = KS || k0 + chunk * 8 < kc ? voff : 0x80000000u;
     }
     __device__ __forceinline__ void piece(uint16_t* st, int q) {
@@ -134,8 +164,8 @@ struct Operand {
         __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (void VE_LDS*)(st + (WAVES * q + wave) * 512), 16, (int)v, 0, 0, 0);
     }
     // Step kt's tile into registers (put() then writes them to LDS).
-    __device__ __forceinline__ void get(int64_t kt) {
-        const int64_t k0 = kt * BK;
+    __device__ __forceinline__ void get(int kt) {
+        const int64_t k0 = (int64_t)kt * BK;
         if constexpr (!DMA) {
 #pragma unroll
             for (int q = 0; q < PIECES; ++q) {
@@ -175,58 +205,103 @@ struct Operand {
     }
 };
 
-// Where a workgroup's tile lies.
-struct TileAt {
+// One work item: an output tile, or a slice of one's contraction.
+struct Work {
     int e;
-    int64_t row0, rows;     // first output row (a token, or a dw row), rows of the tile that exist
-    int64_t col0;
-    int64_t begin, len;     // the group's tokens
+    int row0;        // first output row (a token, or a dw row)
+    int rows;        // rows of the tile that exist (0: nothing to do)
+    int col0;
+    int begin, len;  // the group's tokens
+    int kbeg, nk;    // contraction steps of this item
+    int slice;
+    uint32_t t;      // tile
 };
 
-// Tile t of the sequence (group by group; inside a group in bands of 8 tile
-// rows, column by column, so that consecutive tiles share panels).
+// Tile `in` of a group's tm x tiles_n tiles: bands of 8 tile rows, column by
+// column, so that consecutive tiles share operand panels.
+template <class CF>
+__device__ __forceinline__ void tile_in(const LinArgs& g, uint32_t in, int tm, int& ti, int& tj) {
+    constexpr uint32_t kBand = 8;
+    const uint32_t per = kBand * g.tiles_n, band = in / per, first = band * kBand;
+    const uint32_t rows = min((uint32_t)tm - first, kBand), r = in - band * per;
+    tj = (int)(r / rows);
+    ti = (int)(first + r - tj * rows);
+}
+
+// Tile t of a product (kLinDw: of group e): where it lies.
 template <class CF, int KIND>
-__device__ __forceinline__ bool tile_of(const LinArgs& g, int64_t t, TileAt& at) {
-    int64_t in;  // index inside the group
-    int tm;
+__device__ __forceinline__ bool tile_at(const LinArgs& g, uint32_t t, int e, Work& w) {
+    int tm, ti, tj;
+    uint32_t in = t;
+    w.t = t;
+    w.e = e;
+    w.begin = 0;
+    w.len = (int)g.T;
     if constexpr (KIND == kLinDw) {
         tm = (int)((g.M + CF::BM - 1) / CF::BM);
-        const int64_t per = (int64_t)tm * g.tiles_n;
-        at.e = (int)(t / per);
-        in = t - at.e * per;
-        at.begin = 0;
-        at.len = g.T;
         if (g.offsets) {
-            group_rows(g.offsets, at.e, g.T, at.begin, at.len);
-            at.begin = uniform64(at.begin);
-            at.len = uniform64(at.len);
+            int64_t begin, len;
+            group_rows(g.offsets, e, g.T, begin, len);
+            w.begin = __builtin_amdgcn_readfirstlane((int)begin);
+            w.len = __builtin_amdgcn_readfirstlane((int)len);
+        }
+    } else if (g.offsets) {
+        RaggedGroup r;
+        if (!ragged_find(g.offsets, g.E, g.T, CF::BM, t, g.tiles_n, r)) return false;
+        w.e = r.e;
+        w.begin = (int)r.begin;
+        w.len = (int)r.len;
+        tm = r.tiles;
+        in = t - (uint32_t)r.before * g.tiles_n;
+    } else {
+        tm = (int)((g.T + CF::BM - 1) / CF::BM);
+    }
+    tile_in<CF>(g, in, tm, ti, tj);
+    w.col0 = tj * CF::BN;
+    const int i0 = ti * CF::BM, all = KIND == kLinDw ? (int)g.M : w.len;
+    w.rows = min(all - i0, CF::BM);
+    w.row0 = KIND == kLinDw ? i0 : w.begin + i0;
+    return true;
+}
+
+// Item i of the launch; false: there is none, nor any later one of this
+// workgroup (workgroup b takes items b, b + gridDim.x, ...).  Workgroups go
+// round-robin over the 8 XCDs, each with its own L2, so item i belongs to
+// XCD i % 8 and each XCD takes a contiguous run of the tile sequence; in
+// kLinDw of every group's tiles, because groups differ in length.
+template <class CF, int KIND>
+__device__ __forceinline__ bool fetch(const LinArgs& g, uint32_t total, uint32_t i, Work& w) {
+    uint32_t t;
+    int e = 0;
+    w.slice = 0;
+    if (g.ksplit > 1) {
+        t = i / (uint32_t)g.ksplit;
+        w.slice = (int)(i - t * g.ksplit);
+        if (t >= total) return false;
+    } else if (KIND == kLinDw) {
+        const uint32_t in_e = total / (uint32_t)g.E, part = (in_e + 7) / 8, j = i / 8;
+        e = (int)(j / part);
+        if (e >= g.E) return false;
+        t = (i % 8) * part + j - e * part;
+        if (t >= in_e) {  // a hole: the run of this XCD is shorter
+            w.rows = 0;
+            w.nk = 0;
+            return true;
         }
     } else {
-        if (g.offsets) {
-            RaggedGroup r;
-            if (!ragged_find(g.offsets, g.E, g.T, CF::BM, t, g.tiles_n, r)) return false;
-            at.e = r.e;
-            at.begin = r.begin;
-            at.len = r.len;
-            tm = r.tiles;
-            in = t - (int64_t)r.before * g.tiles_n;
-        } else {
-            at.e = 0;
-            at.begin = 0;
-            at.len = g.T;
-            tm = (int)((g.T + CF::BM - 1) / CF::BM);
-            in = t;
-            if (t >= (int64_t)tm * g.tiles_n) return false;
-        }
+        const uint32_t part = (total + 7) / 8, j = i / 8;
+        t = (i % 8) * part + j;
+        if (j >= part || t >= total) return false;
     }
-    constexpr int kBand = 8;
-    const int i = (int)in, per_band = kBand * g.tiles_n;
-    const int first = (i / per_band) * kBand, rows = min(tm - first, kBand), r = i % per_band;
-    const int ti = first + r % rows, tj = r / rows;
-    at.col0 = (int64_t)tj * CF::BN;
-    const int64_t i0 = (int64_t)ti * CF::BM, all = KIND == kLinDw ? g.M : at.len;
-    at.rows = all - i0 < CF::BM ? all - i0 : CF::BM;
-    at.row0 = KIND == kLinDw ? i0 : at.begin + i0;
+    if (!tile_at<CF, KIND>(g, t, e, w)) return false;
+    const int K = KIND == kLinDw ? w.len : (int)g.K;
+    w.kbeg = 0;
+    w.nk = (int)(((uint32_t)K + BK - 1) / BK);
+    if (g.ksplit > 1) {
+        const int per = (w.nk + g.ksplit - 1) / g.ksplit;
+        w.kbeg = min(w.slice * per, w.nk);
+        w.nk = min(per, w.nk - w.kbeg);
+    }
     return true;
 }
 
@@ -243,6 +318,22 @@ __device__ __forceinline__ void bias8(const LinArgs& g, int e, int64_t col, int 
         widen8(load_bf16x8(g.bias + (int64_t)e * g.bias_group + col, cnt, g.vec_bias), o);
 #pragma unroll
         for (int t = 0; t < 8; ++t) v[t] += o[t];
+    }
+}
+
+// the switch outside the loop over the values
+__device__ __forceinline__ void activate8(int act, float* v) {
+    switch (act) {
+#define VE_ACT_CASE(A)                                   \
+    case A:                                              \
+        _Pragma("unroll") for (int t = 0; t < 8; ++t) v[t] = activate(A, v[t]); \
+        break;
+        VE_ACT_CASE(VE_ACT_RELU)
+        VE_ACT_CASE(VE_ACT_GELU)
+        VE_ACT_CASE(VE_ACT_GELU_TANH)
+        VE_ACT_CASE(VE_ACT_SILU)
+#undef VE_ACT_CASE
+    default: break;
     }
 }
 
@@ -292,10 +383,7 @@ __device__ __forceinline__ void finish8(const LinArgs& g, int e, int64_t row, in
                 const uint32_t run = (uint32_t)col >> __builtin_ctz(g.z8.block);
                 if (((uint32_t)col & (g.z8.block - 1)) == 0) g.z8.scales[row * g.z8.ld_scales + run] = c.scale;
             }
-            if (g.act != VE_ACT_NONE) {
-#pragma unroll
-                for (int t = 0; t < 8; ++t) v[t] = activate(g.act, v[t]);
-            }
+            activate8(g.act, v);
         }
         if (g.res) {
             float o[8];
@@ -307,76 +395,267 @@ __device__ __forceinline__ void finish8(const LinArgs& g, int e, int64_t row, in
     }
 }
 
-// One tile (and slice of the contraction).  DMA: operands go straight from
-// memory to LDS (16-byte rows, no ragged ends inside 16 bytes); else through
-// registers, from any alignment.
-template <class CF, int KIND, bool DMA>
+// The operands of one work item.
+template <class CF, int KIND, class OpA, class OpB>
+__device__ __forceinline__ void set_operands(const LinArgs& g, const Work& w, OpA& A, OpB& B, int lane, int wave) {
+    const int K = KIND == kLinDw ? w.len : (int)g.K, cols = min((int)g.N - w.col0, CF::BN);
+    const bool va = g.lda % 8 == 0 && ((uintptr_t)g.A & 15) == 0;
+    const bool vb = g.ldb % 8 == 0 && ((uintptr_t)g.B & 15) == 0 && g.b_group % 8 == 0;
+    if constexpr (KIND == kLinDw) A.init(g.A + w.begin * g.lda + w.row0, g.lda, w.rows, K, va, lane, wave);
+    else A.init(g.A + w.row0 * g.lda, g.lda, w.rows, K, va, lane, wave);
+    if constexpr (KIND == kLinFwd) B.init(g.B + w.e * g.b_group + w.col0 * g.ldb, g.ldb, cols, K, vb, lane, wave);
+    else if constexpr (KIND == kLinDx) B.init(g.B + w.e * g.b_group + w.col0, g.ldb, cols, K, vb, lane, wave);
+    else B.init(g.B + w.begin * g.ldb + w.col0, g.ldb, cols, K, vb, lane, wave);
+}
+
+// The kernel's arguments, read from memory again.
+__device__ __forceinline__ LinArgs args_again() {
+    auto p = (const __attribute__((address_space(4))) uint32_t*)__builtin_amdgcn_kernarg_segment_ptr();
+    asm volatile("" : "+s"(p));
+    static_assert(sizeof(LinArgs) % 4 == 0, "whole words");
+    uint32_t w[sizeof(LinArgs) / 4];
+#pragma unroll
+    for (int i = 0; i < (int)(sizeof(LinArgs) / 4); ++i) w[i] = p[i];
+    LinArgs h;
+    __builtin_memcpy(&h, w, sizeof(h));
+    return h;
+}
+
+// What the epilogue of a launch has to do, as cases that each get their own
+// loop: one store of bf16, for tokens after bias and residual; activation and
+// saving too (both with 16-byte rows and 32-bit offsets from a wave's first
+// row); everything.
+enum Finish : int { kFinishAll, kFinishStore, kFinishSave };
+
+// Epilogue of one item.  Each wave passes its accumulators through its own
+// 16 rows of LDS (no barrier between the waves), so that a lane gets 8
+// consecutive columns and WN / 8 lanes a whole row of the wave's tile:
+// 16-byte accesses, and runs saved in 8 bits are neighbouring lanes.  A row's
+// 16-byte chunks lie even ones first, then odd ones, permuted by the row: a
+// write (16 rows of two chunks) and a read (the even, then the odd chunks of
+// a row) touch distinct banks.
+template <class CF, int KIND, int FIN>
+__device__ __forceinline__ void epilogue_of(const Work& w, f32x16 (&acc)[CF::TM][CF::TN],
+                                            unsigned char* sw, int wr, int wc, int lane) {
+    constexpr int TM = CF::TM, TN = CF::TN, WM = CF::WM, WN = CF::WN, CPR = WN / 8, ROWB = WN * 4;
+    constexpr int RI = 64 / CPR, IT = 16 / RI;  // rows of one iteration, iterations of 16 rows
+    const LinArgs g = args_again();
+    const int c8 = lane % CPR, r0 = lane / CPR, cc = wc * WN + c8 * 8;  // the lane's columns and first row
+    const int cnt0 = min(max(min((int)g.N - w.col0, CF::BN) - cc, 0), 8);
+    const int64_t first = (int64_t)w.row0 + wr * WM, col = w.col0 + cc;
+    float bias[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    bias8<KIND>(g, w.e, col, cnt0, bias);
+    // byte offsets of the lane from the wave's first row
+    const int ldo = KIND == kLinDw ? (int)g.lddw : (int)g.ldy;
+    uint16_t* out = KIND == kLinDw ? (uint16_t*)g.dw + w.e * g.dw_group + first * g.lddw : g.y + first * g.ldy;
+    uint32_t o_off = (uint32_t)(r0 * ldo + (int)col) * 2;
+    const bool res = KIND != kLinDw && g.res;
+    const uint16_t* rin = res ? g.res + first * g.ldr : nullptr;
+    uint32_t r_off = (uint32_t)(r0 * (int)g.ldr + (int)col) * 2;
+    int ldc = 0, lds = 0, shift = 0;
+    uint32_t c_off = 0, s_off = 0, z_off = 0;
+    VE_GLOBAL char *codes = nullptr, *scales = nullptr, *zout = nullptr;
+    if constexpr (FIN == kFinishSave) {
+        if (g.z8.codes) {
+            ldc = (int)g.z8.ld_codes;
+            lds = (int)g.z8.ld_scales;
+            shift = __builtin_ctz(g.z8.block);
+            codes = (VE_GLOBAL char*)(g.z8.codes + first * ldc);
+            scales = (VE_GLOBAL char*)(g.z8.scales + first * lds);
+            c_off = (uint32_t)(r0 * ldc + (int)col);
+            s_off = (uint32_t)(r0 * lds + ((int)col >> shift)) * 4;
+        }
+        if (g.z) {
+            zout = (VE_GLOBAL char*)(g.z + first * g.ldz);
+            z_off = (uint32_t)(r0 * (int)g.ldz + (int)col) * 2;
+        }
+    }
+    const bool run_first = ((int)col & (g.z8.block - 1)) == 0;
+#pragma unroll 1
+    for (int pass = 0; pass < 2 * TM; ++pass) {
+        const int left = w.rows - wr * WM - pass * 16 - r0;  // rows from the lane's first on
+        u32x4 rv[IT];
+        if (FIN != kFinishAll && res) {
+#pragma unroll
+            for (int i = 0; i < IT; ++i) {
+                rv[i] = u32x4{0, 0, 0, 0};
+                if (left > RI * i && cnt0 > 0)
+                    rv[i] = *(const VE_GLOBAL u32x4*)((const VE_GLOBAL char*)rin + (r_off + (uint32_t)(RI * i * (int)g.ldr * 2)));
+            }
+        }
+        __builtin_amdgcn_wave_barrier();
+#pragma unroll
+        for (int a = 0; a < TM; ++a)
+            if (a == pass >> 1 && ((lane >> 4) & 1) == (pass & 1)) {
+#pragma unroll
+                for (int b = 0; b < TN; ++b)
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const int r = lane & 15, c = ((4 * b + q) ^ (r & (CPR - 1))) + CPR * (lane >> 5);
+                        *(f32x4*)(sw + r * ROWB + c * 16) =
+                            f32x4{acc[a][b][4 * q], acc[a][b][4 * q + 1], acc[a][b][4 * q + 2], acc[a][b][4 * q + 3]};
+                    }
+            }
+        __builtin_amdgcn_wave_barrier();
+        float v[IT][8];
+#pragma unroll
+        for (int i = 0; i < IT; ++i) {
+            const int r = r0 + RI * i;
+            const unsigned char* src = sw + r * ROWB + (c8 ^ (r & (CPR - 1))) * 16;
+            *(f32x4*)&v[i][0] = *(const f32x4*)src;
+            *(f32x4*)&v[i][4] = *(const f32x4*)(src + CPR * 16);
+        }
+        if constexpr (FIN != kFinishAll) {
+#pragma unroll
+            for (int i = 0; i < IT; ++i) {
+                const bool in = left > RI * i && cnt0 > 0;
+                if constexpr (KIND == kLinFwd) {
+#pragma unroll
+                    for (int t = 0; t < 8; ++t) v[i][t] += bias[t];
+                }
+                if constexpr (FIN == kFinishSave) {
+                    if (zout && in)
+                        *(VE_GLOBAL u32x4*)(zout + (z_off + (uint32_t)(RI * i * (int)g.ldz * 2))) = narrow8(v[i]);
+                    if (codes) {
+                        // columns past the last are 0: nothing was loaded for them, and their bias is 0
+                        const RunCode c = run_code(__uint_as_float(amax_lanes(amax8(v[i], 8), g.z8.block / 8)));
+                        const u32x2 q = encode8(c, v[i]);
+                        if (in) {
+                            *(VE_GLOBAL u32x2*)(codes + (c_off + (uint32_t)(RI * i * ldc))) = q;
+                            if (run_first) *(VE_GLOBAL float*)(scales + (s_off + (uint32_t)(RI * i * lds * 4))) = c.scale;
+                        }
+                    }
+                    activate8(g.act, v[i]);
+                }
+                if (res) {
+                    float o[8];
+                    widen8(rv[i], o);
+#pragma unroll
+                    for (int t = 0; t < 8; ++t) v[i][t] += o[t];
+                }
+                if (in)
+                    *(VE_GLOBAL u32x4*)((VE_GLOBAL char*)out + (o_off + (uint32_t)(RI * i * ldo * 2))) = narrow8(v[i]);
+            }
+            o_off += (uint32_t)(16 * ldo * 2);
+            r_off += (uint32_t)(16 * (int)g.ldr * 2);
+            c_off += (uint32_t)(16 * ldc);
+            s_off += (uint32_t)(16 * lds * 4);
+            z_off += (uint32_t)(16 * (int)g.ldz * 2);
+        } else {
+#pragma unroll
+            for (int i = 0; i < IT; ++i) {
+                const int rr = pass * 16 + r0 + RI * i;  // row of the wave's tile
+                if (g.ksplit > 1) {
+                    float* o = g.partial + ((int64_t)w.slice * g.tiles + w.t) * (CF::BM * CF::BN) + (wr * WM + rr) * CF::BN + cc;
+                    *(f32x4*)o = *(const f32x4*)&v[i][0];
+                    *(f32x4*)(o + 4) = *(const f32x4*)&v[i][4];
+                    continue;
+                }
+                const int cnt = left > RI * i ? cnt0 : 0;
+#pragma unroll
+                for (int t = 0; t < 8; ++t) v[i][t] += bias[t];
+                uint32_t m = 0;
+                if (KIND == kLinFwd && g.z8.codes) m = amax_lanes(amax8(v[i], cnt), g.z8.block / 8);
+                finish8<KIND>(g, w.e, first + rr, col, cnt, v[i], m);
+            }
+        }
+    }
+}
+
+template <class CF, int KIND>
+__device__ __forceinline__ void epilogue(int finish, const Work& w, f32x16 (&acc)[CF::TM][CF::TN], unsigned char* sw,
+                                         int wr, int wc, int lane) {
+    if (finish == kFinishStore) epilogue_of<CF, KIND, kFinishStore>(w, acc, sw, wr, wc, lane);
+    else if (KIND == kLinFwd && finish == kFinishSave) epilogue_of<CF, KIND, kFinishSave>(w, acc, sw, wr, wc, lane);
+    else epilogue_of<CF, KIND, kFinishAll>(w, acc, sw, wr, wc, lane);
+}
+
+template <class CF, int KIND>
+__device__ __forceinline__ uint32_t all_tiles(const LinArgs& g) {
+    if (KIND != kLinDw && g.offsets)
+        return (uint32_t)min(g.tiles, (int64_t)ragged_total(g.offsets, g.E, g.T, CF::BM) * g.tiles_n);
+    return (uint32_t)g.tiles;
+}
+
+// Work items with direct loads (16-byte operand rows, no ragged ends inside
+// 16 bytes).  A workgroup stays on its CU and takes one item after the other;
+// the steps of all its items are one stream, which the loads run up to two
+// steps ahead of, so that an item's first loads land during the previous
+// item's last step and epilogue.  (With one workgroup an item, its start and
+// epilogue cost 10 us of a 256 x 256 tile, as much as 7 steps.)
+template <class CF, int KIND>
 __global__ void __launch_bounds__(CF::THREADS, CF::PER_CU) k_product(LinArgs g) {
     constexpr int TM = CF::TM, TN = CF::TN, WM = CF::WM, WN = CF::WN;
-    constexpr bool AKS = KIND == kLinDw, BKS = KIND != kLinFwd;
+    constexpr int NF = TM + TN, MM = TM * TN, H = MM / 2;
     __shared__ __attribute__((aligned(1024))) unsigned char smem[CF::SMEM];
-    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
     const int wr = wave / CF::WAVES_N, wc = wave % CF::WAVES_N;
-
-    // tile and slice: workgroups go round-robin over the 8 XCDs, each with
-    // its own L2, so each XCD takes a contiguous run of the tile sequence
-    int64_t t = blockIdx.x;
-    int slice = 0;
-    if (g.ksplit > 1) {
-        slice = (int)(t % g.ksplit);
-        t /= g.ksplit;
-    } else {
-        int64_t total = g.tiles;
-        if (KIND != kLinDw && g.offsets)
-            total = min(total, (int64_t)ragged_total(g.offsets, g.E, g.T, CF::BM) * g.tiles_n);
-        const int64_t per = (total + 7) / 8;
-        if (t / 8 >= per) return;
-        t = (t % 8) * per + t / 8;
-        if (t >= total) return;
-    }
-    TileAt at;
-    if (!tile_of<CF, KIND>(g, t, at)) return;
-
     uint16_t* ops = (uint16_t*)smem;
-    Operand<AKS, CF::BM, CF::WAVES, DMA> A;
-    Operand<BKS, CF::BN, CF::WAVES, DMA> B;
-    const int64_t K = KIND == kLinDw ? at.len : g.K;
-    const int cols = (int)(g.N - at.col0 < CF::BN ? g.N - at.col0 : CF::BN);
-    if constexpr (AKS) A.init(g.A + at.begin * g.lda + at.row0, g.lda, (int)at.rows, K, g.lda % 8 == 0 && ((uintptr_t)g.A & 15) == 0, lane, wave);
-    else A.init(g.A + at.row0 * g.lda, g.lda, (int)at.rows, K, g.lda % 8 == 0 && ((uintptr_t)g.A & 15) == 0, lane, wave);
-    const bool vb = g.ldb % 8 == 0 && ((uintptr_t)g.B & 15) == 0 && g.b_group % 8 == 0;
-    if constexpr (KIND == kLinFwd) B.init(g.B + at.e * g.b_group + at.col0 * g.ldb, g.ldb, cols, K, vb, lane, wave);
-    else if constexpr (KIND == kLinDx) B.init(g.B + at.e * g.b_group + at.col0, g.ldb, cols, K, vb, lane, wave);
-    else B.init(g.B + at.begin * g.ldb + at.col0, g.ldb, cols, K, vb, lane, wave);
+    unsigned char* sw = smem + CF::STAGES_BYTES + wave * CF::OUT_BYTES;
+    auto stage = [&](uint32_t s) { return ops + (s & 1) * CF::STAGE_ELEMS; };
 
-    f32x16 acc[TM][TN];
-#pragma unroll
-    for (int a = 0; a < TM; ++a)
-#pragma unroll
-        for (int b = 0; b < TN; ++b)
-#pragma unroll
-            for (int r = 0; r < 16; ++r) acc[a][b][r] = 0.f;
+    const uint32_t total = all_tiles<CF, KIND>(g);
+    uint32_t ci = blockIdx.x, li = ci;  // items computed and loaded
+    Work cw;
+    bool cok = fetch<CF, KIND>(g, total, ci, cw);
+    if (!cok) return;
+    Operand<KIND == kLinDw, CF::BM, CF::WAVES, true> A;
+    Operand<KIND != kLinFwd, CF::BN, CF::WAVES, true> B;
+    using OpA = decltype(A);
+    using OpB = decltype(B);
+    constexpr int PA = OpA::PIECES, PB = OpB::PIECES, P = PA + PB, SPAN = 2 * MM;
+    static_assert(SPAN <= H + 3 * MM, "loads of a step must be issued before its barrier");
 
-    int64_t kbeg = 0, nk = (K + BK - 1) / BK;
-    if (g.ksplit > 1) {
-        const int64_t per = (nk + g.ksplit - 1) / g.ksplit;
-        kbeg = min(slice * per, nk);
-        nk = min(per, nk - kbeg);
-    }
-    auto stage = [&](int64_t kt) { return ops + (int)(kt & 1) * CF::STAGE_ELEMS; };
-    // this wave's loads and LDS accesses are complete, then everyone's: a
-    // bare barrier, with the LDS accesses pinned around it
-    auto ready = [&]() {
-        __builtin_amdgcn_s_waitcnt(kWaitAll);
+    // The loads' position: step lk of the item's steps up to lend; lok: there
+    // is an item.  The arguments are read anew for each item (through a
+    // pointer the compiler cannot see through), so that they do not occupy
+    // scalar registers in between.
+    int lk = 0, lend = 0;
+    bool lok = true;
+    auto next_loaded = [&](bool first) {  // the next item with steps
+        const LinArgs h = args_again();
+        Work w;
+        do {
+            if (!first) li += gridDim.x;
+            first = false;
+            lok = __builtin_amdgcn_readfirstlane(fetch<CF, KIND>(h, total, li, w)) != 0;
+            w.nk = __builtin_amdgcn_readfirstlane(w.nk);
+        } while (lok && w.nk == 0);
+        if (!lok) return;
+        lk = __builtin_amdgcn_readfirstlane(w.kbeg);
+        lend = __builtin_amdgcn_readfirstlane(w.kbeg + w.nk);
+        set_operands<CF, KIND>(h, w, A, B, lane, wave);
+        A.make_uniform();
+        B.make_uniform();
+    };
+    auto begin = [&]() {
+        A.begin(lk, lok);
+        B.begin(lk, lok);
+    };
+    auto advance = [&]() {
+        if (lok && ++lk >= lend) next_loaded(false);
+    };
+    auto advance_inside = [&]() { ++lk; };
+    // the pieces of slot s (s MFMAs behind the barrier)
+    auto pieces = [&](int slot, uint32_t s) {
+#pragma unroll
+        for (int p = 0; p < P; ++p)
+            if (p * SPAN / P == slot) {
+                if (p < PA) A.piece(stage(s), p);
+                else B.piece(stage(s) + CF::A_ELEMS, p - PA);
+            }
+    };
+    auto barrier = [&]() {
         asm volatile("" ::: "memory");
         __builtin_amdgcn_s_barrier();
         asm volatile("" ::: "memory");
     };
+
+    f32x16 acc[TM][TN];
     bf16x8 fa[2][TM], fb[2][TN];
-    constexpr int NF = TM + TN, MM = TM * TN, H = MM / 2;
     // fragment f of sub-step kk in the order the MFMAs need them: A0, all B, the other A
-    auto frag1 = [&](int buf, int f, int kk, int64_t kt) {
-        const uint16_t* st = stage(kt);
+    auto frag1 = [&](int buf, int f, int kk, uint32_t s) {
+        const uint16_t* st = stage(s);
         if (f == 0 || f > TN) {
             const int a = f == 0 ? 0 : f - TN;
             fa[buf][a] = A.frag(st, wr * WM + a * 32, kk, lane);
@@ -388,156 +667,157 @@ __global__ void __launch_bounds__(CF::THREADS, CF::PER_CU) k_product(LinArgs g) 
         const int a = m / TN, b = m % TN;
         acc[a][b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fb[buf][b], fa[buf][a], acc[a][b], 0, 0, 0);
     };
-    if constexpr (DMA) {
+
+    A.init(g.A, g.lda, 1, 1, true, lane, wave);
+    B.init(g.B, g.ldb, 1, 1, true, lane, wave);
+    next_loaded(true);
+    begin();
+#pragma unroll
+    for (int q = 0; q < PA; ++q) A.piece(stage(0), q);
+#pragma unroll
+    for (int q = 0; q < PB; ++q) B.piece(stage(0) + CF::A_ELEMS, q);
+    __builtin_amdgcn_s_waitcnt(kWaitAll);
+    advance();
+    begin();
+#pragma unroll
+    for (int m = 0; m < H; ++m) pieces(m, 1);
+    barrier();
+#pragma unroll
+    for (int f = 0; f < NF; ++f) frag1(0, f, 0, 0);
+
+    uint32_t s = 0;  // steps computed, over all items
+    while (cok) {
+#pragma unroll
+        for (int a = 0; a < TM; ++a)
+#pragma unroll
+            for (int b = 0; b < TN; ++b)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) acc[a][b][r] = 0.f;
         // Every MFMA is followed by its share of what feeds the later ones,
         // in this order (the scheduling barriers keep it): the fragment
         // reads of the next sub-step, and direct loads.  In the middle of a
         // step's last sub-step all its reads are complete: the barrier there
         // frees its stage and makes the next one visible, and from there on
-        // the loads of step kt + 2 go out into the freed stage, spread evenly
-        // over two sub-steps: issued faster they stall the wave (all within
-        // half a sub-step: 1,207 TFLOP/s forward at 8192^3, one sub-step:
-        // 1,260), later they have less time to land (two and a half: 1,283;
-        // two: 1,306).
-        using OpA = decltype(A);
-        using OpB = decltype(B);
-        constexpr int PA = OpA::PIECES, PB = OpB::PIECES, P = PA + PB, SPAN = 2 * MM;
-        static_assert(SPAN <= H + 3 * MM, "loads of a step must be issued before its barrier");
-        auto begin = [&](int64_t kt) {
-            A.begin(kbeg + kt, kt < nk);
-            B.begin(kbeg + kt, kt < nk);
-        };
-        // the pieces of slot s (s MFMAs behind the barrier)
-        auto pieces = [&](int s, int64_t kt) {
+        // the loads of the step after the next go out into the freed stage,
+        // spread evenly over two sub-steps: issued faster they stall the
+        // wave (all within half a sub-step: 1,207 TFLOP/s forward at 8192^3,
+        // one sub-step: 1,260), later they have less time to land (two and a
+        // half: 1,283; two: 1,306).
+        auto step = [&](auto&& next) {
 #pragma unroll
-            for (int p = 0; p < P; ++p)
-                if (p * SPAN / P == s) {
-                    if (p < PA) A.piece(stage(kt), p);
-                    else B.piece(stage(kt) + CF::A_ELEMS, p - PA);
-                }
-        };
-        if (nk > 0) {
-            begin(0);
+            for (int kk = 0; kk < BK / 16 - 1; ++kk) {
 #pragma unroll
-            for (int q = 0; q < PA; ++q) A.piece(stage(0), q);
+                for (int m = 0; m < MM; ++m) {
+                    mfma(kk & 1, m);
 #pragma unroll
-            for (int q = 0; q < PB; ++q) B.piece(stage(0) + CF::A_ELEMS, q);
-            __builtin_amdgcn_s_waitcnt(kWaitAll);
-            begin(1);
-#pragma unroll
-            for (int s = 0; s < H; ++s) pieces(s, 1);
-            asm volatile("" ::: "memory");
-            __builtin_amdgcn_s_barrier();
-            asm volatile("" ::: "memory");
-#pragma unroll
-            for (int f = 0; f < NF; ++f) frag1(0, f, 0, 0);
-            for (int64_t kt = 0; kt < nk; ++kt) {
-#pragma unroll
-                for (int kk = 0; kk < BK / 16 - 1; ++kk) {
-#pragma unroll
-                    for (int m = 0; m < MM; ++m) {
-                        mfma(kk & 1, m);
-#pragma unroll
-                        for (int f = m * NF / MM; f < (m + 1) * NF / MM; ++f) frag1((kk + 1) & 1, f, kk + 1, kt);
-                        pieces(H + kk * MM + m, kt + 1);
-                        __builtin_amdgcn_sched_barrier(0);
-                    }
-                }
-#pragma unroll
-                for (int m = 0; m < H; ++m) mfma(1, m);
-                __builtin_amdgcn_sched_barrier(0);
-                ready();
-                begin(kt + 2);
-#pragma unroll
-                for (int m = H; m < MM; ++m) {
-                    mfma(1, m);
-#pragma unroll
-                    for (int f = (m - H) * NF / H; f < (m - H + 1) * NF / H; ++f) frag1(0, f, 0, kt + 1);
-                    pieces(m - H, kt + 2);
+                    for (int f = m * NF / MM; f < (m + 1) * NF / MM; ++f) frag1((kk + 1) & 1, f, kk + 1, s);
+                    pieces(H + kk * MM + m, s + 1);
                     __builtin_amdgcn_sched_barrier(0);
                 }
             }
-            // the loads past the last step (of nothing) land before the end
+            next();
+#pragma unroll
+            for (int m = 0; m < H; ++m) mfma(1, m);
+            __builtin_amdgcn_sched_barrier(0);
+            // this wave's loads and LDS reads are complete, then everyone's
             __builtin_amdgcn_s_waitcnt(kWaitAll);
-        }
-    } else if (nk > 0) {
-        auto get = [&](int64_t kt) {
-            A.get(kbeg + kt);
-            B.get(kbeg + kt);
+            barrier();
+            begin();
+#pragma unroll
+            for (int m = H; m < MM; ++m) {
+                mfma(1, m);
+#pragma unroll
+                for (int f = (m - H) * NF / H; f < (m - H + 1) * NF / H; ++f) frag1(0, f, 0, s + 1);
+                pieces(m - H, s + 2);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            ++s;
         };
-        auto put = [&](int64_t kt) {
-            A.put(stage(kt), lane);
-            B.put(stage(kt) + CF::A_ELEMS, lane);
-        };
+        // the loads leave this item behind in its last two steps
+        const int nk = __builtin_amdgcn_readfirstlane(cw.nk);
+        int kt = 0;
+        for (; kt + 2 < nk; ++kt) step(advance_inside);
+        for (; kt < nk; ++kt) step(advance);
+        // the loads' position waits in a vector register while the epilogue
+        // needs the scalar ones (left to the compiler, it keeps them there in
+        // the steps as well and fetches them back each time)
+        uint32_t keep = 0;
+        A.stash(keep, 0);
+        B.stash(keep, 5);
+        put_lane(keep, 10, (uint32_t)lk);
+        put_lane(keep, 11, (uint32_t)lend);
+        put_lane(keep, 12, (uint32_t)lok);
+        put_lane(keep, 13, li);
+        if (cw.rows > 0) epilogue<CF, KIND>(args_again().finish, cw, acc, sw, wr, wc, lane);
+        ci += gridDim.x;
+        cok = fetch<CF, KIND>(args_again(), total, ci, cw);
+        A.unstash(keep, 0);
+        B.unstash(keep, 5);
+        lk = (int)get_lane(keep, 10);
+        lend = (int)get_lane(keep, 11);
+        lok = get_lane(keep, 12) != 0;
+        li = get_lane(keep, 13);
+        begin();
+    }
+    // the loads past the last step (of nothing) land before the end
+    __builtin_amdgcn_s_waitcnt(kWaitAll);
+}
+
+// One item a workgroup, through registers: operands of any alignment.
+template <class CF, int KIND>
+__global__ void __launch_bounds__(CF::THREADS, CF::PER_CU) k_product_any(LinArgs g) {
+    constexpr int TM = CF::TM, TN = CF::TN, WM = CF::WM, WN = CF::WN;
+    __shared__ __attribute__((aligned(1024))) unsigned char smem[CF::SMEM];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+    const int wr = wave / CF::WAVES_N, wc = wave % CF::WAVES_N;
+    Work w;
+    if (!fetch<CF, KIND>(g, all_tiles<CF, KIND>(g), blockIdx.x, w) || w.rows == 0) return;
+    Operand<KIND == kLinDw, CF::BM, CF::WAVES, false> A;
+    Operand<KIND != kLinFwd, CF::BN, CF::WAVES, false> B;
+    set_operands<CF, KIND>(g, w, A, B, lane, wave);
+    f32x16 acc[TM][TN];
+#pragma unroll
+    for (int a = 0; a < TM; ++a)
+#pragma unroll
+        for (int b = 0; b < TN; ++b)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) acc[a][b][r] = 0.f;
+    auto stage = [&](int kt) { return (uint16_t*)smem + (kt & 1) * CF::STAGE_ELEMS; };
+    auto get = [&](int kt) {
+        A.get(w.kbeg + kt);
+        B.get(w.kbeg + kt);
+    };
+    auto put = [&](int kt) {
+        A.put(stage(kt), lane);
+        B.put(stage(kt) + CF::A_ELEMS, lane);
+    };
+    if (w.nk > 0) {
         get(0);
         put(0);
-        ready();
-        for (int64_t kt = 0; kt < nk; ++kt) {
-            // the next step's registers are loaded while this one computes,
-            // and written to the other stage, which everyone's reads left
-            // before the last barrier
-            if (kt + 1 < nk) get(kt + 1);
-#pragma unroll
-            for (int kk = 0; kk < BK / 16; ++kk) {
-#pragma unroll
-                for (int f = 0; f < NF; ++f) frag1(kk & 1, f, kk, kt);
-#pragma unroll
-                for (int m = 0; m < MM; ++m) mfma(kk & 1, m);
-            }
-            if (kt + 1 < nk) put(kt + 1);
-            ready();
-        }
+        __syncthreads();
     }
-
-    // Epilogue: each wave passes its accumulators through its own share of
-    // LDS (no barrier between the waves), PA rows of 32 at a time, so that a
-    // lane gets 8 consecutive columns and WN / 8 lanes a whole row of the
-    // wave's tile: 16-byte accesses, and runs saved in 8 bits are
-    // neighbouring lanes.  A row's 16-byte chunks lie even ones first, then
-    // odd ones, permuted by the row: a write (32 rows of one chunk) and a read
-    // (the even, then the odd chunks of a row) touch distinct banks.
-    __syncthreads();
-    constexpr int CPR = WN / 8, ROWB = WN * 4, PASS = (CF::SMEM / CF::WAVES) / (32 * ROWB);
-    constexpr int PAS = PASS < TM ? PASS : TM;  // rows of 32 in one pass
-    static_assert(PAS >= 1 && TM % PAS == 0, "epilogue passes");
-    unsigned char* sw = smem + wave * (CF::SMEM / CF::WAVES);
-#pragma unroll 1
-    for (int pass = 0; pass < TM / PAS; ++pass) {
+    for (int kt = 0; kt < w.nk; ++kt) {
+        // the next step's registers are loaded while this one computes, and
+        // written to the other stage, which everyone's reads left before the
+        // last barrier
+        if (kt + 1 < w.nk) get(kt + 1);
+        const uint16_t* st = stage(kt);
 #pragma unroll
-        for (int a = 0; a < TM; ++a)
-            if (a / PAS == pass) {
+        for (int kk = 0; kk < BK / 16; ++kk) {
+            bf16x8 fa[TM], fb[TN];
 #pragma unroll
-                for (int b = 0; b < TN; ++b)
+            for (int a = 0; a < TM; ++a) fa[a] = A.frag(st, wr * WM + a * 32, kk, lane);
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        const int r = (a % PAS) * 32 + (lane & 31), c = ((4 * b + q) ^ (r & (CPR - 1))) + CPR * (lane >> 5);
-                        *(f32x4*)(sw + r * ROWB + c * 16) =
-                            f32x4{acc[a][b][4 * q], acc[a][b][4 * q + 1], acc[a][b][4 * q + 2], acc[a][b][4 * q + 3]};
-                    }
-            }
-        __builtin_amdgcn_wave_barrier();
-#pragma unroll 2
-        for (int i = 0; i < PAS * 32 * CPR / 64; ++i) {
-            const int id = lane + 64 * i, r = id / CPR, c8 = id % CPR;
-            float v[8];
-            const unsigned char* src = sw + r * ROWB + (c8 ^ (r & (CPR - 1))) * 16;
-            *(f32x4*)&v[0] = *(const f32x4*)src;
-            *(f32x4*)&v[4] = *(const f32x4*)(src + CPR * 16);
-            const int rr = wr * WM + pass * (PAS * 32) + r, cc = wc * WN + c8 * 8;  // in the workgroup's tile
-            if (g.ksplit > 1) {
-                float* out = g.partial + ((int64_t)slice * g.tiles + t) * (CF::BM * CF::BN) + rr * CF::BN + cc;
-                *(f32x4*)out = *(const f32x4*)&v[0];
-                *(f32x4*)(out + 4) = *(const f32x4*)&v[4];
-                continue;
-            }
-            const int cnt = rr < at.rows ? min(max(cols - cc, 0), 8) : 0;
-            bias8<KIND>(g, at.e, at.col0 + cc, cnt, v);
-            uint32_t m = 0;
-            if (KIND == kLinFwd && g.z8.codes) m = amax_lanes(amax8(v, cnt), g.z8.block / 8);
-            finish8<KIND>(g, at.e, at.row0 + rr, at.col0 + cc, cnt, v, m);
+            for (int b = 0; b < TN; ++b) fb[b] = B.frag(st + CF::A_ELEMS, wc * WN + b * 32, kk, lane);
+#pragma unroll
+            for (int a = 0; a < TM; ++a)
+#pragma unroll
+                for (int b = 0; b < TN; ++b) acc[a][b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fb[b], fa[a], acc[a][b], 0, 0, 0);
         }
-        __builtin_amdgcn_wave_barrier();
+        if (kt + 1 < w.nk) put(kt + 1);
+        __syncthreads();
     }
+    epilogue<CF, KIND>(g.finish, w, acc, smem + CF::STAGES_BYTES + wave * CF::OUT_BYTES, wr, wc, lane);
 }
 
 // Slices of split tiles summed in slice order, then the epilogue: one thread
@@ -545,11 +825,11 @@ __global__ void __launch_bounds__(CF::THREADS, CF::PER_CU) k_product(LinArgs g) 
 template <class CF, int KIND>
 __global__ void __launch_bounds__(256) k_join(LinArgs g) {
     constexpr int CPR = CF::BN / 8, PER = CF::BM * CPR / 256;  // workgroups of one tile
-    const int64_t t = blockIdx.x / PER;
-    TileAt at;
-    if (!tile_of<CF, KIND>(g, t, at)) return;
+    const uint32_t t = blockIdx.x / PER;
+    Work w;
+    if (!tile_at<CF, KIND>(g, t, 0, w)) return;
     const int id = (int)(blockIdx.x % PER) * 256 + (int)threadIdx.x, row = id / CPR, c8 = (id % CPR) * 8;
-    const float* p = g.partial + t * (CF::BM * CF::BN) + row * CF::BN + c8;
+    const float* p = g.partial + (int64_t)t * (CF::BM * CF::BN) + row * CF::BN + c8;
     float v[8];
     *(f32x4*)&v[0] = *(const f32x4*)p;
     *(f32x4*)&v[4] = *(const f32x4*)(p + 4);
@@ -562,12 +842,12 @@ __global__ void __launch_bounds__(256) k_join(LinArgs g) {
             v[4 + i] += b[i];
         }
     }
-    const int cols = (int)(g.N - at.col0 < CF::BN ? g.N - at.col0 : CF::BN);
-    const int cnt = row < at.rows ? min(max(cols - c8, 0), 8) : 0;
-    bias8<KIND>(g, at.e, at.col0 + c8, cnt, v);
+    const int cols = (int)(g.N - w.col0 < CF::BN ? g.N - w.col0 : CF::BN);
+    const int cnt = row < w.rows ? min(max(cols - c8, 0), 8) : 0;
+    bias8<KIND>(g, 0, w.col0 + c8, cnt, v);
     uint32_t m = 0;
     if (KIND == kLinFwd && g.z8.codes) m = amax_lanes(amax8(v, cnt), g.z8.block / 8);
-    finish8<KIND>(g, at.e, at.row0 + row, at.col0 + c8, cnt, v, m);
+    finish8<KIND>(g, 0, (int64_t)w.row0 + row, w.col0 + c8, cnt, v, m);
 }
 
 // Few tokens (forward, one group): bound by reading the weights, so the
@@ -661,9 +941,27 @@ hipError_t launch_kind(LinArgs g, int ksplit, hipStream_t s) {
     g.ksplit = ksplit;
     g.tiles = tiles_of<CF>(g, (LinKind)KIND);
     if (g.tiles == 0) return hipSuccess;
-    // whole tiles: 8 runs of equal length, one for each XCD
-    const int64_t grid = ksplit > 1 ? g.tiles * ksplit : (g.tiles + 7) / 8 * 8;
-    hipLaunchKernelGGL((k_product<CF, KIND, DMA>), dim3((unsigned)grid), dim3(CF::THREADS), 0, s, g);
+    const int64_t kMaxLd = int64_t(1) << 21;  // 128 rows within 32-bit byte offsets
+    g.finish = kFinishAll;
+    if (ksplit == 1 && g.N % 8 == 0) {
+        if (KIND == kLinDw) {
+            if (g.vec_dw && !g.wide && !g.accumulate && g.lddw <= kMaxLd) g.finish = kFinishStore;
+        } else if (g.vec_y && g.ldy <= kMaxLd && (!g.res || (g.vec_res && g.ldr <= kMaxLd))) {
+            if (KIND == kLinDx || (g.act == VE_ACT_NONE && !g.z && !g.z8.codes)) g.finish = kFinishStore;
+            else if ((!g.z || (g.vec_z && g.ldz <= kMaxLd)) &&
+                     (!g.z8.codes || (g.vec_z8 && g.z8.ld_codes <= kMaxLd && g.z8.ld_scales <= kMaxLd)))
+                g.finish = kFinishSave;
+        }
+    }
+    // 8 runs of equal length, one for each XCD (kLinDw: of every group)
+    int64_t items = (g.tiles + 7) / 8 * 8;
+    if (KIND == kLinDw) items = g.E * ((g.tiles / g.E + 7) / 8 * 8);
+    if (ksplit > 1) items = (g.tiles * ksplit + 7) / 8 * 8;
+    if constexpr (DMA)
+        hipLaunchKernelGGL((k_product<CF, KIND>), dim3((unsigned)std::min<int64_t>(items, kCUs * CF::PER_CU)),
+                           dim3(CF::THREADS), 0, s, g);
+    else
+        hipLaunchKernelGGL((k_product_any<CF, KIND>), dim3((unsigned)items), dim3(CF::THREADS), 0, s, g);
     if (ksplit > 1)
         hipLaunchKernelGGL((k_join<CF, KIND>), dim3((unsigned)(g.tiles * (CF::BM * (CF::BN / 8) / 256))), dim3(256), 0, s, g);
     return hipGetLastError();
@@ -686,9 +984,11 @@ hipError_t launch_path(const LinArgs& g, const LinPlan& p, hipStream_t s) {
     switch (p.path) {
     case kPathFew: return launch_few(g, s);
     case kPath256: return launch_kind<Cfg256, KIND, true>(g, p.ksplit, s);
-    case kPathMid: return launch_kind<CfgMid, KIND, true>(g, p.ksplit, s);
-    case kPath128: return launch_kind<Cfg128, KIND, true>(g, p.ksplit, s);
-    default: return launch_kind<CfgGen, KIND, false>(g, p.ksplit, s);
+    case kPath128:
+        if constexpr (KIND == kLinFwd)
+            if (g.z8.codes && g.z8.block > Cfg128::WN) return launch_kind<Cfg128W, KIND, true>(g, p.ksplit, s);
+        return launch_kind<Cfg128, KIND, true>(g, p.ksplit, s);
+    default: return launch_kind<Cfg128W, KIND, false>(g, p.ksplit, s);
     }
 }
 
@@ -713,15 +1013,11 @@ LinPlan plan_product(const LinArgs& g, LinKind kind) {
         p.path = kPathFew;
         return p;
     }
-    const int64_t tmid = tiles_of<CfgMid>(g, kind);
-    if (dma_ok(g, kind) && pin != kPathGeneral) p.path = t256 >= 2 * kCUs ? kPath256 : tmid >= kCUs ? kPathMid : kPath128;
-    if (p.path != kPathGeneral && (pin == kPath128 || pin == kPathMid || pin == kPath256)) p.path = (int)pin;
-    // a wave of the 128 x 128 tile has 64 columns, half a run of 128
-    const bool wide_runs = kind == kLinFwd && g.z8.codes && g.z8.block > Cfg128::WN;
-    if (p.path == kPath128 && wide_runs) p.path = kPathMid;
-    const int64_t tiles = p.path == kPath256 ? t256 : p.path == kPathMid ? tmid : t128;
-    const int64_t area = p.path == kPath256 ? 256 * 256 : p.path == kPathMid ? 128 * 256 : 128 * 128;
-    p.ksplit = std::max(1, split(tiles, kCUs * (p.path == kPath256 || p.path == kPathMid ? 1 : Cfg128::PER_CU)));
+    if (dma_ok(g, kind) && pin != kPathGeneral) p.path = t256 >= 2 * kCUs ? kPath256 : kPath128;
+    if (p.path != kPathGeneral && (pin == kPath128 || pin == kPath256)) p.path = (int)pin;
+    const int64_t tiles = p.path == kPath256 ? t256 : t128;
+    const int64_t area = p.path == kPath256 ? 256 * 256 : 128 * 128;
+    p.ksplit = std::max(1, split(tiles, kCUs * (p.path == kPath256 ? Cfg256::PER_CU : Cfg128::PER_CU)));
     p.partial_bytes = p.ksplit > 1 ? p.ksplit * tiles * area * 4 : 0;
     return p;
 }

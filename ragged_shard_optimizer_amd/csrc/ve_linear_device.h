@@ -49,8 +49,8 @@ __device__ __forceinline__ u32x4 narrow8(const float* v) {
     return u32x4{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])};
 }
 
-// exp of a non-positive argument (results below 2^-126 may flush to 0)
-__device__ __forceinline__ float exp_neg(float x) { return __builtin_amdgcn_exp2f(x * 1.44269504088896341f); }
+// exp (results below 2^-126 may flush to 0, above fp32's range they are infinite)
+__device__ __forceinline__ float exp_of(float x) { return __builtin_amdgcn_exp2f(x * 1.44269504088896341f); }
 
 // The upper tail of the normal distribution, Q(a) = erfc(a / sqrt 2) / 2 for
 // a >= 0, as exp(-a^2 / 2) t P(t) with t = 1 / (1 + 0.33 a): erfcx falls like
@@ -68,7 +68,7 @@ __device__ __forceinline__ float normal_tail(float a, float& ex) {
     p = __builtin_fmaf(p, t, 0.1172168105840683f);
     p = __builtin_fmaf(p, t, 0.13164697587490082f);
     p = __builtin_fmaf(p, t, 0.13165107369422913f);
-    ex = exp_neg(-0.5f * a * a);
+    ex = exp_of(-0.5f * a * a);
     return ex * (p * t);
 }
 
@@ -88,14 +88,11 @@ __device__ __forceinline__ float activate(int act, float z) {
     }
     case VE_ACT_GELU_TANH: {
         // 0.5 (1 + tanh u) = 1 / (1 + exp(-2 u))
-        const float u = kGeluTanhC * z * __builtin_fmaf(kGeluTanhB * z, z, 1.f);
-        const float e = exp_neg(-2.f * __builtin_fabsf(u)), r = __builtin_amdgcn_rcpf(1.f + e);
-        return __builtin_fmaxf(z, -1e4f) * (z >= 0.f ? r : e * r);
+        const float u = z * __builtin_fmaf(kGeluTanhC * kGeluTanhB * z, z, kGeluTanhC);
+        return __builtin_fmaxf(z, -1e4f) * __builtin_amdgcn_rcpf(1.f + exp_of(-2.f * u));
     }
-    case VE_ACT_SILU: {
-        const float e = exp_neg(-__builtin_fabsf(z)), r = __builtin_amdgcn_rcpf(1.f + e);
-        return __builtin_fmaxf(z, -1e4f) * (z >= 0.f ? r : e * r);
-    }
+    case VE_ACT_SILU:
+        return __builtin_fmaxf(z, -1e4f) * __builtin_amdgcn_rcpf(1.f + exp_of(-z));
     default:
         return z;
     }
@@ -115,13 +112,13 @@ __device__ __forceinline__ float slope(int act, float z) {
     }
     case VE_ACT_GELU_TANH: {
         const float u = kGeluTanhC * z * __builtin_fmaf(kGeluTanhB * z, z, 1.f);
-        const float e = exp_neg(-2.f * __builtin_fabsf(u)), r = __builtin_amdgcn_rcpf(1.f + e);
+        const float e = exp_of(-2.f * __builtin_fabsf(u)), r = __builtin_amdgcn_rcpf(1.f + e);
         const float a = __builtin_fminf(__builtin_fabsf(z), 64.f), zc = z >= 0.f ? a : -a;
         const float du = 2.f * kGeluTanhC * __builtin_fmaf(3.f * kGeluTanhB * zc, zc, 1.f);
         return __builtin_fmaf(zc * du, e * r * r, z >= 0.f ? r : e * r);
     }
     case VE_ACT_SILU: {
-        const float e = exp_neg(-__builtin_fabsf(z)), r = __builtin_amdgcn_rcpf(1.f + e);
+        const float e = exp_of(-__builtin_fabsf(z)), r = __builtin_amdgcn_rcpf(1.f + e);
         const float a = __builtin_fminf(__builtin_fabsf(z), 1e4f), zc = z >= 0.f ? a : -a;
         return __builtin_fmaf(zc, e * r * r, z >= 0.f ? r : e * r);
     }
@@ -146,14 +143,25 @@ __device__ __forceinline__ RunCode run_code(float amax) {
     }
     return c;
 }
-__device__ __forceinline__ int encode(const RunCode& c, float v) {
-    const float r = __builtin_rintf(v * c.up * c.inv);
-    return c.inv == 0.f ? 0 : (int)__builtin_fminf(__builtin_fmaxf(r, -127.f), 127.f);
-}
+// Adding 1.5 * 2^23 rounds to a whole number (nearest even) and leaves its low
+// byte, in two's complement, in the low byte of the sum.  |v inv| is at most
+// 127 (1 + 2^-23), which rounds to 127, so nothing needs clamping.
 __device__ __forceinline__ u32x2 encode8(const RunCode& c, const float* v) {
-    uint32_t w[2] = {0, 0};
+    uint32_t b[8];
+    if (__any(c.up != 1.f)) {  // a run below 2^-100, or one that is not finite
 #pragma unroll
-    for (int t = 0; t < 8; ++t) w[t >> 2] |= (uint32_t)(encode(c, v[t]) & 255) << (8 * (t & 3));
+        for (int t = 0; t < 8; ++t) b[t] = __float_as_uint(v[t] * c.up * c.inv + 12582912.f);
+    } else {
+#pragma unroll
+        for (int t = 0; t < 8; ++t) b[t] = __float_as_uint(v[t] * c.inv + 12582912.f);
+    }
+    uint32_t w[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const uint32_t lo = __builtin_amdgcn_perm(b[4 * h + 1], b[4 * h], 0x0c0c0400u);
+        const uint32_t hi = __builtin_amdgcn_perm(b[4 * h + 3], b[4 * h + 2], 0x04000c0cu);
+        w[h] = c.inv == 0.f ? 0u : lo | hi;
+    }
     return u32x2{w[0], w[1]};
 }
 // Largest |v|, kept as the bits of |v|: unsigned order puts infinity above

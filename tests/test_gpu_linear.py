@@ -213,7 +213,7 @@ def test_forward(case):
 
 
 # every form of the product where it applies, and split contractions
-@pytest.mark.parametrize("path,split", [(1, 1), (2, 0), (2, 1), (3, 0), (3, 1), (4, 0), (4, 1)])
+@pytest.mark.parametrize("path,split", [(1, 1), (2, 0), (2, 1), (3, 0), (3, 1)])
 @pytest.mark.parametrize("case", [
     (200, 1096, 392, None, "gelu", True, True, True, 64, 0, 0),
     (65, 2056, 136, None, "silu", True, False, False, 128, 0, 0),
@@ -238,7 +238,7 @@ def test_forward_forms(case, path, split):
 def test_forward_of_few_tokens(case):
     ve = _ve()
     print(f"[gpu] forward of few tokens {case}", flush=True)
-    with ve.options(linear_path=5):
+    with ve.options(linear_path=4):
         _forward_case(*case)
 
 
@@ -366,7 +366,7 @@ def test_backward(case):
     _backward_case(*case)
 
 
-@pytest.mark.parametrize("path,split", [(1, 1), (2, 0), (2, 1), (3, 0), (3, 1), (4, 0), (4, 1)])
+@pytest.mark.parametrize("path,split", [(1, 1), (2, 0), (2, 1), (3, 0), (3, 1)])
 @pytest.mark.parametrize("case", [
     (1100, 136, 264, None, "silu", 64, True, True, False, True, 0, 0),
     (130, 264, 1096, None, "none", 0, True, False, True, False, 0, 0),
