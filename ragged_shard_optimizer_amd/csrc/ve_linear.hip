@@ -422,10 +422,12 @@ __device__ __forceinline__ LinArgs args_again() {
 }
 
 // What the epilogue of a launch has to do, as cases that each get their own
-// loop: one store of bf16, for tokens after bias and residual; activation and
-// saving too (both with 16-byte rows and 32-bit offsets from a wave's first
-// row); everything.
-enum Finish : int { kFinishAll, kFinishStore, kFinishSave };
+// loop: one store of bf16, for tokens after the bias; the same after the
+// residual; activation and saving too (these with 16-byte rows and 32-bit
+// offsets from a wave's first row); everything.  The residual is a case and
+// not a condition because a load that some path does not use stays pending
+// for the compiler, which then waits for all loads in every later step.
+enum Finish : int { kFinishAll, kFinishStore, kFinishAdd, kFinishSave };
 
 // Epilogue of one item.  Each wave passes its accumulators through its own
 // 16 rows of LDS (no barrier between the waves), so that a lane gets 8
@@ -449,7 +451,7 @@ __device__ __forceinline__ void epilogue_of(const Work& w, f32x16 (&acc)[CF::TM]
     const int ldo = KIND == kLinDw ? (int)g.lddw : (int)g.ldy;
     uint16_t* out = KIND == kLinDw ? (uint16_t*)g.dw + w.e * g.dw_group + first * g.lddw : g.y + first * g.ldy;
     uint32_t o_off = (uint32_t)(r0 * ldo + (int)col) * 2;
-    const bool res = KIND != kLinDw && g.res;
+    constexpr bool res = FIN == kFinishAdd;
     const uint16_t* rin = res ? g.res + first * g.ldr : nullptr;
     uint32_t r_off = (uint32_t)(r0 * (int)g.ldr + (int)col) * 2;
     int ldc = 0, lds = 0, shift = 0;
@@ -475,7 +477,7 @@ __device__ __forceinline__ void epilogue_of(const Work& w, f32x16 (&acc)[CF::TM]
     for (int pass = 0; pass < 2 * TM; ++pass) {
         const int left = w.rows - wr * WM - pass * 16 - r0;  // rows from the lane's first on
         u32x4 rv[IT];
-        if (FIN != kFinishAll && res) {
+        if constexpr (res) {
 #pragma unroll
             for (int i = 0; i < IT; ++i) {
                 rv[i] = u32x4{0, 0, 0, 0};
@@ -527,7 +529,7 @@ __device__ __forceinline__ void epilogue_of(const Work& w, f32x16 (&acc)[CF::TM]
                     }
                     activate8(g.act, v[i]);
                 }
-                if (res) {
+                if constexpr (res) {
                     float o[8];
                     widen8(rv[i], o);
 #pragma unroll
@@ -566,6 +568,7 @@ template <class CF, int KIND>
 __device__ __forceinline__ void epilogue(int finish, const Work& w, f32x16 (&acc)[CF::TM][CF::TN], unsigned char* sw,
                                          int wr, int wc, int lane) {
     if (finish == kFinishStore) epilogue_of<CF, KIND, kFinishStore>(w, acc, sw, wr, wc, lane);
+    else if (KIND != kLinDw && finish == kFinishAdd) epilogue_of<CF, KIND, kFinishAdd>(w, acc, sw, wr, wc, lane);
     else if (KIND == kLinFwd && finish == kFinishSave) epilogue_of<CF, KIND, kFinishSave>(w, acc, sw, wr, wc, lane);
     else epilogue_of<CF, KIND, kFinishAll>(w, acc, sw, wr, wc, lane);
 }
@@ -733,6 +736,10 @@ __global__ void __launch_bounds__(CF::THREADS, CF::PER_CU) k_product(LinArgs g) 
             }
             ++s;
         };
+        // Nothing of the previous item's epilogue may be pending for the
+        // compiler here (it would wait in every step); the other workgroup of
+        // the CU fills the time.
+        if constexpr (CF::PER_CU > 1) __builtin_amdgcn_s_waitcnt(wait_vm(0));
         // the loads leave this item behind in its last two steps
         const int nk = __builtin_amdgcn_readfirstlane(cw.nk);
         int kt = 0;
@@ -946,11 +953,16 @@ hipError_t launch_kind(LinArgs g, int ksplit, hipStream_t s) {
     if (ksplit == 1 && g.N % 8 == 0) {
         if (KIND == kLinDw) {
             if (g.vec_dw && !g.wide && !g.accumulate && g.lddw <= kMaxLd) g.finish = kFinishStore;
-        } else if (g.vec_y && g.ldy <= kMaxLd && (!g.res || (g.vec_res && g.ldr <= kMaxLd))) {
-            if (KIND == kLinDx || (g.act == VE_ACT_NONE && !g.z && !g.z8.codes)) g.finish = kFinishStore;
-            else if ((!g.z || (g.vec_z && g.ldz <= kMaxLd)) &&
-                     (!g.z8.codes || (g.vec_z8 && g.z8.ld_codes <= kMaxLd && g.z8.ld_scales <= kMaxLd)))
+        } else if (g.vec_y && g.ldy <= kMaxLd) {
+            const bool bare = KIND == kLinDx || (g.act == VE_ACT_NONE && !g.z && !g.z8.codes);
+            if (g.res) {
+                if (bare && g.vec_res && g.ldr <= kMaxLd) g.finish = kFinishAdd;
+            } else if (bare) {
+                g.finish = kFinishStore;
+            } else if ((!g.z || (g.vec_z && g.ldz <= kMaxLd)) &&
+                       (!g.z8.codes || (g.vec_z8 && g.z8.ld_codes <= kMaxLd && g.z8.ld_scales <= kMaxLd))) {
                 g.finish = kFinishSave;
+            }
         }
     }
     // 8 runs of equal length, one for each XCD (kLinDw: of every group)
