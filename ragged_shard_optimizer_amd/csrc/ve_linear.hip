@@ -42,7 +42,7 @@ typedef float f32x16 __attribute__((ext_vector_type(16)));
 #define VE_LDS __attribute__((address_space(3)))
 
 constexpr int kCUs = 256;
-constexpr int kFewTokens = 16;  // rows of the few-token form
+constexpr int kFewTokens = 8;  // tokens of the few-token form, at most
 constexpr int BK = 64;          // contraction step
 
 // Workgroup tile BM x BN of four waves of WM x WN; two LDS stages of operands
@@ -423,11 +423,12 @@ __device__ __forceinline__ LinArgs args_again() {
 
 // What the epilogue of a launch has to do, as cases that each get their own
 // loop: one store of bf16, for tokens after the bias; the same after the
-// residual; activation and saving too (these with 16-byte rows and 32-bit
-// offsets from a wave's first row); everything.  The residual is a case and
+// residual (kLinDw: what dw holds); activation and saving too; one store of
+// fp32, and the same after what dw holds (these with 16-byte rows and 32-bit
+// offsets from a wave's first row); everything.  The addend is a case and
 // not a condition because a load that some path does not use stays pending
 // for the compiler, which then waits for all loads in every later step.
-enum Finish : int { kFinishAll, kFinishStore, kFinishAdd, kFinishSave };
+enum Finish : int { kFinishAll, kFinishStore, kFinishAdd, kFinishSave, kFinishWide, kFinishWideAdd };
 
 // Epilogue of one item.  Each wave passes its accumulators through its own
 // 16 rows of LDS (no barrier between the waves), so that a lane gets 8
@@ -448,12 +449,14 @@ __device__ __forceinline__ void epilogue_of(const Work& w, f32x16 (&acc)[CF::TM]
     float bias[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
     bias8<KIND>(g, w.e, col, cnt0, bias);
     // byte offsets of the lane from the wave's first row
-    const int ldo = KIND == kLinDw ? (int)g.lddw : (int)g.ldy;
-    uint16_t* out = KIND == kLinDw ? (uint16_t*)g.dw + w.e * g.dw_group + first * g.lddw : g.y + first * g.ldy;
-    uint32_t o_off = (uint32_t)(r0 * ldo + (int)col) * 2;
-    constexpr bool res = FIN == kFinishAdd;
-    const uint16_t* rin = res ? g.res + first * g.ldr : nullptr;
-    uint32_t r_off = (uint32_t)(r0 * (int)g.ldr + (int)col) * 2;
+    constexpr bool kWide = FIN == kFinishWide || FIN == kFinishWideAdd, res = FIN == kFinishAdd || FIN == kFinishWideAdd;
+    constexpr int kSize = kWide ? 4 : 2;
+    const int ldo = KIND == kLinDw ? (int)g.lddw : (int)g.ldy, ldr = KIND == kLinDw ? ldo : (int)g.ldr;
+    VE_GLOBAL char* out = KIND == kLinDw ? (VE_GLOBAL char*)g.dw + (w.e * g.dw_group + first * g.lddw) * kSize
+                                         : (VE_GLOBAL char*)(g.y + first * g.ldy);
+    uint32_t o_off = (uint32_t)(r0 * ldo + (int)col) * kSize;
+    const VE_GLOBAL char* rin = KIND == kLinDw ? out : (const VE_GLOBAL char*)(res ? g.res + first * g.ldr : nullptr);
+    uint32_t r_off = (uint32_t)(r0 * ldr + (int)col) * kSize;
     int ldc = 0, lds = 0, shift = 0;
     uint32_t c_off = 0, s_off = 0, z_off = 0;
     VE_GLOBAL char *codes = nullptr, *scales = nullptr, *zout = nullptr;
@@ -476,14 +479,16 @@ __device__ __forceinline__ void epilogue_of(const Work& w, f32x16 (&acc)[CF::TM]
 #pragma unroll 1
     for (int pass = 0; pass < 2 * TM; ++pass) {
         const int left = w.rows - wr * WM - pass * 16 - r0;  // rows from the lane's first on
-        u32x4 rv[IT];
+        u32x4 rv[IT][kWide ? 2 : 1];
         if constexpr (res) {
 #pragma unroll
-            for (int i = 0; i < IT; ++i) {
-                rv[i] = u32x4{0, 0, 0, 0};
-                if (left > RI * i && cnt0 > 0)
-                    rv[i] = *(const VE_GLOBAL u32x4*)((const VE_GLOBAL char*)rin + (r_off + (uint32_t)(RI * i * (int)g.ldr * 2)));
-            }
+            for (int i = 0; i < IT; ++i)
+#pragma unroll
+                for (int h = 0; h < (kWide ? 2 : 1); ++h) {
+                    rv[i][h] = u32x4{0, 0, 0, 0};
+                    if (left > RI * i && cnt0 > 0)
+                        rv[i][h] = *(const VE_GLOBAL u32x4*)(rin + (r_off + (uint32_t)(RI * i * ldr * kSize) + 16 * h));
+                }
         }
         __builtin_amdgcn_wave_barrier();
 #pragma unroll
@@ -520,7 +525,7 @@ __device__ __forceinline__ void epilogue_of(const Work& w, f32x16 (&acc)[CF::TM]
                         *(VE_GLOBAL u32x4*)(zout + (z_off + (uint32_t)(RI * i * (int)g.ldz * 2))) = narrow8(v[i]);
                     if (codes) {
                         // columns past the last are 0: nothing was loaded for them, and their bias is 0
-                        const RunCode c = run_code(__uint_as_float(amax_lanes(amax8(v[i], 8), g.z8.block / 8)));
+                        const RunCode c = run_code_near(__uint_as_float(amax_lanes(amax8(v[i], 8), g.z8.block / 8)));
                         const u32x2 q = encode8(c, v[i]);
                         if (in) {
                             *(VE_GLOBAL u32x2*)(codes + (c_off + (uint32_t)(RI * i * ldc))) = q;
@@ -529,17 +534,28 @@ __device__ __forceinline__ void epilogue_of(const Work& w, f32x16 (&acc)[CF::TM]
                     }
                     activate8(g.act, v[i]);
                 }
-                if constexpr (res) {
+                if constexpr (FIN == kFinishAdd) {
                     float o[8];
-                    widen8(rv[i], o);
+                    widen8(rv[i][0], o);
 #pragma unroll
                     for (int t = 0; t < 8; ++t) v[i][t] += o[t];
                 }
-                if (in)
-                    *(VE_GLOBAL u32x4*)((VE_GLOBAL char*)out + (o_off + (uint32_t)(RI * i * ldo * 2))) = narrow8(v[i]);
+                if constexpr (FIN == kFinishWideAdd) {
+#pragma unroll
+                    for (int t = 0; t < 8; ++t) v[i][t] += __builtin_bit_cast(f32x4, rv[i][t >> 2])[t & 3];
+                }
+                if (in) {
+                    VE_GLOBAL char* o = out + (o_off + (uint32_t)(RI * i * ldo * kSize));
+                    if constexpr (kWide) {
+                        *(VE_GLOBAL f32x4*)o = *(const f32x4*)&v[i][0];
+                        *(VE_GLOBAL f32x4*)(o + 16) = *(const f32x4*)&v[i][4];
+                    } else {
+                        *(VE_GLOBAL u32x4*)o = narrow8(v[i]);
+                    }
+                }
             }
-            o_off += (uint32_t)(16 * ldo * 2);
-            r_off += (uint32_t)(16 * (int)g.ldr * 2);
+            o_off += (uint32_t)(16 * ldo * kSize);
+            r_off += (uint32_t)(16 * ldr * kSize);
             c_off += (uint32_t)(16 * ldc);
             s_off += (uint32_t)(16 * lds * 4);
             z_off += (uint32_t)(16 * (int)g.ldz * 2);
@@ -568,7 +584,9 @@ template <class CF, int KIND>
 __device__ __forceinline__ void epilogue(int finish, const Work& w, f32x16 (&acc)[CF::TM][CF::TN], unsigned char* sw,
                                          int wr, int wc, int lane) {
     if (finish == kFinishStore) epilogue_of<CF, KIND, kFinishStore>(w, acc, sw, wr, wc, lane);
-    else if (KIND != kLinDw && finish == kFinishAdd) epilogue_of<CF, KIND, kFinishAdd>(w, acc, sw, wr, wc, lane);
+    else if (finish == kFinishAdd) epilogue_of<CF, KIND, kFinishAdd>(w, acc, sw, wr, wc, lane);
+    else if (KIND == kLinDw && finish == kFinishWide) epilogue_of<CF, KIND, kFinishWide>(w, acc, sw, wr, wc, lane);
+    else if (KIND == kLinDw && finish == kFinishWideAdd) epilogue_of<CF, KIND, kFinishWideAdd>(w, acc, sw, wr, wc, lane);
     else if (KIND == kLinFwd && finish == kFinishSave) epilogue_of<CF, KIND, kFinishSave>(w, acc, sw, wr, wc, lane);
     else epilogue_of<CF, KIND, kFinishAll>(w, acc, sw, wr, wc, lane);
 }
@@ -857,81 +875,88 @@ __global__ void __launch_bounds__(256) k_join(LinArgs g) {
     finish8<KIND>(g, 0, (int64_t)w.row0 + row, w.col0 + c8, cnt, v, m);
 }
 
-// Few tokens (forward, one group): bound by reading the weights, so the
-// contraction is what is split.  A workgroup takes 16 output columns (rows of
-// w); its waves take turns of 128 along the contraction, straight from memory
-// into MFMA fragments (no element of w is read twice, so LDS would only add a
-// copy), with the next turn's loads in flight.  The waves' sums are joined in
-// LDS in wave order, and 8 columns of a token go through the epilogue
-// together.  One token, 8192 -> 28672: 89 us, 5.3 TB/s (128 x 128 tiles: 131);
-// 32 columns a workgroup 104, 4 waves instead of 8 95.
-//
-// MFMA 16x16x32 bf16, w as the first operand: lane l reads 8 consecutive k
-// (8 (l / 16) + 0 .. 7) of row l % 16; accumulator register r of lane l holds
-// column 4 (l / 16) + r of token l % 16.
-template <int WAVES>
-__global__ void __launch_bounds__(64 * WAVES) k_few(LinArgs g) {
-    constexpr int U = 4, MT = kFewTokens, NR = 16, LDN = NR + 4;  // LDS rows of NR columns, padded
-    __shared__ __attribute__((aligned(16))) float part[WAVES][MT][LDN];
+// Few tokens (forward, one group): bound by reading the weights.  A wave takes
+// R rows of w (output columns) whole: each load is 1 KiB of one row, 512
+// steps of the contraction, and every lane keeps its own sums (products of
+// bf16 pairs, v_dot2_f32_bf16) until the end.  x comes from the caches, once
+// for the R rows.  MT: tokens, of which g.T exist.
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+template <int MT, int R, int U>
+__global__ void __launch_bounds__(256) k_few(LinArgs g) {
+    __shared__ float sums[MT][4 * R];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-    const int64_t n0 = (int64_t)blockIdx.x * NR;
-    const int wrows = (int)min(g.N - n0, (int64_t)NR), toks = (int)g.T, row = lane & 15, k8 = (lane >> 4) * 8;
+    const int64_t n0 = (int64_t)blockIdx.x * (4 * R);
+    const int rows = (int)min(max(g.N - n0 - wave * R, (int64_t)0), (int64_t)R), toks = (int)g.T, K = (int)g.K;
+    // reads past the last row, token or the contraction leave the buffers and return 0
+    const uint16_t* wp = g.B + (n0 + min((int64_t)wave * R, g.N - 1 - n0)) * g.ldb;
     const __amdgpu_buffer_rsrc_t wr = __builtin_amdgcn_make_buffer_rsrc(
-        (void*)(g.B + n0 * g.ldb), (short)0, (int)(uint32_t)(((wrows - 1) * g.ldb + g.K) * 2), 0x00020000);
+        (void*)wp, (short)0, rows ? (int)(((rows - 1) * g.ldb + K) * 2) : 0, 0x00020000);
     const __amdgpu_buffer_rsrc_t xr = __builtin_amdgcn_make_buffer_rsrc(
-        (void*)g.A, (short)0, (int)(uint32_t)(((toks - 1) * g.lda + g.K) * 2), 0x00020000);
-    const int K = (int)g.K;
-    // byte offsets of the lane's rows; reads past the last row or the
-    // contraction are sent out of the buffers and return 0
-    const uint32_t wrow = row < wrows ? (uint32_t)(row * g.ldb * 2) : 0x80000000u;
-    const uint32_t xrow = row < toks ? (uint32_t)(row * g.lda * 2) : 0x80000000u;
-    f32x4 acc = {0.f, 0.f, 0.f, 0.f};
-    u32x4 w[2][U], x[2][U];
-    auto load = [&](int buf, int k0) {
+        (void*)g.A, (short)0, (int)(((toks - 1) * g.lda + K) * 2), 0x00020000);
+    float acc[R][MT];
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int t = 0; t < MT; ++t) acc[r][t] = 0.f;
+    for (int k0 = lane * 8; k0 < (K + 511) / 512 * 512; k0 += 512 * U) {
+        u32x4 w[U][R];
+        uint32_t off[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int k = k0 + 32 * u + k8;
-            const uint32_t off = k < K ? (uint32_t)k * 2 : 0x40000000u;
-            w[buf][u] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(wr, (int)(wrow + off), 0, 0));
-            x[buf][u] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(xr, (int)(xrow + off), 0, 0));
+            const int k = k0 + 512 * u;
+            off[u] = k < K ? (uint32_t)k * 2 : 0x80000000u;
+#pragma unroll
+            for (int r = 0; r < R; ++r)
+                w[u][r] = __builtin_bit_cast(
+                    u32x4, __builtin_amdgcn_raw_buffer_load_b128(wr, (int)(off[u] + (uint32_t)(r * (int)g.ldb * 2)), 0, 0));
         }
-    };
-    auto compute = [&](int buf) {
 #pragma unroll
         for (int u = 0; u < U; ++u)
-            acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, w[buf][u]),
-                                                          __builtin_bit_cast(bf16x8, x[buf][u]), acc, 0, 0, 0);
-    };
-    constexpr int STEP = 32 * U * WAVES;
-    int k0 = 32 * U * wave;
-    load(0, k0);
-    for (; k0 < K; k0 += 2 * STEP) {
-        load(1, k0 + STEP);
-        compute(0);
-        load(0, k0 + 2 * STEP);
-        compute(1);
+#pragma unroll
+            for (int t = 0; t < MT; ++t) {
+                const u32x4 x = __builtin_bit_cast(
+                    u32x4, __builtin_amdgcn_raw_buffer_load_b128(xr, (int)(off[u] + (uint32_t)(t * (int)g.lda * 2)), 0, 0));
+#pragma unroll
+                for (int r = 0; r < R; ++r)
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const uint32_t wq = w[u][r][q], xq = x[q];
+                        acc[r][t] = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, wq),
+                                                                    __builtin_bit_cast(bf16x2, xq), acc[r][t], false);
+                    }
+            }
     }
-    *(f32x4*)&part[wave][row][4 * (lane >> 4)] = acc;
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int t = 0; t < MT; ++t) {
+#pragma unroll
+            for (int d = 32; d; d >>= 1) acc[r][t] += __shfl_xor(acc[r][t], d, 64);
+            if (lane == 0) sums[t][wave * R + r] = acc[r][t];
+        }
     __syncthreads();
-    const int t = threadIdx.x / (NR / 8), c8 = (threadIdx.x % (NR / 8)) * 8;
+    constexpr int G = (4 * R + 7) / 8;  // groups of up to 8 columns
+    const int t = threadIdx.x / G, c8 = (threadIdx.x % G) * 8;
     if (t >= toks) return;
     float v[8];
 #pragma unroll
-    for (int c = 0; c < 8; ++c) v[c] = part[0][t][c8 + c];
-#pragma unroll
-    for (int s = 1; s < WAVES; ++s)
-#pragma unroll
-        for (int c = 0; c < 8; ++c) v[c] += part[s][t][c8 + c];
-    const int cnt = min(max(wrows - c8, 0), 8);
+    for (int c = 0; c < 8; ++c) v[c] = c8 + c < 4 * R ? sums[t][c8 + c] : 0.f;
+    const int cnt = (int)min(max(g.N - n0 - c8, (int64_t)0), (int64_t)min(4 * R - c8, 8));
     bias8<kLinFwd>(g, 0, n0 + c8, cnt, v);
     finish8<kLinFwd>(g, 0, t, n0 + c8, cnt, v, 0);
 }
 
+template <int MT>
+void launch_few_t(const LinArgs& g, hipStream_t s) {
+    // one row a wave where four would leave CUs without work
+    if (g.N < 16 * kCUs) hipLaunchKernelGGL((k_few<MT, 1, 8>), dim3((unsigned)((g.N + 3) / 4)), dim3(256), 0, s, g);
+    else hipLaunchKernelGGL((k_few<MT, 4, 4>), dim3((unsigned)((g.N + 15) / 16)), dim3(256), 0, s, g);
+}
 hipError_t launch_few(const LinArgs& g, hipStream_t s) {
-    // 8 waves a workgroup; 16 where there are too few workgroups to fill the CUs
-    const unsigned grid = (unsigned)((g.N + 15) / 16);
-    if (grid <= 4 * kCUs) hipLaunchKernelGGL(k_few<16>, dim3(grid), dim3(1024), 0, s, g);
-    else hipLaunchKernelGGL(k_few<8>, dim3(grid), dim3(512), 0, s, g);
+    if (g.T <= 1) launch_few_t<1>(g, s);
+    else if (g.T <= 2) launch_few_t<2>(g, s);
+    else if (g.T <= 4) launch_few_t<4>(g, s);
+    else launch_few_t<8>(g, s);
     return hipGetLastError();
 }
 
@@ -952,7 +977,8 @@ hipError_t launch_kind(LinArgs g, int ksplit, hipStream_t s) {
     g.finish = kFinishAll;
     if (ksplit == 1 && g.N % 8 == 0) {
         if (KIND == kLinDw) {
-            if (g.vec_dw && !g.wide && !g.accumulate && g.lddw <= kMaxLd) g.finish = kFinishStore;
+            if (g.vec_dw && g.lddw <= kMaxLd)
+                g.finish = g.wide ? (g.accumulate ? kFinishWideAdd : kFinishWide) : (g.accumulate ? kFinishAdd : kFinishStore);
         } else if (g.vec_y && g.ldy <= kMaxLd) {
             const bool bare = KIND == kLinDx || (g.act == VE_ACT_NONE && !g.z && !g.z8.codes);
             if (g.res) {
@@ -1004,33 +1030,57 @@ hipError_t launch_path(const LinArgs& g, const LinPlan& p, hipStream_t s) {
     }
 }
 
+// Microseconds of a product as `items` tiles (or slices) of `steps` steps: a
+// CU takes its share of them, 256 x 256 tiles one by one, 128 x 128 tiles two
+// at a time (a last one alone).  Measured: a step of 256 x 256 takes 1.42 us
+// and its start and epilogue 5; of a pair of 128 x 128 tiles 0.9 and 4, of a
+// single one 0.6.  Slices' sums (bytes) are written and read at 5 TB/s, by
+// one launch more (4 us).  Against measurements, 128^2 / 256^2 in us: 4001
+// tokens 2880 -> 5760 dx 141 / 127 (model 143 / 133), dw 157 / 179 (163 /
+// 189); 2049 tokens 4096 -> 2880 forward 59 (62).
+double product_us(bool big, int64_t items, int64_t steps, int64_t bytes) {
+    const double n = (double)((items + kCUs - 1) / kCUs), st = (double)steps;
+    const double sums = bytes ? (double)bytes * 2 / 5e6 + 4 : 0;
+    if (big) return n * (1.42 * st + 5) + sums;
+    const double pairs = (double)((int64_t)n / 2), one = n - 2 * pairs;
+    return pairs * (0.9 * st + 4) + one * (0.6 * st + 4) + sums;
+}
+
 }  // namespace
 
 LinPlan plan_product(const LinArgs& g, LinKind kind) {
     LinPlan p{kPathGeneral, 1, 0};
     const int64_t pin = option(kOptLinearPath);
-    const int64_t t256 = tiles_of<Cfg256>(g, kind), t128 = tiles_of<Cfg128>(g, kind);
-    const int64_t K = kind == kLinDw ? g.T / std::max(1, g.E) : g.K, nk = (K + BK - 1) / BK;
-    auto split = [&](int64_t tiles, int64_t slots) -> int {
-        if (g.offsets || option(kOptLinearSplit) == 0 || tiles * 2 > slots || nk < 16) return 1;
-        return (int)std::min<int64_t>(std::min(slots / std::max<int64_t>(tiles, 1), nk / 8), 32);
-    };
     // Up to 8 tokens the few-token form is faster (us, 8192 -> 28672 one token
     // 89 against 131 of the tiles; 8192 -> 1024 14 against 19), at 16 the
     // tiles split along the contraction are (8192 -> 8192: 35 against 37).
     // Ragged groups stay with the tiles, which stream 32 groups' weights at
     // 5.6 TB/s with one token or 16 in each.
     const bool few = kind == kLinFwd && !g.offsets && !g.z8.codes && dma_ok(g, kind);
-    if (few && ((pin == kPathAuto && g.T <= 8) || (pin == kPathFew && g.T <= kFewTokens))) {
+    if (few && g.T <= kFewTokens && (pin == kPathAuto || pin == kPathFew)) {
         p.path = kPathFew;
         return p;
     }
-    if (dma_ok(g, kind) && pin != kPathGeneral) p.path = t256 >= 2 * kCUs ? kPath256 : kPath128;
-    if (p.path != kPathGeneral && (pin == kPath128 || pin == kPath256)) p.path = (int)pin;
-    const int64_t tiles = p.path == kPath256 ? t256 : t128;
-    const int64_t area = p.path == kPath256 ? 256 * 256 : 128 * 128;
-    p.ksplit = std::max(1, split(tiles, kCUs * (p.path == kPath256 ? Cfg256::PER_CU : Cfg128::PER_CU)));
-    p.partial_bytes = p.ksplit > 1 ? p.ksplit * tiles * area * 4 : 0;
+    const bool dma = dma_ok(g, kind) && pin != kPathGeneral;
+    const int64_t K = kind == kLinDw ? g.T / g.E : g.K, nk = std::max<int64_t>(1, (K + BK - 1) / BK);
+    const bool may_split = !g.offsets && option(kOptLinearSplit) != 0;
+    double best = 0;
+    for (int path : {(int)kPath128, (int)kPath256}) {
+        if (!dma && path == kPath256) break;
+        if (dma && (pin == kPath128 || pin == kPath256) && pin != path) continue;
+        const int64_t tiles = path == kPath256 ? tiles_of<Cfg256>(g, kind) : tiles_of<Cfg128>(g, kind);
+        const int64_t slots = kCUs * (path == kPath256 ? Cfg256::PER_CU : Cfg128::PER_CU), area = path == kPath256 ? 65536 : 16384;
+        for (int64_t ks = 1; ks <= 32; ++ks) {
+            if (ks > 1 && (!may_split || nk / ks < 4 || tiles * ks > slots)) break;
+            const double us = product_us(path == kPath256, tiles * ks, (nk + ks - 1) / ks, ks > 1 ? tiles * ks * area * 4 : 0);
+            if (best == 0 || us < best) {
+                best = us;
+                p.path = dma ? path : (int)kPathGeneral;
+                p.ksplit = (int)ks;
+                p.partial_bytes = ks > 1 ? ks * tiles * area * 4 : 0;
+            }
+        }
+    }
     return p;
 }
 

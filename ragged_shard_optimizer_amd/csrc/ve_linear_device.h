@@ -143,6 +143,17 @@ __device__ __forceinline__ RunCode run_code(float amax) {
     }
     return c;
 }
+// The same to within a unit in the last place of scale and inv, for a
+// product's epilogue, where two divisions for each 8 values show: the two
+// quotients by multiplication with 1 / 127 and with the reciprocal.
+__device__ __forceinline__ RunCode run_code_near(float amax) {
+    if (__any(!(amax >= 0x1p-100f && amax <= 0x1p100f))) return run_code(amax);
+    RunCode c;
+    c.up = 1.f;
+    c.scale = amax * (1.f / 127.f);
+    c.inv = 127.f * __builtin_amdgcn_rcpf(amax);
+    return c;
+}
 // Adding 1.5 * 2^23 rounds to a whole number (nearest even) and leaves its low
 // byte, in two's complement, in the low byte of the sum.  |v inv| is at most
 // 127 (1 + 2^-23), which rounds to 127, so nothing needs clamping.
@@ -170,12 +181,18 @@ __device__ __forceinline__ uint32_t amax_of(uint32_t m, float v) {
     const uint32_t a = __float_as_uint(v) & 0x7fffffffu;
     return a > m ? a : m;
 }
-// ... over runs of `lanes` consecutive lanes (a power of two)
+// ... over runs of 4, 8 or 16 consecutive lanes, by exchanges inside a row of
+// 16 lanes that need no LDS: neighbours, pairs, mirrored halves, mirrored row.
+template <int CTRL>
+__device__ __forceinline__ uint32_t amax_with(uint32_t m) {
+    const uint32_t o = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, CTRL, 0xf, 0xf, true);
+    return o > m ? o : m;
+}
 __device__ __forceinline__ uint32_t amax_lanes(uint32_t m, int lanes) {
-    for (int d = 1; d < lanes; d <<= 1) {
-        const uint32_t o = (uint32_t)__shfl_xor((int)m, d, 64);
-        m = o > m ? o : m;
-    }
+    m = amax_with<0xB1>(m);                    // quad_perm 1 0 3 2
+    m = amax_with<0x4E>(m);                    // quad_perm 2 3 0 1
+    if (lanes > 4) m = amax_with<0x141>(m);    // row_half_mirror
+    if (lanes > 8) m = amax_with<0x140>(m);    // row_mirror
     return m;
 }
 
