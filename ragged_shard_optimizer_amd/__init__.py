@@ -374,27 +374,38 @@ def gemm_bf16_nt(P, Q, C=None, CT=None, D=None, alpha: float = 1.0, beta: float 
 # ---------------------------------------------------------------------------
 # linear layers and 8-bit saved activations
 
-def _matrix(t, rows, cols, name, device, itemsize=2):
-    """(pointer, leading dimension) of a rows x cols device matrix whose rows
-    are contiguous (any stride between them)."""
-    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols:
-        raise ValueError(f"{name}: shape {tuple(t.shape)} != {(rows, cols)}")
+_TYPES = None  # element types by size, and torch, once a call has needed them
+_torch = None
+
+
+def _types():
+    global _TYPES, _torch
+    if _TYPES is None:
+        import torch
+        _TYPES = {1: (torch.int8, torch.uint8), 2: (torch.bfloat16, torch.int16, torch.uint16), 4: (torch.float32,)}
+        _torch = torch
+    return _TYPES
+
+
+def _rows(t, shape, name, device, itemsize):
+    """(pointer, strides) of a device tensor of this shape and element size
+    whose rows are contiguous (any stride between them)."""
+    if t.shape != shape:
+        raise ValueError(f"{name}: shape {tuple(t.shape)} != {shape}")
     if t.device != device or not t.is_cuda:
         raise ValueError(f"{name}: must be a device tensor on {device}")
-    return t.data_ptr(), _lead(t, rows, cols, name, itemsize)
-
-
-def _lead(t, rows, cols, name, itemsize):
-    _elements(t, name, itemsize)
-    ld, inner = t.stride()[-2:]
-    if inner != 1 and cols > 1:
+    if t.dtype not in _types()[itemsize]:
+        raise ValueError(f"{name}: need {'bf16 (bits)' if itemsize == 2 else 'int8' if itemsize == 1 else 'fp32'} elements")
+    st = t.stride()
+    if st[-1] != 1 and shape[-1] > 1:
         raise ValueError(f"{name}: rows must be contiguous")
-    return ld if rows > 1 else max(ld, cols)
+    return t.data_ptr(), st
 
 
-def _elements(t, name, itemsize):
-    if t.element_size() != itemsize or (itemsize == 2 and "float16" == str(t.dtype)[6:]):
-        raise ValueError(f"{name}: need {itemsize}-byte elements" + (" (bf16 bits)" if itemsize == 2 else ""))
+def _matrix(t, rows, cols, name, device, itemsize=2):
+    """(pointer, leading dimension) of a rows x cols device matrix."""
+    ptr, st = _rows(t, (rows, cols), name, device, itemsize)
+    return ptr, st[0] if rows > 1 else max(st[0], cols)
 
 
 def _groups_of(t, groups, rows, cols, name, device, itemsize=2):
@@ -403,24 +414,14 @@ def _groups_of(t, groups, rows, cols, name, device, itemsize=2):
     if groups is None:
         ptr, ld = _matrix(t, rows, cols, name, device, itemsize)
         return ptr, ld, 0
-    if tuple(t.shape) != (groups, rows, cols):
-        raise ValueError(f"{name}: shape {tuple(t.shape)} != {(groups, rows, cols)}")
-    if t.device != device or not t.is_cuda:
-        raise ValueError(f"{name}: must be a device tensor on {device}")
-    return t.data_ptr(), _lead(t, rows, cols, name, itemsize), t.stride(0)
+    ptr, st = _rows(t, (groups, rows, cols), name, device, itemsize)
+    return ptr, st[1] if rows > 1 else max(st[1], cols), st[0]
 
 
 def _vectors_of(t, groups, n, name, device, itemsize=2):
     """(pointer, group stride) of [n] or [groups, n]."""
-    want = (n,) if groups is None else (groups, n)
-    if tuple(t.shape) != want:
-        raise ValueError(f"{name}: shape {tuple(t.shape)} != {want}")
-    if t.device != device or not t.is_cuda:
-        raise ValueError(f"{name}: must be a device tensor on {device}")
-    _elements(t, name, itemsize)
-    if t.stride(-1) != 1 and n > 1:
-        raise ValueError(f"{name}: must be contiguous")
-    return t.data_ptr(), 0 if groups is None else t.stride(0)
+    ptr, st = _rows(t, (n,) if groups is None else (groups, n), name, device, itemsize)
+    return ptr, 0 if groups is None else st[0]
 
 
 class Act8:
@@ -449,62 +450,50 @@ def new_act8(rows: int, cols: int, block: int = 128, device="cuda") -> Act8:
                 torch.empty(rows, -(-cols // block), dtype=torch.float32, device=device), block)
 
 
-class _On:
-    """The stream of a call whose tensors live on ``device`` (the device's
-    current stream if None), with that device current while it launches."""
-
-    __slots__ = ("device", "stream", "handle", "before")
-
-    def __init__(self, device, stream):
-        import torch
-        self.device, self.stream = device, stream
-        if stream is None:
-            self.handle = torch.cuda.current_stream(device).cuda_stream
-        else:
-            self.handle = stream if isinstance(stream, int) else stream.cuda_stream
-            if not isinstance(stream, int) and stream.device != device:
-                raise ValueError(f"stream on {stream.device}, tensors on {device}")
-
-    def __enter__(self):
-        import torch
-        now = torch.cuda.current_device()
-        self.before = now if now != self.device.index else None
-        if self.before is not None:
-            torch.cuda.set_device(self.device)
-        return self
-
-    def __exit__(self, *exc):
-        if self.before is not None:
-            import torch
-            torch.cuda.set_device(self.before)
-        return False
-
-    def workspace(self, need: int, given):
-        """(pointer, bytes) of the call's scratch.  Where it is allocated here
-        it belongs to the call's stream, so the allocator hands it out again
-        only behind the call."""
-        if given is not None:
-            if given.device != self.device:
-                raise ValueError("workspace: must be on the tensors' device")
-            _require_buffer(given, need, 1, "workspace")
-            return given.data_ptr(), given.numel()
-        if need == 0:
-            return None, 0
-        import torch
-        if self.stream is None:
-            return torch.empty(need, dtype=torch.uint8, device=self.device)
-        st = torch.cuda.ExternalStream(self.stream, self.device) if isinstance(self.stream, int) else self.stream
-        with torch.cuda.stream(st):
-            return torch.empty(need, dtype=torch.uint8, device=self.device)
+def _stream_on(device, stream):
+    """The handle of ``stream``, or of the current stream of ``device``."""
+    if stream is None:
+        return _torch.cuda.current_stream(device).cuda_stream
+    if isinstance(stream, int):
+        return stream
+    if stream.device != device:
+        raise ValueError(f"stream on {stream.device}, tensors on {device}")
+    return stream.cuda_stream
 
 
-def _run(call, args, query, device, stream, workspace):
-    with _On(device, stream) as on:
-        need = C.c_int64()
-        _check(query(C.byref(args), C.byref(need)))
-        ws = on.workspace(need.value, workspace)
-        ptr, size = ws if isinstance(ws, tuple) else (ws.data_ptr(), need.value)
-        _check(call(C.byref(args), ptr, size, on.handle))
+def _scratch(need, device, stream):
+    """A workspace that belongs to the call's stream, so that the allocator
+    hands it out again only behind the call."""
+    if stream is None:
+        return _torch.empty(need, dtype=_torch.uint8, device=device)
+    st = _torch.cuda.ExternalStream(stream, device) if isinstance(stream, int) else stream
+    with _torch.cuda.stream(st):
+        return _torch.empty(need, dtype=_torch.uint8, device=device)
+
+
+def _call(device, fn, *args):
+    """A launching entry point with the tensors' device current."""
+    if _torch.cuda.current_device() == device.index:
+        return _check(fn(*args))
+    with _torch.cuda.device(device):
+        return _check(fn(*args))
+
+
+def _run(call, query, args, device, stream, workspace):
+    handle = _stream_on(device, stream)
+    if workspace is not None:
+        if workspace.device != device:
+            raise ValueError("workspace: must be on the tensors' device")
+        _require_buffer(workspace, 0, 1, "workspace")
+        _call(device, call, C.byref(args), workspace.data_ptr(), workspace.numel(), handle)
+        return
+    need = C.c_int64()
+    _check(query(C.byref(args), C.byref(need)))
+    if need.value == 0:
+        _call(device, call, C.byref(args), None, 0, handle)
+        return
+    ws = _scratch(need.value, device, stream)
+    _call(device, call, C.byref(args), ws.data_ptr(), need.value, handle)
 
 
 def act8_pack(x, out: Act8, stream=None) -> Act8:
@@ -512,8 +501,7 @@ def act8_pack(x, out: Act8, stream=None) -> Act8:
     rows, cols = x.shape
     ptr, ld = _matrix(x, rows, cols, "x", x.device)
     q = out._fill(rows, cols, "out", x.device)
-    with _On(x.device, stream) as on:
-        _check(lib().ve_act8_pack(ptr, ld, rows, cols, C.byref(q), on.handle))
+    _call(x.device, lib().ve_act8_pack, ptr, ld, rows, cols, C.byref(q), _stream_on(x.device, stream))
     return out
 
 
@@ -522,8 +510,7 @@ def act8_unpack(q: Act8, out, stream=None):
     rows, cols = out.shape
     ptr, ld = _matrix(out, rows, cols, "out", out.device)
     s = q._fill(rows, cols, "q", out.device)
-    with _On(out.device, stream) as on:
-        _check(lib().ve_act8_unpack(C.byref(s), rows, cols, ptr, ld, on.handle))
+    _call(out.device, lib().ve_act8_unpack, C.byref(s), rows, cols, ptr, ld, _stream_on(out.device, stream))
     return out
 
 
@@ -531,7 +518,8 @@ def _shape(a, tokens, w, offsets, activation, device, wname="w"):
     """Fill the shape of an argument record; returns groups (None without offsets)."""
     groups = None
     if offsets is not None:
-        if offsets.dim() != 1 or offsets.shape[0] < 2 or str(offsets.dtype) != "torch.int64":
+        _types()
+        if offsets.dim() != 1 or offsets.shape[0] < 2 or offsets.dtype != _torch.int64:
             raise ValueError("offsets: a 1-D int64 tensor of groups + 1 elements")
         if offsets.device != device or not offsets.is_contiguous():
             raise ValueError(f"offsets: must be contiguous on {device}")
@@ -591,7 +579,7 @@ def _forward(x, w, y, bias, activation, residual, z, z8, offsets, workspace, str
         need = C.c_int64()
         _check(L.ve_linear_forward_workspace(C.byref(a), C.byref(need)))
         return need.value
-    _run(L.ve_linear_forward, a, L.ve_linear_forward_workspace, dev, stream, workspace)
+    _run(L.ve_linear_forward, L.ve_linear_forward_workspace, a, dev, stream, workspace)
     return y
 
 
@@ -644,9 +632,6 @@ def _backward(dy, w, x, z, activation, dx, dx_add, dw, dbias, accumulate, offset
     if len(sizes) > 1 or not sizes <= {2, 4}:
         raise ValueError("dw and dbias: both bf16 or both fp32")
     item = sizes.pop() if sizes else 2
-    for t, name in ((dw, "dw"), (dbias, "dbias")):
-        if t is not None and item == 4 and str(t.dtype) != "torch.float32":
-            raise ValueError(f"{name}: need bf16 or fp32")
     a.grad_fp32, a.accumulate = int(item == 4), int(bool(accumulate))
     if dw is not None:
         a.dw, a.lddw, a.dw_group = _groups_of(dw, g, N, K, "dw", dev, item)
@@ -657,7 +642,7 @@ def _backward(dy, w, x, z, activation, dx, dx_add, dw, dbias, accumulate, offset
         need = C.c_int64()
         _check(L.ve_linear_backward_workspace(C.byref(a), C.byref(need)))
         return need.value
-    _run(L.ve_linear_backward, a, L.ve_linear_backward_workspace, dev, stream, workspace)
+    _run(L.ve_linear_backward, L.ve_linear_backward_workspace, a, dev, stream, workspace)
 
 
 def stream_copy(dst, src, stream=None):

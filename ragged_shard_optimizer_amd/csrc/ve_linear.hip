@@ -723,7 +723,10 @@ __global__ void __launch_bounds__(CF::THREADS, CF::PER_CU) k_product(LinArgs g) 
         // spread evenly over two sub-steps: issued faster they stall the
         // wave (all within half a sub-step: 1,207 TFLOP/s forward at 8192^3,
         // one sub-step: 1,260), later they have less time to land (two and a
-        // half: 1,283; two: 1,306).
+        // half: 1,283; two: 1,306).  Four stages of steps of 32, with the
+        // loads two to three steps ahead, were slower (forward 1,249 against
+        // 1,412 at 8192 x 8192 -> 28672: 64-byte pieces of a row, and twice
+        // the barriers).
         auto step = [&](auto&& next) {
 #pragma unroll
             for (int kk = 0; kk < BK / 16 - 1; ++kk) {
@@ -1072,7 +1075,11 @@ LinPlan plan_product(const LinArgs& g, LinKind kind) {
         const int64_t slots = kCUs * (path == kPath256 ? Cfg256::PER_CU : Cfg128::PER_CU), area = path == kPath256 ? 65536 : 16384;
         for (int64_t ks = 1; ks <= 32; ++ks) {
             if (ks > 1 && (!may_split || nk / ks < 4 || tiles * ks > slots)) break;
-            const double us = product_us(path == kPath256, tiles * ks, (nk + ks - 1) / ks, ks > 1 ? tiles * ks * area * 4 : 0);
+            double us = product_us(path == kPath256, tiles * ks, (nk + ks - 1) / ks, ks > 1 ? tiles * ks * area * 4 : 0);
+            // runs of 128 columns saved from 128 x 128 tiles need waves of 32 x
+            // 128, which take 1.5 times as long (16384 tokens of 32 experts
+            // 7168 -> 2048: 852 us against 577)
+            if (path == kPath128 && ks == 1 && kind == kLinFwd && g.z8.codes && g.z8.block > Cfg128::WN) us *= 1.5;
             if (best == 0 || us < best) {
                 best = us;
                 p.path = dma ? path : (int)kPathGeneral;
