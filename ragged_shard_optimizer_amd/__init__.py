@@ -376,14 +376,16 @@ def gemm_bf16_nt(P, Q, C=None, CT=None, D=None, alpha: float = 1.0, beta: float 
 
 _TYPES = None  # element types by size, and torch, once a call has needed them
 _torch = None
+_raw_stream = None  # torch's handle-only query of the current stream, where it has one (3 us less than the object)
 
 
 def _types():
-    global _TYPES, _torch
+    global _TYPES, _torch, _raw_stream
     if _TYPES is None:
         import torch
         _TYPES = {1: (torch.int8, torch.uint8), 2: (torch.bfloat16, torch.int16, torch.uint16), 4: (torch.float32,)}
         _torch = torch
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
     return _TYPES
 
 
@@ -453,6 +455,8 @@ def new_act8(rows: int, cols: int, block: int = 128, device="cuda") -> Act8:
 def _stream_on(device, stream):
     """The handle of ``stream``, or of the current stream of ``device``."""
     if stream is None:
+        if _raw_stream is not None:
+            return _raw_stream(device.index)
         return _torch.cuda.current_stream(device).cuda_stream
     if isinstance(stream, int):
         return stream

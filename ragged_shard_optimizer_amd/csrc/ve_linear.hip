@@ -633,6 +633,7 @@ __global__ void __launch_bounds__(CF::THREADS, CF::PER_CU) k_product(LinArgs g) 
     // scalar registers in between.
     int lk = 0, lend = 0;
     bool lok = true;
+    uint32_t item = 0;
     auto next_loaded = [&](bool first) {  // the next item with steps
         const LinArgs h = args_again();
         Work w;
@@ -643,6 +644,14 @@ __global__ void __launch_bounds__(CF::THREADS, CF::PER_CU) k_product(LinArgs g) 
             w.nk = __builtin_amdgcn_readfirstlane(w.nk);
         } while (lok && w.nk == 0);
         if (!lok) return;
+        // what the item's epilogue will need, in lanes of a vector register
+        put_lane(item, 0, (uint32_t)w.e);
+        put_lane(item, 1, (uint32_t)w.row0);
+        put_lane(item, 2, (uint32_t)w.rows);
+        put_lane(item, 3, (uint32_t)w.col0);
+        put_lane(item, 4, (uint32_t)w.nk);
+        put_lane(item, 5, (uint32_t)w.slice);
+        put_lane(item, 6, w.t);
         lk = __builtin_amdgcn_readfirstlane(w.kbeg);
         lend = __builtin_amdgcn_readfirstlane(w.kbeg + w.nk);
         set_operands<CF, KIND>(h, w, A, B, lane, wave);
@@ -778,7 +787,17 @@ __global__ void __launch_bounds__(CF::THREADS, CF::PER_CU) k_product(LinArgs g) 
         put_lane(keep, 13, li);
         if (cw.rows > 0) epilogue<CF, KIND>(args_again().finish, cw, acc, sw, wr, wc, lane);
         ci += gridDim.x;
-        cok = fetch<CF, KIND>(args_again(), total, ci, cw);
+        if (get_lane(keep, 12) != 0 && get_lane(keep, 13) == ci) {  // the item the loads are at
+            cw.e = (int)get_lane(item, 0);
+            cw.row0 = (int)get_lane(item, 1);
+            cw.rows = (int)get_lane(item, 2);
+            cw.col0 = (int)get_lane(item, 3);
+            cw.nk = (int)get_lane(item, 4);
+            cw.slice = (int)get_lane(item, 5);
+            cw.t = get_lane(item, 6);
+        } else {
+            cok = fetch<CF, KIND>(args_again(), total, ci, cw);
+        }
         A.unstash(keep, 0);
         B.unstash(keep, 5);
         lk = (int)get_lane(keep, 10);
