@@ -97,7 +97,6 @@ struct Operand {
     int64_t ld;
     int valid;             // KC: rows; KS: columns (from the tile's first on)
     int kc;                // contraction length
-    bool vec;              // !DMA: rows allow 16-byte loads
     int lrow, chunk, wave;
     uint32_t voff, step_off;
     __amdgpu_buffer_rsrc_t rs;
@@ -112,9 +111,9 @@ struct Operand {
     __device__ static __forceinline__ int place(int s) { return (s & ~7) | ((s & 1) << 2) | ((s >> 1) & 3); }
     __device__ static __forceinline__ int unplace(int f) { return (f & ~7) | ((f & 3) << 1) | ((f >> 2) & 1); }
 
-    __device__ __forceinline__ void init(const uint16_t* base_, int64_t ld_, int valid_, int kc_, bool vec_, int lane,
+    __device__ __forceinline__ void init(const uint16_t* base_, int64_t ld_, int valid_, int kc_, int lane,
                                          int wave_) {
-        base = base_; ld = ld_; valid = valid_; kc = kc_; vec = vec_; wave = wave_;
+        base = base_; ld = ld_; valid = valid_; kc = kc_; wave = wave_;
         const int slot = lane % SLOTS, row0 = wave * LROWS + lane / SLOTS;  // row of piece 0
         lrow = row0;
         if constexpr (KS) {
@@ -167,6 +166,18 @@ struct Operand {
     __device__ __forceinline__ void get(int kt) {
         const int64_t k0 = (int64_t)kt * BK;
         if constexpr (!DMA) {
+            // A step without ragged ends: plain loads, which run together
+            // (KC rows past the last read it again: their outputs are not
+            // stored).  Else element by element at the ends.
+            if (k0 + BK <= kc && (!KS || valid == ROWS)) {
+#pragma unroll
+                for (int q = 0; q < PIECES; ++q) {
+                    const int row = lrow + q * WAVES * LROWS;
+                    const uint16_t* p = KS ? base + (k0 + row) * ld + chunk * 8 : base + min(row, valid - 1) * ld + k0 + chunk * 8;
+                    reg[q] = *(const VE_GLOBAL u32x4_any*)(const VE_GLOBAL uint16_t*)p;
+                }
+                return;
+            }
 #pragma unroll
             for (int q = 0; q < PIECES; ++q) {
                 const int row = lrow + q * WAVES * LROWS;
@@ -179,7 +190,7 @@ struct Operand {
                     p = base + row * ld + k0 + chunk * 8;
                     cnt = row < valid ? kc - (k0 + chunk * 8) : 0;
                 }
-                reg[q] = cnt > 0 ? load_bf16x8(p, (int)(cnt < 8 ? cnt : 8), vec) : u32x4{0, 0, 0, 0};
+                reg[q] = cnt > 0 ? load_bf16x8(p, (int)(cnt < 8 ? cnt : 8), false) : u32x4{0, 0, 0, 0};
             }
         }
     }
@@ -399,13 +410,11 @@ __device__ __forceinline__ void finish8(const LinArgs& g, int e, int64_t row, in
 template <class CF, int KIND, class OpA, class OpB>
 __device__ __forceinline__ void set_operands(const LinArgs& g, const Work& w, OpA& A, OpB& B, int lane, int wave) {
     const int K = KIND == kLinDw ? w.len : (int)g.K, cols = min((int)g.N - w.col0, CF::BN);
-    const bool va = g.lda % 8 == 0 && ((uintptr_t)g.A & 15) == 0;
-    const bool vb = g.ldb % 8 == 0 && ((uintptr_t)g.B & 15) == 0 && g.b_group % 8 == 0;
-    if constexpr (KIND == kLinDw) A.init(g.A + w.begin * g.lda + w.row0, g.lda, w.rows, K, va, lane, wave);
-    else A.init(g.A + w.row0 * g.lda, g.lda, w.rows, K, va, lane, wave);
-    if constexpr (KIND == kLinFwd) B.init(g.B + w.e * g.b_group + w.col0 * g.ldb, g.ldb, cols, K, vb, lane, wave);
-    else if constexpr (KIND == kLinDx) B.init(g.B + w.e * g.b_group + w.col0, g.ldb, cols, K, vb, lane, wave);
-    else B.init(g.B + w.begin * g.ldb + w.col0, g.ldb, cols, K, vb, lane, wave);
+    if constexpr (KIND == kLinDw) A.init(g.A + w.begin * g.lda + w.row0, g.lda, w.rows, K, lane, wave);
+    else A.init(g.A + w.row0 * g.lda, g.lda, w.rows, K, lane, wave);
+    if constexpr (KIND == kLinFwd) B.init(g.B + w.e * g.b_group + w.col0 * g.ldb, g.ldb, cols, K, lane, wave);
+    else if constexpr (KIND == kLinDx) B.init(g.B + w.e * g.b_group + w.col0, g.ldb, cols, K, lane, wave);
+    else B.init(g.B + w.begin * g.ldb + w.col0, g.ldb, cols, K, lane, wave);
 }
 
 // The kernel's arguments, read from memory again.
@@ -698,8 +707,8 @@ __global__ void __launch_bounds__(CF::THREADS, CF::PER_CU) k_product(LinArgs g) 
         acc[a][b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fb[buf][b], fa[buf][a], acc[a][b], 0, 0, 0);
     };
 
-    A.init(g.A, g.lda, 1, 1, true, lane, wave);
-    B.init(g.B, g.ldb, 1, 1, true, lane, wave);
+    A.init(g.A, g.lda, 1, 1, lane, wave);
+    B.init(g.B, g.ldb, 1, 1, lane, wave);
     next_loaded(true);
     begin();
 #pragma unroll

@@ -501,7 +501,111 @@ def test_refusals_of_the_binding():
 
 
 # ---------------------------------------------------------------------------
+# sizes and strides whose offsets pass 32 bits
+
+def test_offsets_beyond_32_bits():
+    """Outputs of more than 2^31 elements (4.6 GB), checked on sampled rows;
+    the last rows lie past 2^32 bytes."""
+    import torch
+    ve = _ve()
+    T, K, N = 70001, 64, 32776
+    assert T * N > 2 ** 31
+    g = torch.Generator(device=DEV)
+    g.manual_seed(3)
+    x = torch.randn(T, K, generator=g, device=DEV).to(torch.bfloat16)
+    w = torch.randn(N, K, generator=g, device=DEV).to(torch.bfloat16)
+    y = torch.zeros(T, N, dtype=torch.bfloat16, device=DEV)
+    q = ve.new_act8(T, N, 128, DEV)
+    for kw in ({}, {"z8": q}):
+        y.zero_()
+        ve.linear_forward(x, w, y, **kw)
+        rows = [0, 1, 255, 256, 33000, 65519, 65520, 65536, 69999, 70000]
+        xs, ws = _host(x[rows]), _host(w)
+        ref, z, mag = linear.forward(xs, ws)
+        _, ey = forward_bounds(ref, z, mag, K, "none")
+        _within(_host(y[rows]), ref, ey, "y")
+    back = torch.empty_like(y)
+    ve.act8_unpack(q, back)
+    torch.cuda.synchronize()
+    got, want = back[rows].float(), y[rows].float()
+    step = q.scales[rows].repeat_interleave(128, 1)[:, :N]
+    assert bool(((got - want).abs() <= 0.5 * step * 1.001 + 2.0 ** -7 * want.abs()).all())
+    p = ve.new_act8(T, N, 128, DEV)
+    ve.act8_pack(y, p)
+    torch.cuda.synchronize()
+    codes, scales = linear.pack(_host(y[rows]).astype(np.float32), 128)
+    assert np.array_equal(p.codes[rows].cpu().numpy(), codes) and np.array_equal(p.scales[rows].cpu().numpy(), scales)
+    # dz w and dz^T x over the same rows: the contraction of 70,001 tokens against a float64 product of a column sample
+    dx, dw = torch.empty_like(x), torch.empty(N, K, dtype=torch.float32, device=DEV)
+    db = torch.empty(N, dtype=torch.float32, device=DEV)
+    y.mul_(2.0 ** -6)
+    ve.linear_backward(y, w, x=x, dx=dx, dw=dw, dbias=db)
+    cols = [0, 7, 127, 128, 16384, 32768, 32775]
+    dy, xv = _host(y[:, cols]), _host(x)
+    from linear_common import gamma
+    _within(_host(dw[cols]), dy.T @ xv, gamma(T + 34) * (np.abs(dy).T @ np.abs(xv)) + 2.0 ** -126, "dw")
+    _within(_host(db[cols]), dy.sum(0), gamma(T + 8) * np.abs(dy).sum(0) + 2.0 ** -126, "dbias")
+    dyr = _host(y[rows])
+    r = dyr @ ws
+    _within(_host(dx[rows]), r, 2.0 ** -8 * np.abs(r) + 1.01 * gamma(N + 2) * (np.abs(dyr) @ np.abs(ws)) + 2.0 ** -126, "dx")
+
+
+@pytest.mark.parametrize("ld", [2 ** 21, 2 ** 21 + 8])
+def test_long_leading_dimensions(ld):
+    """Rows 2^21 elements apart (the direct loads' limit) and just beyond it."""
+    import torch
+    ve = _ve()
+    T, K, N = 40, 64, 72
+    xb, wb, dyb = _bits((T, K), 1), _bits((N, K), 2), _bits((T, N), 3)
+    x, y, dy, dx = (torch.zeros(T, ld, dtype=torch.bfloat16, device=DEV) for _ in range(4))
+    w, dw = (torch.zeros(N, ld, dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    x[:, :K], w[:, :K], dy[:, :N] = _dev(xb), _dev(wb), _dev(dyb)
+    ve.linear_forward(x[:, :K], w[:, :K], y[:, :N], activation="silu", residual=dy[:, :N])
+    ve.linear_backward(dy[:, :N], w[:, :K], x=x[:, :K], dx=dx[:, :K], dx_add=x[:, :K], dw=dw[:, :K])
+    ref, z, mag = linear.forward(_up(xb), _up(wb), None, "silu", _up(dyb))
+    _within(_host(y[:, :N]), ref, forward_bounds(ref, z, mag, K, "silu", _up(dyb))[1], "y")
+    r = linear.backward(_up(dyb), _up(wb), _up(xb), None, "none", _up(xb))
+    b = backward_bounds(r, _up(dyb), _up(wb), _up(xb), "none", None, False, _up(xb))
+    _within(_host(dx[:, :K]), r["dx"], b["dx"], "dx")
+    _within(_host(dw[:, :K]), r["dw"], b["dw"], "dw")
+    assert not y[:, N:].any() and not dx[:, K:].any() and not dw[:, K:].any()
+
+
+# ---------------------------------------------------------------------------
 # streams, graphs, and the operators together
+
+def test_two_streams_at_once():
+    """Calls that overlap on two streams, each with its own (allocated) scratch."""
+    import torch
+    ve = _ve()
+    dy, w, args, _ = _backward_case(1100, 136, 264, None, "silu", 64, True, True, False, False, 0, 0)
+    want = {k: args[k].clone() for k in ("dx", "dw", "dbias")}
+    streams = [torch.cuda.Stream(DEV) for _ in range(2)]
+    outs = [{k: torch.full_like(v, 7) for k, v in want.items()} for _ in streams]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for s, o in zip(streams, outs):
+            ve.linear_backward(dy, w, **{**args, **o}, stream=s)
+    torch.cuda.synchronize()
+    for o in outs:
+        for k, v in want.items():
+            assert torch.equal(o[k], v), k
+
+
+def test_short_workspace_is_refused():
+    import torch
+    ve = _ve()
+    dy, w, args, _ = _backward_case(130, 264, 392, None, "silu", 0, True, False, True, False, 0, 0)
+    need = ve.linear_backward_workspace(dy, w, **args)
+    before = args["dx"].clone()
+    for ws in (torch.empty(need - 256, dtype=torch.uint8, device=DEV), torch.empty(need + 256, dtype=torch.uint8, device=DEV)[16:]):
+        args["dx"].fill_(5)
+        with pytest.raises(ve.VeError, match="workspace"):
+            ve.linear_backward(dy, w, workspace=ws, **args)
+        torch.cuda.synchronize()
+        assert bool((args["dx"] == 5).all())
+    args["dx"].copy_(before)
+
 
 def test_other_stream_and_captured_graph():
     import torch
