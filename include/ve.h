@@ -391,8 +391,12 @@ typedef enum {
  * and residual are applied in fp32 and y is rounded once.  For the backward
  * pass z can be written as bf16 (z) or in 8 bits (z8, from the fp32 values),
  * in the same pass.
+ * z8's scale and code are those of the rule above to within one unit in the
+ * last place of scale and of 127 / amax.
  * All matrices are row-major bf16 on the device with the given leading
- * dimensions (elements). */
+ * dimensions (elements).  Any alignment is correct; rows that start on 16
+ * bytes and features that are multiples of 8 are much faster.  Outputs may
+ * not overlap inputs or each other, but where noted. */
 typedef struct {
     int64_t tokens, in_features, out_features;  /* tokens >= 0 (0: no-op) */
     int32_t groups;                             /* 1 .. 65536 */
@@ -422,8 +426,8 @@ typedef struct {
  * the same results, bit for bit, as from ve_act8_unpack's output).  Any
  * output may be NULL, and then what only it needs may be NULL too: w is read
  * for dx, x for dw.  Empty groups get dw = dbias = 0 (or keep theirs with
- * accumulate).  dx, dw and dbias of a call do not depend on anything but its
- * inputs: no atomics, the same bits every call. */
+ * accumulate).  No atomics: the same inputs give the same bits every call.
+ * Outputs may not overlap inputs or each other, but where noted. */
 typedef struct {
     int64_t tokens, in_features, out_features;
     int32_t groups;
@@ -451,8 +455,8 @@ typedef struct {
  * that may overlap must not share one.  Errors of all four: NULL arguments or
  * needed pointers, sizes, groups or leading dimensions out of range (a
  * leading dimension shorter than the row, groups > 1 without offsets), an
- * unknown activation, a block other than 32, 64 or 128, a short or
- * misaligned workspace: VE_ERR_INVALID_ARG; sizes beyond one launch:
+ * unknown activation, a block other than 32, 64 or 128, y at x or dx at dy, a
+ * short or misaligned workspace: VE_ERR_INVALID_ARG; sizes beyond one launch:
  * VE_ERR_UNSUPPORTED; launch failures: VE_ERR_DEVICE. */
 ve_status ve_linear_forward_workspace(const ve_linear_forward_args* a, int64_t* bytes);
 ve_status ve_linear_forward(const ve_linear_forward_args* a, void* workspace, int64_t workspace_bytes, void* stream);

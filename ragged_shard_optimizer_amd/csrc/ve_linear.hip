@@ -124,12 +124,7 @@ struct Operand {
         }
         voff = (uint32_t)((lrow * ld + chunk * 8) * 2);
     }
-    // Direct loads of step kt's tile into the LDS stage at `st`: begin() for
-    // the step, then piece() for each piece.  A buffer resource from the
-    // step's first element on: reads past the last valid row return 0, and so
-    // do those of a KC row past the contraction (sent past the end by hand)
-    // and every read of a step past the last (kt >= nk).
-    // base, valid and kc in five lanes of a vector register, and back
+    // base, valid, kc and ld in five lanes of a vector register, and back
     __device__ __forceinline__ void stash(uint32_t& keep, int at) const {
         put_lane(keep, at, (uint32_t)(uintptr_t)base);
         put_lane(keep, at + 1, (uint32_t)((uintptr_t)base >> 32));
@@ -144,12 +139,18 @@ struct Operand {
         kc = (int)get_lane(keep, at + 3);
         ld = (int)get_lane(keep, at + 4);
     }
+    // scalars for the compiler, whatever way they were found
     __device__ __forceinline__ void make_uniform() {
         base = (const uint16_t*)uniform64((int64_t)base);
         ld = __builtin_amdgcn_readfirstlane((int)ld);
         valid = __builtin_amdgcn_readfirstlane(valid);
         kc = __builtin_amdgcn_readfirstlane(kc);
     }
+    // Direct loads of step kt's tile into the LDS stage at `st`: begin() for
+    // the step, then piece() for each piece.  A buffer resource from the
+    // step's first element on: reads past the last valid row return 0, and so
+    // do those of a KC row past the contraction (sent past the end by hand)
+    // and every read of a step that does not exist (not live).
     __device__ __forceinline__ void begin(int kt, bool live) {
         const int k0 = kt * BK, l = (int)ld;
         const uint16_t* p = KS ? base + (int64_t)k0 * l : base + k0;
@@ -332,7 +333,7 @@ __device__ __forceinline__ void bias8(const LinArgs& g, int e, int64_t col, int 
     }
 }
 
-// the switch outside the loop over the values
+// act of 8 values, the switch outside the loop over them
 __device__ __forceinline__ void activate8(int act, float* v) {
     switch (act) {
 #define VE_ACT_CASE(A)                                   \
@@ -600,6 +601,7 @@ __device__ __forceinline__ void epilogue(int finish, const Work& w, f32x16 (&acc
     else epilogue_of<CF, KIND, kFinishAll>(w, acc, sw, wr, wc, lane);
 }
 
+// Tiles of the launch; of ragged rows those that the offsets give.
 template <class CF, int KIND>
 __device__ __forceinline__ uint32_t all_tiles(const LinArgs& g) {
     if (KIND != kLinDw && g.offsets)
@@ -612,7 +614,15 @@ __device__ __forceinline__ uint32_t all_tiles(const LinArgs& g) {
 // the steps of all its items are one stream, which the loads run up to two
 // steps ahead of, so that an item's first loads land during the previous
 // item's last step and epilogue.  (With one workgroup an item, its start and
-// epilogue cost 10 us of a 256 x 256 tile, as much as 7 steps.)
+// epilogue cost 10 us of a 256 x 256 tile, as much as 7 steps; with the
+// stream, 5.)  One wave of 128 x 128 on a SIMD reads two thirds of the LDS
+// bytes an MFMA of two waves of 128 x 64, which need not meet at barriers
+// inside a step either: 1,375 against 1,166 TFLOP/s for dw at 8192^3, and
+// 1,293 where two such waves took turns at the MFMAs.
+//
+// 8192 tokens, 8192 -> 28672: forward 1,414, dx 1,358, dw 1,278 TFLOP/s
+// (library products 1,582, 1,387, 1,183).  The MFMAs are busy three quarters
+// of the cycles, at a clock that the card's power holds at 1.5 to 1.7 GHz.
 template <class CF, int KIND>
 __global__ void __launch_bounds__(CF::THREADS, CF::PER_CU) k_product(LinArgs g) {
     constexpr int TM = CF::TM, TN = CF::TN, WM = CF::WM, WN = CF::WN;

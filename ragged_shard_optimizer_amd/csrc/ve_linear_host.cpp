@@ -67,6 +67,7 @@ ve_status check_forward(const ve_linear_forward_args& a) {
     if (st != VE_OK) return st;
     if (!a.w) return fail(VE_ERR_INVALID_ARG, "w is NULL");
     if (a.tokens > 0 && (!a.x || !a.y)) return fail(VE_ERR_INVALID_ARG, "x or y is NULL");
+    if (a.tokens > 0 && (const uint16_t*)a.y == a.x) return fail(VE_ERR_INVALID_ARG, "y is x");
     const int64_t K = a.in_features, N = a.out_features;
     if (a.ldx < K || a.ldw < K || a.ldy < N || (a.residual && a.ldr < N) || (a.z && a.ldz < N))
         return fail(VE_ERR_INVALID_ARG, "leading dimension smaller than the row");
@@ -105,6 +106,7 @@ ve_status check_backward(const ve_linear_backward_args& a) {
     if (a.lddy < N) return fail(VE_ERR_INVALID_ARG, "leading dimension smaller than the row");
     if (a.dx && (a.lddx < K || (a.dx_add && a.ld_add < K)))
         return fail(VE_ERR_INVALID_ARG, "leading dimension smaller than the row");
+    if (some && a.dx && a.dx == a.dy) return fail(VE_ERR_INVALID_ARG, "dx is dy");
     if (a.dx && !a.w) return fail(VE_ERR_INVALID_ARG, "dx needs w");
     if (a.dx && a.ldw < K) return fail(VE_ERR_INVALID_ARG, "leading dimension smaller than the row");
     if (a.dx && a.groups > 1 && a.w_group < (N - 1) * a.ldw + K)

@@ -16,7 +16,7 @@ BAD, OK, UNSUP = ve.VE_ERR_INVALID_ARG, ve.VE_OK, ve.VE_ERR_UNSUPPORTED
 
 def _fwd(**kw):
     a = ve._LinearForward(tokens=8, in_features=16, out_features=24, groups=1, activation=0, x=P, ldx=16, w=P, ldw=16,
-                          y=P, ldy=24)
+                          y=2 * P, ldy=24)
     for k, v in kw.items():
         setattr(a, k, v)
     return a
@@ -24,7 +24,7 @@ def _fwd(**kw):
 
 def _bwd(**kw):
     a = ve._LinearBackward(tokens=8, in_features=16, out_features=24, groups=1, activation=0, dy=P, lddy=24, w=P,
-                           ldw=16, x=P, ldx=16, dx=P, lddx=16, dw=P, lddw=16)
+                           ldw=16, x=P, ldx=16, dx=2 * P, lddx=16, dw=P, lddw=16)
     for k, v in kw.items():
         setattr(a, k, v)
     return a
@@ -38,7 +38,7 @@ def _q(a, fn):
 
 @pytest.mark.parametrize("kw,rc", [
     ({}, OK),
-    (dict(x=None), BAD), (dict(w=None), BAD), (dict(y=None), BAD),
+    (dict(x=None), BAD), (dict(w=None), BAD), (dict(y=None), BAD), (dict(y=P), BAD),
     (dict(tokens=0, x=None, y=None), OK),
     (dict(tokens=-1), BAD), (dict(in_features=0), BAD), (dict(out_features=0), BAD),
     (dict(tokens=1 << 31), UNSUP),
@@ -71,7 +71,7 @@ def test_forward_checks(kw, rc):
     (dict(activation=4), BAD), (dict(activation=4, z=P, ldz=24), OK), (dict(activation=4, z=P, ldz=23), BAD),
     (dict(activation=4, z=P, ldz=24, z8=ve._Act8(P, 24, P, 1, 32)), BAD),
     (dict(activation=4, z8=ve._Act8(P, 24, P, 1, 32)), OK),
-    (dict(lddy=23), BAD), (dict(ldw=15), BAD), (dict(lddx=15), BAD), (dict(lddw=15), BAD), (dict(ldx=15), BAD),
+    (dict(dx=P), BAD), (dict(lddy=23), BAD), (dict(ldw=15), BAD), (dict(lddx=15), BAD), (dict(lddw=15), BAD), (dict(ldx=15), BAD),
     (dict(dx_add=P, ld_add=15), BAD),
     (dict(groups=3, offsets=P, w_group=384, dw_group=383), BAD),
     (dict(groups=3, offsets=P, w_group=383, dw_group=384), BAD),
