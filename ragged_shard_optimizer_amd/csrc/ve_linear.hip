@@ -167,18 +167,27 @@ struct Operand {
     __device__ __forceinline__ void get(int kt) {
         const int64_t k0 = (int64_t)kt * BK;
         if constexpr (!DMA) {
-            // A step without ragged ends: plain loads, which run together
-            // (KC rows past the last read it again: their outputs are not
-            // stored).  Else element by element at the ends.
-            if (k0 + BK <= kc && (!KS || valid == ROWS)) {
+            // No ragged end inside 16 bytes: plain loads, which run together.
+            // KC rows past the last read it again (their outputs are not
+            // stored); KS rows past the contraction too, and become 0.
+            if (KS ? valid == ROWS : k0 + BK <= kc) {
 #pragma unroll
                 for (int q = 0; q < PIECES; ++q) {
                     const int row = lrow + q * WAVES * LROWS;
-                    const uint16_t* p = KS ? base + (k0 + row) * ld + chunk * 8 : base + min(row, valid - 1) * ld + k0 + chunk * 8;
+                    const uint16_t* p = KS ? base + min(k0 + row, (int64_t)kc - 1) * ld + chunk * 8
+                                           : base + min(row, valid - 1) * ld + k0 + chunk * 8;
                     reg[q] = *(const VE_GLOBAL u32x4_any*)(const VE_GLOBAL uint16_t*)p;
+                }
+                if constexpr (KS) {
+                    if (k0 + BK > kc) {
+#pragma unroll
+                        for (int q = 0; q < PIECES; ++q)
+                            if (k0 + lrow + q * WAVES * LROWS >= kc) reg[q] = u32x4{0, 0, 0, 0};
+                    }
                 }
                 return;
             }
+            // else element by element at the ends
 #pragma unroll
             for (int q = 0; q < PIECES; ++q) {
                 const int row = lrow + q * WAVES * LROWS;
@@ -363,14 +372,15 @@ __device__ __forceinline__ void finish8(const LinArgs& g, int e, int64_t row, in
         const int64_t at = (int64_t)e * g.dw_group + row * g.lddw + col;
         if (g.wide) {
             VE_GLOBAL float* p = (VE_GLOBAL float*)((float*)g.dw + at);
-            if (cnt == 8 && g.vec_dw) {
+            typedef f32x4 __attribute__((aligned(4))) f32x4_any;
+            if (cnt == 8) {
                 f32x4 a = {v[0], v[1], v[2], v[3]}, b = {v[4], v[5], v[6], v[7]};
                 if (g.accumulate) {
-                    a += *(VE_GLOBAL f32x4*)p;
-                    b += *(VE_GLOBAL f32x4*)(p + 4);
+                    a += *(VE_GLOBAL f32x4_any*)p;
+                    b += *(VE_GLOBAL f32x4_any*)(p + 4);
                 }
-                *(VE_GLOBAL f32x4*)p = a;
-                *(VE_GLOBAL f32x4*)(p + 4) = b;
+                *(VE_GLOBAL f32x4_any*)p = a;
+                *(VE_GLOBAL f32x4_any*)(p + 4) = b;
             } else {
 #pragma unroll
                 for (int t = 0; t < 8; ++t)

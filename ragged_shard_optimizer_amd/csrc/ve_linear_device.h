@@ -10,8 +10,10 @@ namespace ve {
 
 __device__ __forceinline__ float bf16_up(uint16_t h) { return __uint_as_float((uint32_t)h << 16); }
 
-// bf16 elements at an address that is only 2-byte aligned, 16 bytes at once
+// 16 bytes of bf16 at an address that is only 2-byte aligned, and 8 codes at
+// any address, at once (the memory unit takes such addresses)
 typedef u32x4 __attribute__((aligned(2))) u32x4_any;
+typedef u32x2 __attribute__((aligned(1))) u32x2_any;
 
 // 8 bf16 at p (cnt of them valid, the others 0); vec: p is 16-byte aligned.
 __device__ __forceinline__ u32x4 load_bf16x8(const uint16_t* p, int cnt, bool vec) {
@@ -29,8 +31,9 @@ __device__ __forceinline__ u32x4 load_bf16x8(const uint16_t* p, int cnt, bool ve
 
 __device__ __forceinline__ void store_bf16x8(uint16_t* p, u32x4 h, int cnt, bool vec) {
     VE_GLOBAL uint16_t* q = (VE_GLOBAL uint16_t*)p;
-    if (cnt >= 8 && vec) {
-        *(VE_GLOBAL u32x4*)q = h;
+    if (cnt >= 8) {
+        if (vec) *(VE_GLOBAL u32x4*)q = h;
+        else *(VE_GLOBAL u32x4_any*)q = h;
         return;
     }
     const uint32_t w[4] = {h.x, h.y, h.z, h.w};
@@ -199,8 +202,9 @@ __device__ __forceinline__ uint32_t amax_lanes(uint32_t m, int lanes) {
 // 8 codes at p, cnt valid; vec: p is 8-byte aligned
 __device__ __forceinline__ void store_codes8(int8_t* p, u32x2 w, int cnt, bool vec) {
     VE_GLOBAL int8_t* q = (VE_GLOBAL int8_t*)p;
-    if (cnt >= 8 && vec) {
-        *(VE_GLOBAL u32x2*)q = w;
+    if (cnt >= 8) {
+        if (vec) *(VE_GLOBAL u32x2*)q = w;
+        else *(VE_GLOBAL u32x2_any*)q = w;
         return;
     }
     const uint32_t u[2] = {w.x, w.y};
@@ -210,7 +214,10 @@ __device__ __forceinline__ void store_codes8(int8_t* p, u32x2 w, int cnt, bool v
 }
 __device__ __forceinline__ u32x2 load_codes8(const int8_t* p, int cnt, bool vec) {
     const VE_GLOBAL int8_t* q = (const VE_GLOBAL int8_t*)p;
-    if (cnt >= 8 && vec) return *(const VE_GLOBAL u32x2*)q;
+    if (cnt >= 8) {
+        if (vec) return *(const VE_GLOBAL u32x2*)q;
+        return *(const VE_GLOBAL u32x2_any*)q;
+    }
     uint32_t u[2] = {0, 0};
 #pragma unroll
     for (int t = 0; t < 8; ++t)
