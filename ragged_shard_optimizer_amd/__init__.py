@@ -10,7 +10,9 @@ Names follow the C ABI: ``plan_load`` / ``Plan.query`` / ``Plan.slice`` /
 ``Plan.copy_in`` / ``Plan.step`` / ``Plan.group_op`` / ``plan_layout`` wrap
 ``ve_plan_load``, ``ve_plan_query``, ``ve_dbuffer_slice``,
 ``ve_dbuffer_copy_in``, ``ve_shard_adam8bit_step``, ``ve_dbuffer_group_op``
-and ``ve_plan_layout``.
+and ``ve_plan_layout``; ``linear_forward`` / ``linear_backward`` /
+``act8_pack`` / ``act8_unpack`` wrap the linear layer's entry points and take
+torch tensors with any row stride.
 """
 
 from __future__ import annotations
