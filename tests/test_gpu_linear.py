@@ -109,6 +109,27 @@ def test_pack_and_unpack_bit_for_bit(rows, cols, block, pad, shift):
     assert _untouched(flat, out)
 
 
+def test_scales_of_every_bf16_magnitude():
+    """One run for each positive finite bf16 value as its largest magnitude
+    (normal and subnormal), with values spread below it: scales and codes bit
+    for bit, in waves of one kind and in mixed ones."""
+    import torch
+    ve = _ve()
+    amax = np.arange(1, 0x7F80, dtype=np.uint16)
+    for order in (np.arange(len(amax)), np.random.default_rng(0).permutation(len(amax))):
+        a = bf16_bits_to_f64(amax[order])
+        v = a[:, None] * np.random.default_rng(1).uniform(-1, 1, (len(a), 32))
+        v[:, 7] = a
+        v[:, 8] = -a / 2
+        bits = f64_to_bf16_bits(v)
+        codes, scales = linear.pack(_up(bits).astype(np.float32), 32)
+        q = ve.new_act8(len(a), 32, 32, DEV)
+        ve.act8_pack(_dev(bits), q)
+        torch.cuda.synchronize()
+        assert np.array_equal(q.scales.cpu().numpy().view(np.uint32), scales.view(np.uint32))
+        assert np.array_equal(q.codes.cpu().numpy(), codes)
+
+
 def test_pack_of_non_finite_runs():
     import torch
     ve = _ve()
