@@ -233,7 +233,8 @@ ve_status ve_dbuffer_group_op(const ve_plan* plan, int32_t rank, int32_t op, flo
  *       results, slower; needs "wg_dynamic" and no pinned shape);
  *   "linear_path" (VE_LINEAR_PATH, 0): pin the form of the linear layer's
  *       products where it applies: 1 = register staged (any alignment), 2 /
- *       3 = direct-to-LDS tiles of 128 x 128 / 256 x 256, 4 = the forward
+ *       3 = direct-to-LDS tiles of 128 x 128 / 256 x 256 (rows that are not
+ *       whole 16 bytes are laid out anew in the workspace), 4 = the forward
  *       form for few tokens; 0 = chosen by shape;
  *   "linear_split" (VE_LINEAR_SPLIT, 1): 0 = never cut their contraction
  *       into slices (the options must not change between a workspace query
@@ -449,8 +450,10 @@ typedef struct {
     int32_t accumulate;                         /* add to what dw and dbias hold */
 } ve_linear_backward_args;
 
-/* Device scratch a call needs (0 is common; the arguments' sizes and which of
- * its pointers are NULL decide, nothing is read through them).  The caller
+/* Device scratch a call needs (0 is common; the arguments' sizes and strides,
+ * which of its pointers are NULL and which are 16-byte aligned decide, nothing
+ * is read through them).  Operands whose rows are not whole 16 bytes can be
+ * laid out anew in it: up to the size of x, w and dy together.  The caller
  * owns the workspace, 256-byte aligned; its contents are scratch, and calls
  * that may overlap must not share one.  Errors of all four: NULL arguments or
  * needed pointers, sizes, groups or leading dimensions out of range (a

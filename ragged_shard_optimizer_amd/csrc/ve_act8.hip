@@ -84,6 +84,35 @@ __global__ void __launch_bounds__(256) k_unpack(ve_act8 q, int64_t rows, int col
         if (cnt[k] > 0) store_bf16x8(x + row[k] * ldx + col[k], restore8(w[k], scale[k]), cnt[k], VEC);
 }
 
+// Rows of `cols` elements, any alignment, as rows of whole 16 bytes that end
+// in zeros (per: 16-byte groups of a row; rows: of one group; all: of all).
+// Bound by HBM, 4 bytes an element.
+__global__ void __launch_bounds__(256) k_pad(const uint16_t* src, int64_t ld, int64_t group, int64_t all, int64_t rows,
+                                             int cols, uint16_t* dst, int per) {
+    const int64_t first = (int64_t)blockIdx.x * (256 * kItems), row0 = first / per;
+    const uint32_t rem = (uint32_t)(first - row0 * per);
+    const int64_t e0 = row0 / rows, in0 = row0 - e0 * rows;
+    u32x4 h[kItems];
+    int64_t at[kItems];
+#pragma unroll
+    for (int k = 0; k < kItems; ++k) {
+        const uint32_t i = rem + threadIdx.x + 256 * k, r = i / (uint32_t)per;
+        const int col = (int)(i - r * per) * 8;
+        const int64_t row = row0 + r;
+        int64_t e = e0, in = in0 + r;
+        if (in >= rows) {
+            const int64_t over = in / rows;
+            e += over;
+            in -= over * rows;
+        }
+        at[k] = row < all ? row * per * 8 + col : -1;
+        if (at[k] >= 0) h[k] = load_bf16x8(src + e * group + in * ld + col, min(cols - col, 8), false);
+    }
+#pragma unroll
+    for (int k = 0; k < kItems; ++k)
+        if (at[k] >= 0) *(VE_GLOBAL u32x4*)(VE_GLOBAL uint16_t*)(dst + at[k]) = h[k];
+}
+
 // dz and column sums.  A workgroup takes a tile of kDzRows tokens of one
 // group and 512 columns: 64 lanes of 8 columns, its four waves on every
 // fourth row, each summing its rows in fp32; the four sums are joined in LDS.
@@ -121,8 +150,8 @@ __global__ void __launch_bounds__(256) k_dz(DzArgs a, int col_tiles) {
                                     a.z8.scales[row * a.z8.ld_scales + (col >> shift)]),
                            z);
 #pragma unroll
-                for (int t = 0; t < 8; ++t) d[t] *= slope(a.act, z[t]);
-                store_bf16x8(a.dz + row * a.lddz + col, narrow8(d), cnt, VEC);
+                for (int t = 0; t < 8; ++t) d[t] = VEC || t < cnt ? d[t] * slope(a.act, z[t]) : 0.f;
+                store_bf16x8(a.dz + row * a.lddz + col, narrow8(d), 8, true);  // rows of whole 16 bytes, zeros at the end
             }
 #pragma unroll
             for (int t = 0; t < 8; ++t) sum[t] += d[t];
@@ -199,6 +228,14 @@ hipError_t launch_dz(const DzArgs& a, hipStream_t s) {
         if (a.vec) hipLaunchKernelGGL((k_dz<2, true>), g, b, 0, s, a, ct);
         else hipLaunchKernelGGL((k_dz<2, false>), g, b, 0, s, a, ct);
     }
+    return hipGetLastError();
+}
+
+hipError_t launch_pad(const uint16_t* src, int64_t ld, int64_t group, int64_t E, int64_t rows, int64_t cols, uint16_t* dst,
+                      hipStream_t s) {
+    const int64_t per = (cols + 7) / 8, grid = (E * rows * per + 256 * kItems - 1) / (256 * kItems);
+    if (grid == 0) return hipSuccess;
+    hipLaunchKernelGGL(k_pad, dim3((unsigned)grid), dim3(256), 0, s, src, ld, group, E * rows, rows, (int)cols, dst, (int)per);
     return hipGetLastError();
 }
 

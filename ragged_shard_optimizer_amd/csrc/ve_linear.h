@@ -39,6 +39,9 @@ struct LinArgs {
     int32_t wide, accumulate;                 // fp32 instead of bf16; add to what dw holds
     // 16-byte accesses allowed on rows of these
     bool vec_bias, vec_res, vec_y, vec_z, vec_z8, vec_dw;
+    // rows of A / B go on for whole 16 bytes (in the workspace), with zeros
+    // where the contiguous dimension is the contraction
+    bool pad_a, pad_b;
     // set by the launcher
     int32_t finish;                           // which epilogue
     int32_t tiles_n, ksplit;
@@ -47,7 +50,7 @@ struct LinArgs {
 };
 
 // How a product runs: tile form and slices of the contraction.
-struct LinPlan { int path; int ksplit; int64_t partial_bytes; };
+struct LinPlan { int path; int ksplit; int64_t partial_bytes; double us; };  // us: the time model's estimate
 LinPlan plan_product(const LinArgs& g, LinKind kind);
 hipError_t launch_product(LinArgs g, LinKind kind, const LinPlan& p, hipStream_t s);
 
@@ -72,6 +75,10 @@ hipError_t launch_dz(const DzArgs& a, hipStream_t s);
 hipError_t launch_dbias(const DzArgs& a, void* dbias, int64_t group, bool wide, bool accumulate, hipStream_t s);
 
 hipError_t launch_act8_pack(const uint16_t* x, int64_t ldx, int64_t rows, int64_t cols, const ve_act8& q, hipStream_t s);
+// rows x cols of each of E groups (ld and group: source strides) one after the
+// other into dst, whose rows of `cols` rounded up to 8 end in zeros.
+hipError_t launch_pad(const uint16_t* src, int64_t ld, int64_t group, int64_t E, int64_t rows, int64_t cols, uint16_t* dst,
+                      hipStream_t s);
 hipError_t launch_act8_unpack(const ve_act8& q, int64_t rows, int64_t cols, uint16_t* x, int64_t ldx, hipStream_t s);
 
 }  // namespace ve

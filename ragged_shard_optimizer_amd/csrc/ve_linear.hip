@@ -417,15 +417,18 @@ __device__ __forceinline__ void finish8(const LinArgs& g, int e, int64_t row, in
     }
 }
 
-// The operands of one work item.
-template <class CF, int KIND, class OpA, class OpB>
+// The operands of one work item.  With direct loads, contiguous dimensions
+// are rounded up to whole 16 bytes, whose rest is 0 or whose product is not
+// stored (dma_ok).
+template <class CF, int KIND, bool DMA, class OpA, class OpB>
 __device__ __forceinline__ void set_operands(const LinArgs& g, const Work& w, OpA& A, OpB& B, int lane, int wave) {
     const int K = KIND == kLinDw ? w.len : (int)g.K, cols = min((int)g.N - w.col0, CF::BN);
-    if constexpr (KIND == kLinDw) A.init(g.A + w.begin * g.lda + w.row0, g.lda, w.rows, K, lane, wave);
-    else A.init(g.A + w.row0 * g.lda, g.lda, w.rows, K, lane, wave);
-    if constexpr (KIND == kLinFwd) B.init(g.B + w.e * g.b_group + w.col0 * g.ldb, g.ldb, cols, K, lane, wave);
-    else if constexpr (KIND == kLinDx) B.init(g.B + w.e * g.b_group + w.col0, g.ldb, cols, K, lane, wave);
-    else B.init(g.B + w.begin * g.ldb + w.col0, g.ldb, cols, K, lane, wave);
+    auto up = [](int n) { return DMA ? (n + 7) & ~7 : n; };
+    if constexpr (KIND == kLinDw) A.init(g.A + w.begin * g.lda + w.row0, g.lda, up(w.rows), K, lane, wave);
+    else A.init(g.A + w.row0 * g.lda, g.lda, w.rows, up(K), lane, wave);
+    if constexpr (KIND == kLinFwd) B.init(g.B + w.e * g.b_group + w.col0 * g.ldb, g.ldb, cols, up(K), lane, wave);
+    else if constexpr (KIND == kLinDx) B.init(g.B + w.e * g.b_group + w.col0, g.ldb, up(cols), K, lane, wave);
+    else B.init(g.B + w.begin * g.ldb + w.col0, g.ldb, up(cols), K, lane, wave);
 }
 
 // The kernel's arguments, read from memory again.
@@ -683,7 +686,7 @@ __global__ void __launch_bounds__(CF::THREADS, CF::PER_CU) k_product(LinArgs g) 
         put_lane(item, 6, w.t);
         lk = __builtin_amdgcn_readfirstlane(w.kbeg);
         lend = __builtin_amdgcn_readfirstlane(w.kbeg + w.nk);
-        set_operands<CF, KIND>(h, w, A, B, lane, wave);
+        set_operands<CF, KIND, true>(h, w, A, B, lane, wave);
         A.make_uniform();
         B.make_uniform();
     };
@@ -839,7 +842,9 @@ __global__ void __launch_bounds__(CF::THREADS, CF::PER_CU) k_product(LinArgs g) 
     __builtin_amdgcn_s_waitcnt(kWaitAll);
 }
 
-// One item a workgroup, through registers: operands of any alignment.
+// One item a workgroup, through registers: operands of any alignment, where
+// laying them out anew would take longer than it saves (calls of tens of
+// microseconds, weights of many groups).
 template <class CF, int KIND>
 __global__ void __launch_bounds__(CF::THREADS, CF::PER_CU) k_product_any(LinArgs g) {
     constexpr int TM = CF::TM, TN = CF::TN, WM = CF::WM, WN = CF::WN;
@@ -850,7 +855,7 @@ __global__ void __launch_bounds__(CF::THREADS, CF::PER_CU) k_product_any(LinArgs
     if (!fetch<CF, KIND>(g, all_tiles<CF, KIND>(g), blockIdx.x, w) || w.rows == 0) return;
     Operand<KIND == kLinDw, CF::BM, CF::WAVES, false> A;
     Operand<KIND != kLinFwd, CF::BN, CF::WAVES, false> B;
-    set_operands<CF, KIND>(g, w, A, B, lane, wave);
+    set_operands<CF, KIND, false>(g, w, A, B, lane, wave);
     f32x16 acc[TM][TN];
 #pragma unroll
     for (int a = 0; a < TM; ++a)
@@ -1059,13 +1064,14 @@ hipError_t launch_kind(LinArgs g, int ksplit, hipStream_t s) {
 bool aligned16(const void* p) { return ((uintptr_t)p & 15) == 0; }
 
 // Direct loads: 16-byte operand rows, the contiguous dimensions whole 16-byte
-// groups, and a tile's rows within 32-bit byte offsets.
+// groups (or padded to them), and a tile's rows within 32-bit byte offsets.
 bool dma_ok(const LinArgs& g, LinKind kind) {
     const int64_t kMaxLd = int64_t(1) << 21;
     if (!aligned16(g.A) || !aligned16(g.B) || g.lda % 8 || g.ldb % 8 || g.lda > kMaxLd || g.ldb > kMaxLd) return false;
     if (kind != kLinDw && g.b_group % 8) return false;
-    if (kind == kLinDw) return g.M % 8 == 0 && g.N % 8 == 0;
-    return g.K % 8 == 0 && (kind == kLinFwd || g.N % 8 == 0);
+    if (kind == kLinDw) return (g.M % 8 == 0 || g.pad_a) && (g.N % 8 == 0 || g.pad_b);
+    if (kind == kLinDx) return (g.K % 8 == 0 || g.pad_a) && (g.N % 8 == 0 || g.pad_b);
+    return g.K % 8 == 0 || (g.pad_a && g.pad_b);
 }
 
 template <int KIND>
@@ -1089,25 +1095,40 @@ hipError_t launch_path(const LinArgs& g, const LinPlan& p, hipStream_t s) {
 // one launch more (4 us).  Against measurements, 128^2 / 256^2 in us: 4001
 // tokens 2880 -> 5760 dx 141 / 127 (model 143 / 133), dw 157 / 179 (163 /
 // 189); 2049 tokens 4096 -> 2880 forward 59 (62).
-double product_us(bool big, int64_t items, int64_t steps, int64_t bytes) {
+// us: a step of two 128 x 128 tiles, of a single one, their start and
+// epilogue, those of a 256 x 256 tile
+struct TileCost { double pair, one, start, start256; };
+constexpr TileCost kDirect{0.9, 0.6, 4, 5};
+// Columns that are not whole 16 bytes take the epilogue of every case, which
+// one workgroup a CU hides less than two (dw of 4099 x 4101 over one token:
+// 41 us in 256 x 256 tiles, 28 in 128 x 128).
+constexpr TileCost kDirectOdd{0.9, 0.6, 5.5, 14};
+// The register-staged form, by kind: fitted to 13 shapes of rows that are not
+// 16-byte multiples (the products' order is their cost: dw transposes both
+// operands).  8192 tokens 8190 -> 8190: 2390 / 3031 / 6347 us, with operands
+// laid out anew and direct loads 913 / 906 / 905; 33 tokens 4101 -> 2051
+// 24 / 33 / 20 against 33 / 33 / 25.
+constexpr TileCost kStaged[3] = {{2.2, 1.2, 8, 0}, {3.6, 2.4, 12, 0}, {5, 3.4, 8, 0}};
+
+double product_us(bool big, int64_t items, int64_t steps, int64_t bytes, const TileCost& c) {
     const double n = (double)((items + kCUs - 1) / kCUs), st = (double)steps;
     const double sums = bytes ? (double)bytes * 2 / 5e6 + 4 : 0;
-    if (big) return n * (1.42 * st + 5) + sums;
+    if (big) return n * (1.42 * st + c.start256) + sums;
     const double pairs = (double)((int64_t)n / 2), one = n - 2 * pairs;
-    return pairs * (0.9 * st + 4) + one * (0.6 * st + 4) + sums;
+    return pairs * (c.pair * st + c.start) + one * (c.one * st + c.start) + sums;
 }
 
 }  // namespace
 
 LinPlan plan_product(const LinArgs& g, LinKind kind) {
-    LinPlan p{kPathGeneral, 1, 0};
+    LinPlan p{kPathGeneral, 1, 0, 0};
     const int64_t pin = option(kOptLinearPath);
     // Up to 8 tokens the few-token form is faster (us, 8192 -> 28672 one token
     // 89 against 131 of the tiles; 8192 -> 1024 14 against 19), at 16 the
     // tiles split along the contraction are (8192 -> 8192: 35 against 37).
     // Ragged groups stay with the tiles, which stream 32 groups' weights at
     // 5.6 TB/s with one token or 16 in each.
-    const bool few = kind == kLinFwd && !g.offsets && !g.z8.codes && dma_ok(g, kind);
+    const bool few = kind == kLinFwd && !g.offsets && !g.z8.codes && g.K % 8 == 0 && dma_ok(g, kind);
     if (few && g.T <= kFewTokens && (pin == kPathAuto || pin == kPathFew)) {
         p.path = kPathFew;
         return p;
@@ -1123,13 +1144,15 @@ LinPlan plan_product(const LinArgs& g, LinKind kind) {
         const int64_t slots = kCUs * (path == kPath256 ? Cfg256::PER_CU : Cfg128::PER_CU), area = path == kPath256 ? 65536 : 16384;
         for (int64_t ks = 1; ks <= 32; ++ks) {
             if (ks > 1 && (!may_split || nk / ks < 4 || tiles * ks > slots)) break;
-            double us = product_us(path == kPath256, tiles * ks, (nk + ks - 1) / ks, ks > 1 ? tiles * ks * area * 4 : 0);
+            double us = product_us(path == kPath256, tiles * ks, (nk + ks - 1) / ks, ks > 1 ? tiles * ks * area * 4 : 0,
+                                   !dma ? kStaged[kind] : g.N % 8 ? kDirectOdd : kDirect);
             // runs of 128 columns saved from 128 x 128 tiles need waves of 32 x
             // 128, which take 1.5 times as long (16384 tokens of 32 experts
             // 7168 -> 2048: 852 us against 577)
             if (path == kPath128 && ks == 1 && kind == kLinFwd && g.z8.codes && g.z8.block > Cfg128::WN) us *= 1.5;
             if (best == 0 || us < best) {
                 best = us;
+                p.us = us;
                 p.path = dma ? path : (int)kPathGeneral;
                 p.ksplit = (int)ks;
                 p.partial_bytes = ks > 1 ? ks * tiles * area * 4 : 0;

@@ -8,6 +8,8 @@
 //   2. dbias from the sums;
 //   3. dx = dz w;
 //   4. x restored into the workspace if it comes in 8 bits, then dw = dz^T x.
+// Operands that direct loads cannot take are laid out anew in the workspace
+// before their product, if the time model says so (plan_copies).
 
 #include <hip/hip_runtime.h>
 
@@ -97,6 +99,86 @@ LinArgs forward_product(const ve_linear_forward_args& a) {
     return g;
 }
 
+int64_t up8(int64_t n) { return (n + 7) / 8 * 8; }
+
+// Operands of a product that direct loads cannot take are laid out anew, in
+// rows of whole 16 bytes, where that and the direct form together take less
+// time than the register-staged form.  A copy moves its bytes twice, at 4
+// TB/s, by one launch.  8192 tokens, 8190 -> 8190: forward 2390 -> 920 us, dx
+// 3030 -> 910, dw 6340 -> 915; 16 groups of 6 tokens 2046 -> 2046 forward
+// keep the other form (47 us against 88: the copies are of all weights).
+struct Copy {
+    const uint16_t* src; int64_t ld, group, E, rows, cols;
+    double elems() const { return (double)E * (double)rows * (double)up8(cols); }
+    int64_t bytes() const { return E * rows * up8(cols) * 2; }  // once elems() fits a launch
+    double us() const { return E ? 4 + elems() * 4 / 4e6 : 0; }
+};
+struct Copies { Copy a, b; };
+
+// The product g with the operands that need it laid out anew (addresses are
+// set by the caller), or g itself; its plan.
+// x restored from 8 bits is charged like a copy, so that the choice, and with
+// it every bit of dw, is that of the same x in bf16.
+LinPlan plan_copies(LinArgs& g, LinKind kind, Copies& c) {
+    c = Copies{};
+    const LinPlan plain = plan_product(g, kind);
+    const int64_t pin = option(kOptLinearPath);
+    if (plain.path != kPathGeneral || pin == kPathGeneral) return plain;
+    const int64_t a_cols = kind == kLinDw ? g.M : g.K, b_cols = kind == kLinFwd ? g.K : g.N;
+    const int64_t b_rows = kind == kLinFwd ? g.N : kind == kLinDx ? g.K : g.T, b_groups = kind == kLinDw ? 1 : g.E;
+    LinArgs p = g;
+    if (!g.pad_a && (!vec16(g.A, g.lda) || a_cols % 8)) {
+        c.a = Copy{g.A, g.lda, 0, 1, g.T, a_cols};
+        p.A = (const uint16_t*)(uintptr_t)256; p.lda = up8(a_cols); p.pad_a = true;
+    }
+    double b_us = 0;
+    if (g.pad_b) b_us = Copy{g.B, g.ldb, 0, b_groups, b_rows, b_cols}.us();
+    else if (!vec16(g.B, g.ldb) || g.b_group % 8 || b_cols % 8) {
+        c.b = Copy{g.B, g.ldb, g.b_group, b_groups, b_rows, b_cols};
+        b_us = c.b.us();
+        p.B = (const uint16_t*)(uintptr_t)256; p.ldb = up8(b_cols); p.pad_b = true;
+        if (b_groups > 1) p.b_group = b_rows * p.ldb;
+    }
+    const LinPlan fast = plan_product(p, kind);
+    const bool pinned = pin == kPath128 || pin == kPath256;
+    const double most = (double)kMaxWorkgroups * 8192;  // elements of one copying launch
+    const bool fits = c.a.elems() <= most && c.b.elems() <= most;
+    if (fast.path == kPathGeneral || !fits || (!pinned && fast.us + c.a.us() + b_us >= plain.us)) {
+        c = Copies{};
+        return plain;
+    }
+    g = p;
+    return fast;
+}
+
+ve_status run_copy(const Copy& c, const uint16_t* to, hipStream_t s) {
+    if (!c.src) return VE_OK;
+    return status_of(launch_pad(c.src, c.ld, c.group, c.E, c.rows, c.cols, (uint16_t*)to, s), "operand layout");
+}
+
+// What a forward call launches, and where its scratch lies.
+struct Forward {
+    LinArgs g;
+    LinPlan p;
+    Copies c;
+    int64_t total;
+};
+
+void plan_forward(const ve_linear_forward_args& a, char* ws, Forward& f) {
+    f.g = forward_product(a);
+    f.p = plan_copies(f.g, kLinFwd, f.c);
+    int64_t at = round256(f.p.partial_bytes);
+    auto carve = [&](const Copy& c, const uint16_t*& to) {
+        if (!c.src) return;
+        if (ws) to = (const uint16_t*)(ws + at);
+        at += round256(c.bytes());
+    };
+    carve(f.c.a, f.g.A);
+    carve(f.c.b, f.g.B);
+    f.g.partial = (float*)ws;
+    f.total = at;
+}
+
 ve_status check_backward(const ve_linear_backward_args& a) {
     ve_status st = check_shape(a.tokens, a.in_features, a.out_features, a.groups, a.offsets, a.activation);
     if (st != VE_OK) return st;
@@ -137,6 +219,7 @@ struct Backward {
     DzArgs dz;
     LinArgs dx, dw;
     LinPlan pdx, pdw;
+    Copies cdx, cdw;
     int64_t dz_at, sums_at, x_at, partial_at, total;
 };
 
@@ -176,6 +259,7 @@ void plan_backward(const ve_linear_backward_args& a, char* ws, Backward& b) {
     g.y = a.dx; g.ldy = a.lddx;
     g.vec_res = vec16(a.dx_add, a.ld_add);
     g.vec_y = vec16(a.dx, a.lddx);
+    g.pad_a = act;
     b.dx = g;
     g = LinArgs{};
     g.A = dz; g.lda = lddz;
@@ -184,9 +268,25 @@ void plan_backward(const ve_linear_backward_args& a, char* ws, Backward& b) {
     g.dw = a.dw; g.lddw = a.lddw; g.dw_group = a.groups > 1 ? a.dw_group : 0;
     g.wide = a.grad_fp32 != 0; g.accumulate = a.accumulate != 0;
     g.vec_dw = aligned(a.dw, 16) && a.lddw % 8 == 0 && g.dw_group % 8 == 0;
+    g.pad_a = act;
+    g.pad_b = restore;
     b.dw = g;
-    b.pdx = a.dx && T > 0 ? plan_product(b.dx, kLinDx) : LinPlan{kPathGeneral, 1, 0};
-    b.pdw = a.dw ? plan_product(b.dw, kLinDw) : LinPlan{kPathGeneral, 1, 0};
+    b.pdx = b.pdw = LinPlan{kPathGeneral, 1, 0, 0};
+    b.cdx = b.cdw = Copies{};
+    if (a.dx && T > 0) b.pdx = plan_copies(b.dx, kLinDx, b.cdx);
+    if (a.dw) b.pdw = T > 0 ? plan_copies(b.dw, kLinDw, b.cdw) : plan_product(b.dw, kLinDw);
+    auto place = [&](const Copy& c, const uint16_t*& to) {
+        if (c.src) to = in_ws(carve(true, c.bytes()));
+    };
+    place(b.cdx.a, b.dx.A);
+    place(b.cdx.b, b.dx.B);
+    // dy is laid out once for both products
+    if (b.cdw.a.src && b.cdx.a.src) {
+        b.dw.A = b.dx.A;
+        b.cdw.a.src = nullptr;
+    }
+    place(b.cdw.a, b.dw.A);
+    place(b.cdw.b, b.dw.B);
     const int64_t partial = std::max(b.pdx.partial_bytes, b.pdw.partial_bytes);
     b.partial_at = carve(partial > 0, partial);
     b.dx.partial = b.dw.partial = (float*)in_ws(b.partial_at);
@@ -233,7 +333,11 @@ ve_status ve_act8_unpack(const ve_act8* in, int64_t rows, int64_t cols, uint16_t
 ve_status ve_linear_forward_workspace(const ve_linear_forward_args* a, int64_t* bytes) {
     if (!a || !bytes) return fail(VE_ERR_INVALID_ARG, "arguments or bytes is NULL");
     if (const ve_status st = check_forward(*a); st != VE_OK) return st;
-    *bytes = a->tokens > 0 ? plan_product(forward_product(*a), kLinFwd).partial_bytes : 0;
+    *bytes = 0;
+    if (a->tokens == 0) return VE_OK;
+    Forward f;
+    plan_forward(*a, nullptr, f);
+    *bytes = f.total;
     return VE_OK;
 }
 
@@ -241,12 +345,14 @@ ve_status ve_linear_forward(const ve_linear_forward_args* a, void* workspace, in
     if (!a) return fail(VE_ERR_INVALID_ARG, "arguments are NULL");
     if (const ve_status st = check_forward(*a); st != VE_OK) return st;
     if (a->tokens == 0) return VE_OK;
-    LinArgs g = forward_product(*a);
-    const LinPlan p = plan_product(g, kLinFwd);
-    if (const ve_status st = check_workspace(workspace, workspace_bytes, p.partial_bytes); st != VE_OK) return st;
-    g.partial = (float*)workspace;
+    Forward f;
+    plan_forward(*a, (char*)workspace, f);
+    ve_status st = check_workspace(workspace, workspace_bytes, f.total);
+    if (st != VE_OK) return st;
+    hipStream_t s = (hipStream_t)stream;
     (void)hipGetLastError();
-    return status_of(launch_product(g, kLinFwd, p, (hipStream_t)stream), "forward product");
+    if ((st = run_copy(f.c.a, f.g.A, s)) != VE_OK || (st = run_copy(f.c.b, f.g.B, s)) != VE_OK) return st;
+    return status_of(launch_product(f.g, kLinFwd, f.p, s), "forward product");
 }
 
 ve_status ve_linear_backward_workspace(const ve_linear_backward_args* a, int64_t* bytes) {
@@ -274,6 +380,7 @@ ve_status ve_linear_backward(const ve_linear_backward_args* a, void* workspace, 
                                                  a->accumulate != 0, s),
                                     "dbias")) != VE_OK)
         return st;
+    if ((st = run_copy(b.cdx.a, b.dx.A, s)) != VE_OK || (st = run_copy(b.cdx.b, b.dx.B, s)) != VE_OK) return st;
     if (a->dx && a->tokens > 0 && (st = status_of(launch_product(b.dx, kLinDx, b.pdx, s), "dx product")) != VE_OK)
         return st;
     if (!a->dw) return VE_OK;
@@ -281,6 +388,7 @@ ve_status ve_linear_backward(const ve_linear_backward_args* a, void* workspace, 
         (st = status_of(launch_act8_unpack(a->x8, a->tokens, a->in_features, (uint16_t*)b.dw.B, b.dw.ldb, s),
                         "restore")) != VE_OK)
         return st;
+    if ((st = run_copy(b.cdw.a, b.dw.A, s)) != VE_OK || (st = run_copy(b.cdw.b, b.dw.B, s)) != VE_OK) return st;
     return status_of(launch_product(b.dw, kLinDw, b.pdw, s), "dw product");
 }
 

@@ -745,3 +745,125 @@ def test_layer_gradients_into_a_bucket_and_step():
         moved = (st["master"] - master).abs()
         assert bool((moved[bucket[rank * S:(rank + 1) * S] != 0] > 0).all())
     plan.close()
+
+
+# ---------------------------------------------------------------------------
+# rows that are not whole 16 bytes: operands laid out anew in the workspace
+
+LAID_OUT_FORWARD = [
+    (65, 2053, 139, None, "silu", True, False, False, 128, 0, 0),
+    (200, 1091, 397, None, "gelu", True, True, True, 64, 3, 1),
+    (300, 136, 520, None, "none", False, True, False, 0, 4, 4),      # whole rows at addresses that are not
+    (130, 1, 257, None, "relu", False, False, False, 0, 0, 0),
+    (333, 99, 75, 7, "silu", True, True, True, 32, 3, 1),
+    (700, 63, 135, 70, "none", True, False, False, 0, 0, 0),
+]
+LAID_OUT_BACKWARD = [
+    (1100, 135, 263, None, "silu", 64, True, True, False, True, 0, 0),
+    (130, 263, 1091, None, "none", 0, True, False, True, False, 1, 3),
+    (129, 264, 75, None, "gelu", 128, True, False, True, False, 0, 0),  # out_features alone is odd
+    (129, 99, 136, None, "none", 0, True, True, False, False, 0, 0),    # in_features alone is odd
+    (300, 136, 264, None, "relu", 0, True, False, False, False, 4, 4),
+    (333, 261, 397, 7, "gelu", 128, True, True, False, False, 0, 0),
+    (700, 63, 135, 70, "none", 0, True, False, False, True, 2, 1),
+]
+
+
+def _poison(bytes_):
+    """A workspace whose every bf16 and fp32 is NaN."""
+    import torch
+    return torch.full((bytes_ or 1,), 255, dtype=torch.uint8, device=DEV)
+
+
+@pytest.mark.parametrize("path,split", [(2, 0), (2, 1), (3, 0), (3, 1)])
+@pytest.mark.parametrize("case", LAID_OUT_FORWARD, ids=lambda c: "-".join(map(str, c)))
+def test_forward_of_rows_laid_out_anew(case, path, split):
+    import torch
+    ve = _ve()
+    print(f"[gpu] forward {case} path {path} split {split}", flush=True)
+    with ve.options(linear_path=path, linear_split=split):
+        x, w, y, args, _ = _forward_case(*case)
+        want = y.clone()
+        y.fill_(7)
+        need = ve.linear_forward_workspace(x, w, y, **args)
+        assert need > 0
+        ve.linear_forward(x, w, y, workspace=_poison(need), **args)
+        torch.cuda.synchronize()
+        assert torch.equal(y, want)
+
+
+@pytest.mark.parametrize("path,split", [(2, 0), (2, 1), (3, 0), (3, 1)])
+@pytest.mark.parametrize("case", LAID_OUT_BACKWARD, ids=lambda c: "-".join(map(str, c)))
+def test_backward_of_rows_laid_out_anew(case, path, split):
+    import torch
+    ve = _ve()
+    print(f"[gpu] backward {case} path {path} split {split}", flush=True)
+    with ve.options(linear_path=path, linear_split=split):
+        dy, w, args, _ = _backward_case(*case)
+        args["accumulate"] = False
+        outs = ("dx", "dw", "dbias")
+        ve.linear_backward(dy, w, **args)
+        want = {k: args[k].clone() for k in outs}
+        for k in outs:
+            args[k].fill_(7)
+        need = ve.linear_backward_workspace(dy, w, **args)
+        assert need > 0
+        ve.linear_backward(dy, w, workspace=_poison(need), **args)
+        torch.cuda.synchronize()
+        inside = slice(None)
+        if args["offsets"] is not None:
+            off = args["offsets"].tolist()
+            inside = slice(off[0], off[-1])
+        assert torch.equal(args["dx"][inside], want["dx"][inside])
+        for k in ("dw", "dbias"):
+            assert torch.equal(args[k], want[k]), k
+
+
+@pytest.mark.parametrize("case", [
+    (2051, 1037, 1203, None, "gelu", 64, True, False, False, False, 0, 0),
+    (130, 263, 521, None, "silu", 32, True, False, False, False, 0, 0),
+    (333, 261, 397, 7, "silu", 128, True, False, True, False, 0, 0),
+], ids=lambda c: "-".join(map(str, c)))
+def test_odd_backward_from_8_bits_equals_from_restored(case):
+    import torch
+    ve = _ve()
+    dy, w, args, (rx, rz) = _backward_case(*case)
+    got = {k: args[k].clone() for k in ("dx", "dw", "dbias")}
+    ve.linear_backward(dy, w, **{**args, "x": rx, "z": rz})
+    torch.cuda.synchronize()
+    for k, v in got.items():
+        assert torch.equal(v, args[k]), k
+
+
+def test_rows_laid_out_anew_in_a_captured_graph():
+    import torch
+    ve = _ve()
+    with ve.options(linear_path=2):
+        x, w, y, fargs, _ = _forward_case(200, 1091, 397, None, "gelu", True, False, False, 0, 3, 1)
+        dy, w2, args, _ = _backward_case(130, 263, 1091, None, "none", 0, True, False, True, False, 1, 3)
+        outs = [y] + [args[k] for k in ("dx", "dw", "dbias")]
+        want = [t.clone() for t in outs]
+        fws, bws = _poison(ve.linear_forward_workspace(x, w, y, **fargs)), _poison(ve.linear_backward_workspace(dy, w2, **args))
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            ve.linear_forward(x, w, y, workspace=fws, **fargs)
+            ve.linear_backward(dy, w2, workspace=bws, **args)
+        for _ in range(3):
+            for t in outs:
+                t.fill_(1)
+            g.replay()
+            torch.cuda.synchronize()
+            assert all(torch.equal(a, b) for a, b in zip(outs, want))
+            ve.linear_forward(x, w, y, **fargs)
+            ve.linear_backward(dy, w2, **args)
+            torch.cuda.synchronize()
+            assert all(torch.equal(a, b) for a, b in zip(outs, want))
+        # what the operands hold at the replay counts, not at the capture
+        x.mul_(2)
+        ve.linear_forward(x, w, y, **fargs)
+        torch.cuda.synchronize()
+        twice = y.clone()
+        y.fill_(1)
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y, twice) and not torch.equal(y, want[0])

@@ -137,3 +137,21 @@ def test_binding_refuses_host_tensors_and_bad_names():
         ve.act8_pack(x, ve.new_act8(4, 8, device="cpu"))
     with pytest.raises(ValueError, match="1-D int64"):
         ve.linear_forward(x, w, y, offsets=torch.zeros(2, dtype=torch.int32))
+
+
+def test_workspace_of_rows_laid_out_anew():
+    L = ve.lib()
+    big = dict(tokens=4096, in_features=4097, out_features=4099, ldx=4097, ldw=4097, ldy=4099)
+    rc, need = _q(_fwd(**big), L.ve_linear_forward_workspace)
+    assert rc == OK and need >= (4096 + 4099) * 4104 * 2
+    whole = dict(tokens=4096, in_features=4096, out_features=4096, ldx=4096, ldw=4096, ldy=4096)
+    rc, need = _q(_fwd(**whole), L.ve_linear_forward_workspace)
+    assert rc == OK and need == 0
+    with ve.options(linear_path=1):
+        rc, need = _q(_fwd(**big), L.ve_linear_forward_workspace)
+        assert rc == OK and need == 0
+    # an operand too large for one copying launch is read where it lies
+    top = (1 << 31) - 1
+    rc, need = _q(_fwd(tokens=1, in_features=top, out_features=1 << 20, ldx=top, ldw=top, ldy=1 << 20),
+                  L.ve_linear_forward_workspace)
+    assert rc == OK and need < 1 << 40
