@@ -136,27 +136,33 @@ __global__ void __launch_bounds__(256) k_dz(DzArgs a, int col_tiles) {
     const int cnt = a.N - col < 8 ? (int)(a.N - col) : 8;
     float sum[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
     const int shift = ZMODE == 2 ? __builtin_ctz(a.z8.block) : 0;
-    if (cnt > 0) {
+    // n: the lane's columns, a constant for all but the row's last lane, so
+    // that a lane's loads of several rows run together (8192 x 8190 with bf16
+    // z: 131 us; 195 with the row's end tested at every load)
+    auto rows_of = [&](auto n_of) {
 #pragma unroll 4
         for (int64_t i = wave; i < rows; i += 4) {
+            const int n = n_of();
             const int64_t row = begin + i;
             float d[8];
-            widen8(load_bf16x8(a.dy + row * a.lddy + col, cnt, VEC), d);
+            widen8(load_bf16x8(a.dy + row * a.lddy + col, n, VEC), d);
             if constexpr (ZMODE != 0) {
                 float z[8];
-                if constexpr (ZMODE == 1) widen8(load_bf16x8(a.z + row * a.ldz + col, cnt, VEC), z);
+                if constexpr (ZMODE == 1) widen8(load_bf16x8(a.z + row * a.ldz + col, n, VEC), z);
                 else
-                    widen8(restore8(load_codes8(a.z8.codes + row * a.z8.ld_codes + col, cnt, VEC),
+                    widen8(restore8(load_codes8(a.z8.codes + row * a.z8.ld_codes + col, n, VEC),
                                     a.z8.scales[row * a.z8.ld_scales + (col >> shift)]),
                            z);
 #pragma unroll
-                for (int t = 0; t < 8; ++t) d[t] = VEC || t < cnt ? d[t] * slope(a.act, z[t]) : 0.f;
+                for (int t = 0; t < 8; ++t) d[t] = t < n ? d[t] * slope(a.act, z[t]) : 0.f;
                 store_bf16x8(a.dz + row * a.lddz + col, narrow8(d), 8, true);  // rows of whole 16 bytes, zeros at the end
             }
 #pragma unroll
             for (int t = 0; t < 8; ++t) sum[t] += d[t];
         }
-    }
+    };
+    if (cnt >= 8) rows_of([] { return 8; });
+    else if (cnt > 0) rows_of([cnt] { return cnt; });
     if (!a.sums) return;
     __shared__ float part[4][512];
 #pragma unroll
