@@ -117,14 +117,17 @@ struct Copies { Copy a, b; };
 
 // The product g with the operands that need it laid out anew (addresses are
 // set by the caller), or g itself; its plan.
-// x restored from 8 bits is charged like a copy, so that the choice, and with
-// it every bit of dw, is that of the same x in bf16.
+// x restored from 8 bits is weighed like the same x in bf16 (without its
+// padding at first, then charged like a copy), so that the choice, and with it
+// every bit of dw, is the same.
 LinPlan plan_copies(LinArgs& g, LinKind kind, Copies& c) {
     c = Copies{};
-    const LinPlan plain = plan_product(g, kind);
+    const int64_t a_cols = kind == kLinDw ? g.M : g.K, b_cols = kind == kLinFwd ? g.K : g.N;
+    LinArgs as_is = g;
+    as_is.pad_b = g.pad_b && b_cols % 8 == 0;
+    const LinPlan plain = plan_product(as_is, kind);
     const int64_t pin = option(kOptLinearPath);
     if (plain.path != kPathGeneral || pin == kPathGeneral) return plain;
-    const int64_t a_cols = kind == kLinDw ? g.M : g.K, b_cols = kind == kLinFwd ? g.K : g.N;
     const int64_t b_rows = kind == kLinFwd ? g.N : kind == kLinDx ? g.K : g.T, b_groups = kind == kLinDw ? 1 : g.E;
     LinArgs p = g;
     if (!g.pad_a && (!vec16(g.A, g.lda) || a_cols % 8)) {
@@ -132,7 +135,7 @@ LinPlan plan_copies(LinArgs& g, LinKind kind, Copies& c) {
         p.A = (const uint16_t*)(uintptr_t)256; p.lda = up8(a_cols); p.pad_a = true;
     }
     double b_us = 0;
-    if (g.pad_b) b_us = Copy{g.B, g.ldb, 0, b_groups, b_rows, b_cols}.us();
+    if (g.pad_b) b_us = b_cols % 8 ? Copy{g.B, g.ldb, 0, b_groups, b_rows, b_cols}.us() : 0;
     else if (!vec16(g.B, g.ldb) || g.b_group % 8 || b_cols % 8) {
         c.b = Copy{g.B, g.ldb, g.b_group, b_groups, b_rows, b_cols};
         b_us = c.b.us();

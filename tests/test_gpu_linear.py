@@ -822,6 +822,9 @@ def test_backward_of_rows_laid_out_anew(case, path, split):
 @pytest.mark.parametrize("case", [
     (2051, 1037, 1203, None, "gelu", 64, True, False, False, False, 0, 0),
     (130, 263, 521, None, "silu", 32, True, False, False, False, 0, 0),
+    (33, 1037, 1203, None, "silu", 32, True, False, False, False, 0, 0),
+    (700, 101, 136, None, "relu", 64, True, False, True, False, 0, 0),
+    (2100, 263, 75, None, "gelu", 64, True, False, True, False, 0, 0),   # long contraction, few tiles
     (333, 261, 397, 7, "silu", 128, True, False, True, False, 0, 0),
 ], ids=lambda c: "-".join(map(str, c)))
 def test_odd_backward_from_8_bits_equals_from_restored(case):
