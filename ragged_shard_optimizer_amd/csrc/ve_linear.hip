@@ -169,7 +169,8 @@ struct Operand {
         if constexpr (!DMA) {
             // No ragged end inside 16 bytes: plain loads, which run together.
             // KC rows past the last read it again (their outputs are not
-            // stored); KS rows past the contraction too, and become 0.
+            // stored, and the epilogue keeps them out of a run's largest
+            // magnitude); KS rows past the contraction too, and become 0.
             if (KS ? valid == ROWS : k0 + BK <= kc) {
 #pragma unroll
                 for (int q = 0; q < PIECES; ++q) {
@@ -547,8 +548,9 @@ __device__ __forceinline__ void epilogue_of(const Work& w, f32x16 (&acc)[CF::TM]
                     if (zout && in)
                         *(VE_GLOBAL u32x4*)(zout + (z_off + (uint32_t)(RI * i * (int)g.ldz * 2))) = narrow8(v[i]);
                     if (codes) {
-                        // columns past the last are 0: nothing was loaded for them, and their bias is 0
-                        const RunCode c = run_code_near(__uint_as_float(amax_lanes(amax8(v[i], 8), g.z8.block / 8)));
+                        // columns past the last count for nothing: w's rows for them are zeros with
+                        // direct loads, but copies of the last row in the register-staged form
+                        const RunCode c = run_code_near(__uint_as_float(amax_lanes(amax8(v[i], cnt0), g.z8.block / 8)));
                         const u32x2 q = encode8(c, v[i]);
                         if (in) {
                             *(VE_GLOBAL u32x2*)(codes + (c_off + (uint32_t)(RI * i * ldc))) = q;
