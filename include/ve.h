@@ -372,7 +372,9 @@ typedef struct {
 /* Save (pack) the bf16 rows x cols matrix x as codes and scales, or restore
  * (unpack) it.  One pass over memory.  rows >= 0 (0: no-op), 1 <= cols <
  * 2^31, leading dimensions at least the row; any alignment is correct, rows
- * that start on 16 bytes (codes: 8) are faster.  Buffers may not overlap. */
+ * that start on 16 bytes (codes: 8) are faster.  Buffers may not overlap; an
+ * output that starts inside another buffer, or the other way round, is
+ * VE_ERR_INVALID_ARG. */
 ve_status ve_act8_pack(const uint16_t* x, int64_t ldx, int64_t rows, int64_t cols, const ve_act8* out, void* stream);
 ve_status ve_act8_unpack(const ve_act8* in, int64_t rows, int64_t cols, uint16_t* x, int64_t ldx, void* stream);
 
@@ -460,7 +462,10 @@ typedef struct {
  * leading dimension shorter than the row, groups > 1 without offsets), an
  * unknown activation, a block other than 32, 64 or 128, y at x or dx at dy, a
  * short or misaligned workspace: VE_ERR_INVALID_ARG; sizes beyond one launch:
- * VE_ERR_UNSUPPORTED; launch failures: VE_ERR_DEVICE. */
+ * VE_ERR_UNSUPPORTED; launch failures: VE_ERR_DEVICE.  The two that launch
+ * also refuse (VE_ERR_INVALID_ARG) an output, or the workspace, whose first
+ * element is an element of an input that is read or of another output, or
+ * the other way round.  Column slices of one buffer are apart. */
 ve_status ve_linear_forward_workspace(const ve_linear_forward_args* a, int64_t* bytes);
 ve_status ve_linear_forward(const ve_linear_forward_args* a, void* workspace, int64_t workspace_bytes, void* stream);
 ve_status ve_linear_backward_workspace(const ve_linear_backward_args* a, int64_t* bytes);

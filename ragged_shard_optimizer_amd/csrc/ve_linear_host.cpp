@@ -15,6 +15,7 @@
 
 #include <algorithm>
 #include <cstdint>
+#include <initializer_list>
 
 #include "ve.h"
 #include "ve_linear.h"
@@ -296,6 +297,79 @@ void plan_backward(const ve_linear_backward_args& a, char* ws, Backward& b) {
     b.total = at;
 }
 
+// Device memory of a matrix, or of groups of them, in bytes.
+struct Span {
+    const char* name;
+    const void* p;
+    int64_t rows, row, pitch, groups, group;  // row: bytes of one; pitch, group: from one to the next
+
+    // Whether the byte at q is one of the matrix's (not of what lies between
+    // its rows, so that column slices of one buffer may stand side by side).
+    bool holds(const void* q) const {
+        if (!p || !q || (uintptr_t)q < (uintptr_t)p) return false;
+        uint64_t off = (uintptr_t)q - (uintptr_t)p;
+        if (off >= (uint64_t)((groups - 1) * group + (rows - 1) * pitch + row)) return false;
+        if (groups > 1) off -= std::min<uint64_t>(off / group, groups - 1) * group;
+        if (rows > 1) off -= std::min<uint64_t>(off / pitch, rows - 1) * pitch;
+        return off < (uint64_t)row;
+    }
+};
+Span matrix_span(const char* name, const void* p, int64_t rows, int64_t cols, int64_t ld, int64_t size) {
+    return Span{name, rows > 0 ? p : nullptr, rows, cols * size, ld * size, 1, 0};
+}
+Span group_span(const char* name, const void* p, int64_t groups, int64_t rows, int64_t cols, int64_t ld, int64_t group,
+                int64_t size) {
+    return Span{name, p, rows, cols * size, ld * size, groups, group * size};
+}
+Span codes_span(const ve_act8& q, int64_t rows, int64_t cols) { return matrix_span("codes", q.codes, rows, cols, q.ld_codes, 1); }
+Span scales_span(const ve_act8& q, int64_t rows, int64_t cols) {
+    return matrix_span("scales", q.codes ? q.scales : nullptr, rows, q.codes ? (cols + q.block - 1) / q.block : 0, q.ld_scales, 4);
+}
+
+// Refuses an output whose first element is an element of an input or of
+// another output, or the other way round: outputs in place of an input, or a
+// row or more into it.  Nothing that is refused could have been meant.
+ve_status check_apart(std::initializer_list<Span> outs, std::initializer_list<Span> ins) {
+    for (const Span* o = outs.begin(); o != outs.end(); ++o) {
+        if (!o->p) continue;
+        for (const Span& i : ins)
+            if (i.holds(o->p) || o->holds(i.p)) return fail(VE_ERR_INVALID_ARG, "%s overlaps %s", o->name, i.name);
+        for (const Span* q = o + 1; q != outs.end(); ++q)
+            if (q->holds(o->p) || o->holds(q->p)) return fail(VE_ERR_INVALID_ARG, "%s overlaps %s", o->name, q->name);
+    }
+    return VE_OK;
+}
+
+// The residual may be y itself, dx_add may be dx itself (the same rows).
+ve_status check_forward_apart(const ve_linear_forward_args& a, const void* ws, int64_t ws_bytes) {
+    const int64_t T = a.tokens, K = a.in_features, N = a.out_features, E = a.groups;
+    const bool same = a.residual == a.y && (a.ldr == a.ldy || T == 1);
+    return check_apart({matrix_span("y", a.y, T, N, a.ldy, 2), matrix_span("z", a.z, T, N, a.ldz, 2),
+                        codes_span(a.z8, T, N), scales_span(a.z8, T, N),
+                        matrix_span("workspace", ws_bytes ? ws : nullptr, 1, ws_bytes, ws_bytes, 1)},
+                       {matrix_span("x", a.x, T, K, a.ldx, 2), group_span("w", a.w, E, N, K, a.ldw, a.w_group, 2),
+                        group_span("bias", a.bias, E, 1, N, N, a.bias_group, 2),
+                        matrix_span("residual", same ? nullptr : a.residual, T, N, a.ldr, 2),
+                        matrix_span("offsets", a.offsets, 1, E + 1, E + 1, 8)});
+}
+
+// What is read: w for dx, x for dw, z for an activation's slope.
+ve_status check_backward_apart(const ve_linear_backward_args& a, const void* ws, int64_t ws_bytes) {
+    const int64_t T = a.tokens, K = a.in_features, N = a.out_features, E = a.groups, grad = a.grad_fp32 ? 4 : 2;
+    const bool same = a.dx_add == a.dx && (a.ld_add == a.lddx || T == 1), act = a.activation != VE_ACT_NONE;
+    const ve_act8 none{}, x8 = a.dw ? a.x8 : none, z8 = act ? a.z8 : none;
+    return check_apart({matrix_span("dx", a.dx, T, K, a.lddx, 2),
+                        group_span("dw", a.dw, E, N, K, a.lddw, a.dw_group, grad),
+                        group_span("dbias", a.dbias, E, 1, N, N, a.dbias_group, grad),
+                        matrix_span("workspace", ws_bytes ? ws : nullptr, 1, ws_bytes, ws_bytes, 1)},
+                       {matrix_span("dy", a.dy, T, N, a.lddy, 2),
+                        group_span("w", a.dx ? a.w : nullptr, E, N, K, a.ldw, a.w_group, 2),
+                        matrix_span("x", a.dw ? a.x : nullptr, T, K, a.ldx, 2), codes_span(x8, T, K), scales_span(x8, T, K),
+                        matrix_span("z", act ? a.z : nullptr, T, N, a.ldz, 2), codes_span(z8, T, N), scales_span(z8, T, N),
+                        matrix_span("dx_add", a.dx && !same ? a.dx_add : nullptr, T, K, a.ld_add, 2),
+                        matrix_span("offsets", a.offsets, 1, E + 1, E + 1, 8)});
+}
+
 ve_status check_workspace(void* ws, int64_t have, int64_t need) {
     if (need == 0) return VE_OK;
     if (!ws || have < need) return fail(VE_ERR_INVALID_ARG, "workspace of %lld bytes needed", (long long)need);
@@ -316,6 +390,10 @@ ve_status ve_act8_pack(const uint16_t* x, int64_t ldx, int64_t rows, int64_t col
     if (const ve_status st = check_act8(*out, cols, "out"); st != VE_OK) return st;
     if (cols > kMaxDim || rows > kMaxWorkgroups * 8192 / (cols + 128))
         return fail(VE_ERR_UNSUPPORTED, "matrix too large for one launch");
+    if (const ve_status st = check_apart({codes_span(*out, rows, cols), scales_span(*out, rows, cols)},
+                                         {matrix_span("x", x, rows, cols, ldx, 2)});
+        st != VE_OK)
+        return st;
     (void)hipGetLastError();
     return status_of(launch_act8_pack(x, ldx, rows, cols, *out, (hipStream_t)stream), "pack");
 }
@@ -329,6 +407,10 @@ ve_status ve_act8_unpack(const ve_act8* in, int64_t rows, int64_t cols, uint16_t
     if (const ve_status st = check_act8(*in, cols, "in"); st != VE_OK) return st;
     if (cols > kMaxDim || rows > kMaxWorkgroups * 8192 / (cols + 128))
         return fail(VE_ERR_UNSUPPORTED, "matrix too large for one launch");
+    if (const ve_status st = check_apart({matrix_span("x", x, rows, cols, ldx, 2)},
+                                         {codes_span(*in, rows, cols), scales_span(*in, rows, cols)});
+        st != VE_OK)
+        return st;
     (void)hipGetLastError();
     return status_of(launch_act8_unpack(*in, rows, cols, x, ldx, (hipStream_t)stream), "unpack");
 }
@@ -351,7 +433,7 @@ ve_status ve_linear_forward(const ve_linear_forward_args* a, void* workspace, in
     Forward f;
     plan_forward(*a, (char*)workspace, f);
     ve_status st = check_workspace(workspace, workspace_bytes, f.total);
-    if (st != VE_OK) return st;
+    if (st != VE_OK || (st = check_forward_apart(*a, workspace, f.total)) != VE_OK) return st;
     hipStream_t s = (hipStream_t)stream;
     (void)hipGetLastError();
     if ((st = run_copy(f.c.a, f.g.A, s)) != VE_OK || (st = run_copy(f.c.b, f.g.B, s)) != VE_OK) return st;
@@ -373,7 +455,9 @@ ve_status ve_linear_backward(const ve_linear_backward_args* a, void* workspace, 
     if (st != VE_OK) return st;
     Backward b;
     plan_backward(*a, (char*)workspace, b);
-    if ((st = check_workspace(workspace, workspace_bytes, b.total)) != VE_OK) return st;
+    if ((st = check_workspace(workspace, workspace_bytes, b.total)) != VE_OK ||
+        (st = check_backward_apart(*a, workspace, b.total)) != VE_OK)
+        return st;
     hipStream_t s = (hipStream_t)stream;
     (void)hipGetLastError();
     if (a->tokens > 0 && (a->dbias || (b.dz.dz && (a->dx || a->dw))) &&

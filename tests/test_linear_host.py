@@ -155,3 +155,70 @@ def test_workspace_of_rows_laid_out_anew():
     rc, need = _q(_fwd(tokens=1, in_features=top, out_features=1 << 20, ldx=top, ldw=top, ldy=1 << 20),
                   L.ve_linear_forward_workspace)
     assert rc == OK and need < 1 << 40
+
+
+Q = 1 << 40  # the buffers of these records lie far apart, but for the one that is moved
+
+
+def _apart_fwd(**kw):
+    a = ve._LinearForward(tokens=8, in_features=16, out_features=24, groups=2, activation=0, offsets=Q, x=2 * Q, ldx=16,
+                          w=3 * Q, ldw=16, w_group=400, y=4 * Q, ldy=24, bias=5 * Q, bias_group=32, residual=6 * Q, ldr=24,
+                          z=7 * Q, ldz=24, z8=ve._Act8(8 * Q, 24, 9 * Q, 1, 32))
+    for k, v in kw.items():
+        setattr(a, k, v)
+    return a
+
+
+def _apart_bwd(**kw):
+    a = ve._LinearBackward(tokens=8, in_features=16, out_features=24, groups=2, activation=4, offsets=Q, dy=2 * Q, lddy=24,
+                           w=3 * Q, ldw=16, w_group=400, x=4 * Q, ldx=16, z=5 * Q, ldz=24, dx=6 * Q, lddx=16, dx_add=7 * Q,
+                           ld_add=16, dw=8 * Q, lddw=16, dw_group=400, dbias=9 * Q, dbias_group=32)
+    for k, v in kw.items():
+        setattr(a, k, v)
+    return a
+
+
+def _refused(fn, query, a, names, workspace=10 * Q):
+    n = C.c_int64()
+    assert query(C.byref(a), C.byref(n)) == OK
+    assert fn(C.byref(a), workspace, n.value, None) == BAD
+    msg = ve.lib().ve_last_error().decode()
+    assert "overlaps" in msg and all(w in msg for w in names), msg
+
+
+@pytest.mark.parametrize("kw,names", [
+    (dict(y=2 * Q + 32), "yx"), (dict(y=3 * Q), "yw"), (dict(y=3 * Q + 800), "yw"), (dict(y=5 * Q + 64), ("y", "bias")),
+    (dict(y=6 * Q + 48), ("y", "residual")), (dict(y=6 * Q, ldy=32), ("y", "residual")), (dict(y=Q + 8), ("y", "offsets")),
+    (dict(x=4 * Q + 48 * 7), "yx"), (dict(z=4 * Q), "yz"), (dict(z=2 * Q), "zx"),
+    (dict(z8=ve._Act8(2 * Q + 1, 24, 9 * Q, 1, 32)), ("codes", "x")), (dict(z8=ve._Act8(8 * Q, 24, 7 * Q, 1, 32)), ("scales", "z")),
+    (dict(z8=ve._Act8(8 * Q, 24, 8 * Q + 24, 1, 32)), ("codes", "scales")),
+])
+def test_forward_outputs_over_other_buffers(kw, names):
+    L = ve.lib()
+    _refused(L.ve_linear_forward, L.ve_linear_forward_workspace, _apart_fwd(**kw), names)
+
+
+@pytest.mark.parametrize("kw,names", [
+    (dict(dx=4 * Q), ("dx", "x")), (dict(dx=4 * Q + 32), ("dx", "x")), (dict(dx=3 * Q), ("dx", "w")), (dict(dx=5 * Q), ("dx", "z")),
+    (dict(dx=2 * Q + 48), ("dx", "dy")), (dict(dx=7 * Q, lddx=24), ("dx", "dx_add")), (dict(dx=7 * Q + 32), ("dx", "dx_add")),
+    (dict(dx=8 * Q), ("dx", "dw")), (dict(dw=2 * Q), ("dw", "dy")), (dict(dw=4 * Q), ("dw", "x")), (dict(dw=3 * Q), ("dw", "w")),
+    (dict(dbias=2 * Q + 2), ("dbias", "dy")), (dict(dbias=8 * Q + 832), ("dw", "dbias")), (dict(dx=10 * Q), ("dx", "workspace")),
+    (dict(x=None, x8=ve._Act8(6 * Q, 16, 11 * Q, 1, 32)), ("dx", "codes")),
+    (dict(x=None, x8=ve._Act8(11 * Q, 16, 6 * Q, 1, 32)), ("dx", "scales")),
+    (dict(z=None, z8=ve._Act8(8 * Q, 24, 11 * Q, 1, 32)), ("dw", "codes")),
+])
+def test_backward_outputs_over_other_buffers(kw, names):
+    L = ve.lib()
+    _refused(L.ve_linear_backward, L.ve_linear_backward_workspace, _apart_bwd(**kw), names)
+
+
+def test_act8_over_other_buffers():
+    L = ve.lib()
+    for codes, scales in ((2 * Q, 3 * Q), (2 * Q + 200, 3 * Q), (3 * Q, 2 * Q + 4), (3 * Q, 3 * Q + 100)):
+        q = ve._Act8(codes, 100, scales, 4, 32)
+        assert L.ve_act8_pack(2 * Q, 100, 4, 100, C.byref(q), None) == BAD
+        assert b"overlaps" in L.ve_last_error()
+    q = ve._Act8(3 * Q, 100, 4 * Q, 4, 32)
+    for x in (3 * Q, 3 * Q + 1, 4 * Q - 200):
+        assert L.ve_act8_unpack(C.byref(q), 4, 100, x, 100, None) == BAD
+        assert b"overlaps" in L.ve_last_error()
