@@ -58,7 +58,10 @@ __global__ void __launch_bounds__(256) k_pack(const uint16_t* x, int64_t ldx, in
 }
 
 template <bool VEC>
-__global__ void __launch_bounds__(256) k_unpack(ve_act8 q, int64_t rows, int cols, uint16_t* x, int64_t ldx, int per) {
+__global__ void __launch_bounds__(256) k_unpack(ve_act8 q, int64_t rows, int cols, uint16_t* x, int64_t ldx, int per,
+                                                const int64_t* offsets, int E) {
+    int64_t lo, hi;
+    grouped_rows(offsets, E, rows, lo, hi);
     const int64_t first = (int64_t)blockIdx.x * (256 * kItems), row0 = first / per;
     const uint32_t rem = (uint32_t)(first - row0 * per);
     u32x2 w[kItems];
@@ -71,7 +74,7 @@ __global__ void __launch_bounds__(256) k_unpack(ve_act8 q, int64_t rows, int col
         const uint32_t i = rem + threadIdx.x + 256 * k, r = i / (uint32_t)per;
         row[k] = row0 + r;
         col[k] = (int)(i - r * per) * 8;
-        cnt[k] = row[k] < rows ? min(cols - col[k], 8) : 0;
+        cnt[k] = row[k] >= lo && row[k] < hi ? min(cols - col[k], 8) : 0;
         w[k] = u32x2{0, 0};
         scale[k] = 0.f;
         if (cnt[k] > 0) {
@@ -85,10 +88,13 @@ __global__ void __launch_bounds__(256) k_unpack(ve_act8 q, int64_t rows, int col
 }
 
 // Rows of `cols` elements, any alignment, as rows of whole 16 bytes that end
-// in zeros (per: 16-byte groups of a row; rows: of one group; all: of all).
+// in zeros (per: 16-byte groups of a row; rows: of one matrix; all: of all of
+// them; offsets: of the E groups that the rows are cut into, or null).
 // Bound by HBM, 4 bytes an element.
 __global__ void __launch_bounds__(256) k_pad(const uint16_t* src, int64_t ld, int64_t group, int64_t all, int64_t rows,
-                                             int cols, uint16_t* dst, int per) {
+                                             int cols, uint16_t* dst, int per, const int64_t* offsets, int E) {
+    int64_t lo, hi;
+    grouped_rows(offsets, E, all, lo, hi);
     const int64_t first = (int64_t)blockIdx.x * (256 * kItems), row0 = first / per;
     const uint32_t rem = (uint32_t)(first - row0 * per);
     const int64_t e0 = row0 / rows, in0 = row0 - e0 * rows;
@@ -105,7 +111,7 @@ __global__ void __launch_bounds__(256) k_pad(const uint16_t* src, int64_t ld, in
             e += over;
             in -= over * rows;
         }
-        at[k] = row < all ? row * per * 8 + col : -1;
+        at[k] = row >= lo && row < hi ? row * per * 8 + col : -1;
         if (at[k] >= 0) h[k] = load_bf16x8(src + e * group + in * ld + col, min(cols - col, 8), false);
     }
 #pragma unroll
@@ -237,11 +243,12 @@ hipError_t launch_dz(const DzArgs& a, hipStream_t s) {
     return hipGetLastError();
 }
 
-hipError_t launch_pad(const uint16_t* src, int64_t ld, int64_t group, int64_t E, int64_t rows, int64_t cols, uint16_t* dst,
-                      hipStream_t s) {
-    const int64_t per = (cols + 7) / 8, grid = (E * rows * per + 256 * kItems - 1) / (256 * kItems);
+hipError_t launch_pad(const uint16_t* src, int64_t ld, int64_t group, int64_t count, int64_t rows, int64_t cols, uint16_t* dst,
+                      const int64_t* offsets, int32_t E, hipStream_t s) {
+    const int64_t per = (cols + 7) / 8, grid = (count * rows * per + 256 * kItems - 1) / (256 * kItems);
     if (grid == 0) return hipSuccess;
-    hipLaunchKernelGGL(k_pad, dim3((unsigned)grid), dim3(256), 0, s, src, ld, group, E * rows, rows, (int)cols, dst, (int)per);
+    hipLaunchKernelGGL(k_pad, dim3((unsigned)grid), dim3(256), 0, s, src, ld, group, count * rows, rows, (int)cols, dst, (int)per,
+                       offsets, E);
     return hipGetLastError();
 }
 
@@ -266,13 +273,14 @@ hipError_t launch_act8_pack(const uint16_t* x, int64_t ldx, int64_t rows, int64_
     return hipGetLastError();
 }
 
-hipError_t launch_act8_unpack(const ve_act8& q, int64_t rows, int64_t cols, uint16_t* x, int64_t ldx, hipStream_t s) {
+hipError_t launch_act8_unpack(const ve_act8& q, int64_t rows, int64_t cols, uint16_t* x, int64_t ldx, const int64_t* offsets,
+                              int32_t E, hipStream_t s) {
     const int per = groups_per_row(cols, q.block);
     const int64_t grid = (rows * per + 256 * kItems - 1) / (256 * kItems);
     if (grid == 0) return hipSuccess;
     const bool vec = aligned(x, 16) && ldx % 8 == 0 && aligned(q.codes, 8) && q.ld_codes % 8 == 0;
-    if (vec) hipLaunchKernelGGL(k_unpack<true>, dim3((unsigned)grid), dim3(256), 0, s, q, rows, (int)cols, x, ldx, per);
-    else hipLaunchKernelGGL(k_unpack<false>, dim3((unsigned)grid), dim3(256), 0, s, q, rows, (int)cols, x, ldx, per);
+    if (vec) hipLaunchKernelGGL(k_unpack<true>, dim3((unsigned)grid), dim3(256), 0, s, q, rows, (int)cols, x, ldx, per, offsets, E);
+    else hipLaunchKernelGGL(k_unpack<false>, dim3((unsigned)grid), dim3(256), 0, s, q, rows, (int)cols, x, ldx, per, offsets, E);
     return hipGetLastError();
 }
 

@@ -75,10 +75,12 @@ hipError_t launch_dz(const DzArgs& a, hipStream_t s);
 hipError_t launch_dbias(const DzArgs& a, void* dbias, int64_t group, bool wide, bool accumulate, hipStream_t s);
 
 hipError_t launch_act8_pack(const uint16_t* x, int64_t ldx, int64_t rows, int64_t cols, const ve_act8& q, hipStream_t s);
-// rows x cols of each of E groups (ld and group: source strides) one after the
-// other into dst, whose rows of `cols` rounded up to 8 end in zeros.
-hipError_t launch_pad(const uint16_t* src, int64_t ld, int64_t group, int64_t E, int64_t rows, int64_t cols, uint16_t* dst,
-                      hipStream_t s);
-hipError_t launch_act8_unpack(const ve_act8& q, int64_t rows, int64_t cols, uint16_t* x, int64_t ldx, hipStream_t s);
+// rows x cols of each of `count` matrices (ld and group: source strides) one
+// after the other into dst, whose rows of `cols` rounded up to 8 end in zeros.
+// offsets (of E groups, or null): rows in no group are neither read nor written.
+hipError_t launch_pad(const uint16_t* src, int64_t ld, int64_t group, int64_t count, int64_t rows, int64_t cols, uint16_t* dst,
+                      const int64_t* offsets, int32_t E, hipStream_t s);
+hipError_t launch_act8_unpack(const ve_act8& q, int64_t rows, int64_t cols, uint16_t* x, int64_t ldx, const int64_t* offsets,
+                              int32_t E, hipStream_t s);
 
 }  // namespace ve

@@ -244,6 +244,13 @@ __device__ __forceinline__ void group_rows(const int64_t* off, int e, int64_t T,
     len = max(min(off[e + 1], T) - b, (int64_t)0);
 }
 
+// The rows from the first group's first to the last group's last (all rows
+// without offsets): what lies outside is not read.
+__device__ __forceinline__ void grouped_rows(const int64_t* off, int E, int64_t T, int64_t& lo, int64_t& hi) {
+    lo = off ? min(max(off[0], (int64_t)0), T) : 0;
+    hi = off ? min(max(off[E], (int64_t)0), T) : T;
+}
+
 __device__ __forceinline__ int64_t uniform64(int64_t v) {
     const uint32_t lo = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)v);
     const uint32_t hi = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)((uint64_t)v >> 32));

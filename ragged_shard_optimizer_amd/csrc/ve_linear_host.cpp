@@ -109,10 +109,11 @@ int64_t up8(int64_t n) { return (n + 7) / 8 * 8; }
 // 3030 -> 910, dw 6340 -> 915; 16 groups of 6 tokens 2046 -> 2046 forward
 // keep the other form (47 us against 88: the copies are of all weights).
 struct Copy {
-    const uint16_t* src; int64_t ld, group, E, rows, cols;
-    double elems() const { return (double)E * (double)rows * (double)up8(cols); }
-    int64_t bytes() const { return E * rows * up8(cols) * 2; }  // once elems() fits a launch
-    double us() const { return E ? 4 + elems() * 4 / 4e6 : 0; }
+    const uint16_t* src; int64_t ld, group, count, rows, cols;
+    const int64_t* offsets; int32_t E;  // rows of tokens: of the groups' rows only
+    double elems() const { return (double)count * (double)rows * (double)up8(cols); }
+    int64_t bytes() const { return count * rows * up8(cols) * 2; }  // once elems() fits a launch
+    double us() const { return count ? 4 + elems() * 4 / 4e6 : 0; }
 };
 struct Copies { Copy a, b; };
 
@@ -132,13 +133,13 @@ LinPlan plan_copies(LinArgs& g, LinKind kind, Copies& c) {
     const int64_t b_rows = kind == kLinFwd ? g.N : kind == kLinDx ? g.K : g.T, b_groups = kind == kLinDw ? 1 : g.E;
     LinArgs p = g;
     if (!g.pad_a && (!vec16(g.A, g.lda) || a_cols % 8)) {
-        c.a = Copy{g.A, g.lda, 0, 1, g.T, a_cols};
+        c.a = Copy{g.A, g.lda, 0, 1, g.T, a_cols, g.offsets, g.E};
         p.A = (const uint16_t*)(uintptr_t)256; p.lda = up8(a_cols); p.pad_a = true;
     }
     double b_us = 0;
-    if (g.pad_b) b_us = b_cols % 8 ? Copy{g.B, g.ldb, 0, b_groups, b_rows, b_cols}.us() : 0;
+    if (g.pad_b) b_us = b_cols % 8 ? Copy{g.B, g.ldb, 0, b_groups, b_rows, b_cols, nullptr, 0}.us() : 0;
     else if (!vec16(g.B, g.ldb) || g.b_group % 8 || b_cols % 8) {
-        c.b = Copy{g.B, g.ldb, g.b_group, b_groups, b_rows, b_cols};
+        c.b = Copy{g.B, g.ldb, g.b_group, b_groups, b_rows, b_cols, kind == kLinDw ? g.offsets : nullptr, g.E};
         b_us = c.b.us();
         p.B = (const uint16_t*)(uintptr_t)256; p.ldb = up8(b_cols); p.pad_b = true;
         if (b_groups > 1) p.b_group = b_rows * p.ldb;
@@ -157,7 +158,8 @@ LinPlan plan_copies(LinArgs& g, LinKind kind, Copies& c) {
 
 ve_status run_copy(const Copy& c, const uint16_t* to, hipStream_t s) {
     if (!c.src) return VE_OK;
-    return status_of(launch_pad(c.src, c.ld, c.group, c.E, c.rows, c.cols, (uint16_t*)to, s), "operand layout");
+    return status_of(launch_pad(c.src, c.ld, c.group, c.count, c.rows, c.cols, (uint16_t*)to, c.offsets, c.E, s),
+                     "operand layout");
 }
 
 // What a forward call launches, and where its scratch lies.
@@ -412,7 +414,7 @@ ve_status ve_act8_unpack(const ve_act8* in, int64_t rows, int64_t cols, uint16_t
         st != VE_OK)
         return st;
     (void)hipGetLastError();
-    return status_of(launch_act8_unpack(*in, rows, cols, x, ldx, (hipStream_t)stream), "unpack");
+    return status_of(launch_act8_unpack(*in, rows, cols, x, ldx, nullptr, 0, (hipStream_t)stream), "unpack");
 }
 
 ve_status ve_linear_forward_workspace(const ve_linear_forward_args* a, int64_t* bytes) {
@@ -472,7 +474,7 @@ ve_status ve_linear_backward(const ve_linear_backward_args* a, void* workspace, 
         return st;
     if (!a->dw) return VE_OK;
     if (a->tokens > 0 && a->x8.codes &&
-        (st = status_of(launch_act8_unpack(a->x8, a->tokens, a->in_features, (uint16_t*)b.dw.B, b.dw.ldb, s),
+        (st = status_of(launch_act8_unpack(a->x8, a->tokens, a->in_features, (uint16_t*)b.dw.B, b.dw.ldb, a->offsets, a->groups, s),
                         "restore")) != VE_OK)
         return st;
     if ((st = run_copy(b.cdw.a, b.dw.A, s)) != VE_OK || (st = run_copy(b.cdw.b, b.dw.B, s)) != VE_OK) return st;
