@@ -393,9 +393,8 @@ typedef enum {
  * Products of bf16 accumulate in fp32 on the MFMA units; bias, activation
  * and residual are applied in fp32 and y is rounded once.  For the backward
  * pass z can be written as bf16 (z) or in 8 bits (z8, from the fp32 values),
- * in the same pass.
- * z8's scale and code are those of the rule above to within one unit in the
- * last place of scale and of 127 / amax.
+ * in the same pass; z8's scales and codes are those of the rule above, bit
+ * for bit, for the fp32 z that the product gave.
  * All matrices are row-major bf16 on the device with the given leading
  * dimensions (elements).  Any alignment is correct; rows that start on 16
  * bytes and features that are multiples of 8 are much faster.  Outputs may

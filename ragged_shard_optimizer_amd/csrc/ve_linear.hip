@@ -550,7 +550,7 @@ __device__ __forceinline__ void epilogue_of(const Work& w, f32x16 (&acc)[CF::TM]
                     if (codes) {
                         // columns past the last count for nothing: w's rows for them are zeros with
                         // direct loads, but copies of the last row in the register-staged form
-                        const RunCode c = run_code_near(__uint_as_float(amax_lanes(amax8(v[i], cnt0), g.z8.block / 8)));
+                        const RunCode c = run_code_quick(__uint_as_float(amax_lanes(amax8(v[i], cnt0), g.z8.block / 8)));
                         const u32x2 q = encode8(c, v[i]);
                         if (in) {
                             *(VE_GLOBAL u32x2*)(codes + (c_off + (uint32_t)(RI * i * ldc))) = q;
