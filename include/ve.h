@@ -381,7 +381,7 @@ ve_status ve_act8_unpack(const ve_act8* in, int64_t rows, int64_t cols, uint16_t
 /* Activation functions of the linear layer. */
 typedef enum {
     VE_ACT_NONE = 0,
-    VE_ACT_RELU = 1,      /* max(z, 0); slope 0 at 0 */
+    VE_ACT_RELU = 1,      /* max(z, 0); slope 1 where z > 0, else 0 (at 0 and for NaN too) */
     VE_ACT_GELU = 2,      /* z (1 + erf(z / sqrt 2)) / 2 */
     VE_ACT_GELU_TANH = 3, /* z (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3))) / 2 */
     VE_ACT_SILU = 4       /* z / (1 + exp(-z)) */
@@ -425,7 +425,9 @@ typedef struct {
  * The MFMA units take bf16, so dz is rounded once before the two products
  * (not with VE_ACT_NONE, where dz is dy); sums are fp32.  x and z come as
  * bf16 or in 8 bits (then their restored values are what is computed with:
- * the same results, bit for bit, as from ve_act8_unpack's output).  Any
+ * the same results, bit for bit, as from ve_act8_unpack's output; where
+ * in_features is a multiple of 8, as from an output whose rows start on 16
+ * bytes, at most 2^21 elements apart).  Any
  * output may be NULL, and then what only it needs may be NULL too: w is read
  * for dx, x for dw.  Empty groups get dw = dbias = 0 (or keep theirs with
  * accumulate).  No atomics: the same inputs give the same bits every call.
@@ -454,10 +456,10 @@ typedef struct {
 /* Device scratch a call needs (0 is common; the arguments' sizes and strides,
  * which of its pointers are NULL and which are 16-byte aligned decide, nothing
  * is read through them).  Operands whose rows are not whole 16 bytes can be
- * laid out anew in it: up to the size of x, w and dy together.  The caller
- * owns the workspace, 256-byte aligned; its contents are scratch, and calls
- * that may overlap must not share one.  Errors of all four: NULL arguments or
- * needed pointers, sizes, groups or leading dimensions out of range (a
+ * laid out anew in it: up to x, w and dy together, each row rounded up to a
+ * multiple of 8 elements.  The caller owns the workspace, 256-byte aligned;
+ * its contents are scratch, and calls that may overlap must not share one.
+ * Errors of all four: NULL arguments or needed pointers, sizes, groups or leading dimensions out of range (a
  * leading dimension shorter than the row, groups > 1 without offsets), an
  * unknown activation, a block other than 32, 64 or 128, y at x or dx at dy, a
  * short or misaligned workspace: VE_ERR_INVALID_ARG; sizes beyond one launch:

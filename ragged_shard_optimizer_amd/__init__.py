@@ -552,8 +552,11 @@ def linear_forward(x, w, y, bias=None, activation="none", residual=None, z=None,
     [offsets[e], offsets[e + 1]) belong to expert e, and ``w`` is [groups,
     out, in], ``bias`` [groups, out].  ``z`` (bf16) or ``z8`` (:class:`Act8`)
     receives the input of the activation for the backward pass.
-    ``residual`` may be ``y``.  ``workspace``: uint8, at least
-    :func:`linear_forward_workspace` bytes (allocated here if None)."""
+    ``residual`` may be ``y``; otherwise outputs may not overlap inputs or
+    each other.  Writes into the given tensors and records nothing for
+    autograd: the gradients are :func:`linear_backward`'s.  ``workspace``:
+    uint8, at least :func:`linear_forward_workspace` bytes (allocated here if
+    None)."""
     return _forward(x, w, y, bias, activation, residual, z, z8, offsets, workspace, stream, False)
 
 
@@ -598,7 +601,8 @@ def linear_backward(dy, w, x=None, z=None, activation="none", dx=None, dx_add=No
     ``x`` (needed for ``dw``) and ``z`` (needed unless the activation is
     "none") are bf16 tensors or :class:`Act8`.  ``dw`` may be any tensor of
     w's shape with contiguous rows, e.g. a view of a DBuffer bucket at the
-    tensor's offset.  ``dx_add`` may be ``dx``."""
+    tensor's offset.  ``dx_add`` may be ``dx``; otherwise outputs may not
+    overlap inputs or each other."""
     _backward(dy, w, x, z, activation, dx, dx_add, dw, dbias, accumulate, offsets, workspace, stream, False)
 
 

@@ -8,8 +8,8 @@
 // All kernels are bound by HBM: 3 bytes an element for pack and unpack, 6
 // (bf16 z) or 5 (8-bit z) for dz.  16384 x 8192, block 128: pack 68 us (6.0
 // TB/s; 88 without the streaming hint on its loads, which leaves the caches
-// to the codes), unpack 68 to 74 us (5.5 to 6.0 TB/s).  dz of 8192 x 28672 from
-// 8 bits 241 us (4.9 TB/s).
+// to the codes), unpack 69 to 78 us (5.3 to 5.9 TB/s).  dz of 8192 x 28672 from
+// 8 bits 220 to 228 us (5.2 to 5.4 TB/s).
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -122,7 +122,12 @@ __global__ void __launch_bounds__(256) k_pad(const uint16_t* src, int64_t ld, in
 // dz and column sums.  A workgroup takes a tile of kDzRows tokens of one
 // group and 512 columns: 64 lanes of 8 columns, its four waves on every
 // fourth row, each summing its rows in fp32; the four sums are joined in LDS.
-// The sums are of dz before its rounding to bf16.
+// The sums are of dz before its rounding.  dz is rounded to bf16 once, because
+// the matrix units that dx and dw run on take bf16: each term of their sums is
+// off by at most 2^-8 of itself, which makes their error against exact
+// gradients 1.4 times that of an fp32 dz (0.0023 against 0.0017 of the
+// result's norm, most of both from the result's own rounding to bf16).  A dz
+// in two bf16 parts would double the products' work.
 template <int ZMODE, bool VEC>  // ZMODE 0: act none (dz = dy, sums only), 1: bf16 z, 2: 8-bit z
 __global__ void __launch_bounds__(256) k_dz(DzArgs a, int col_tiles) {
     const int ct = blockIdx.x % col_tiles, rt = blockIdx.x / col_tiles;

@@ -635,9 +635,11 @@ __device__ __forceinline__ uint32_t all_tiles(const LinArgs& g) {
 // inside a step either: 1,375 against 1,166 TFLOP/s for dw at 8192^3, and
 // 1,293 where two such waves took turns at the MFMAs.
 //
-// 8192 tokens, 8192 -> 28672: forward 1,414, dx 1,358, dw 1,278 TFLOP/s
-// (library products 1,582, 1,387, 1,183).  The MFMAs are busy three quarters
-// of the cycles, at a clock that the card's power holds at 1.5 to 1.7 GHz.
+// 8192 tokens, 8192 -> 28672, normal values: forward 1,384 to 1,395, dx 1,327
+// to 1,332, dw 1,250 TFLOP/s (library products 1,558, 1,363, 1,176);
+// values of many magnitudes cost up to 4%.  By the counters the MFMAs are busy
+// 79, 76 and 72% of the cycles once the clock has settled at 1.65 to 1.7 GHz;
+// the first calls after a pause run at 1.2 to 1.5 GHz and 1,040 to 1,240.
 template <class CF, int KIND>
 __global__ void __launch_bounds__(CF::THREADS, CF::PER_CU) k_product(LinArgs g) {
     constexpr int TM = CF::TM, TN = CF::TN, WM = CF::WM, WN = CF::WN;
@@ -1096,7 +1098,12 @@ hipError_t launch_path(const LinArgs& g, const LinPlan& p, hipStream_t s) {
 // single one 0.6.  Slices' sums (bytes) are written and read at 5 TB/s, by
 // one launch more (4 us).  Against measurements, 128^2 / 256^2 in us: 4001
 // tokens 2880 -> 5760 dx 141 / 127 (model 143 / 133), dw 157 / 179 (163 /
-// 189); 2049 tokens 4096 -> 2880 forward 59 (62).
+// 189); 2049 tokens 4096 -> 2880 forward 59 (62).  The fit is to contractions
+// of a thousand and more, and without a term for bytes: products that bytes
+// bind take 2 to 2.5 times the estimate (fp32 dw of 77 tokens 7168 -> 1536 19
+// us, estimated 8; of 16 groups with 500 tokens 2880 -> 2880 120, estimated
+// 58; dx of the latter 91, estimated 45), and of ragged rows it counts the
+// most tiles that any offsets could need.
 // us: a step of two 128 x 128 tiles, of a single one, their start and
 // epilogue, those of a 256 x 256 tile
 struct TileCost { double pair, one, start, start256; };
@@ -1125,11 +1132,15 @@ double product_us(bool big, int64_t items, int64_t steps, int64_t bytes, const T
 LinPlan plan_product(const LinArgs& g, LinKind kind) {
     LinPlan p{kPathGeneral, 1, 0, 0};
     const int64_t pin = option(kOptLinearPath);
-    // Up to 8 tokens the few-token form is faster (us, 8192 -> 28672 one token
-    // 89 against 131 of the tiles; 8192 -> 1024 14 against 19), at 16 the
-    // tiles split along the contraction are (8192 -> 8192: 35 against 37).
-    // Ragged groups stay with the tiles, which stream 32 groups' weights at
-    // 5.6 TB/s with one token or 16 in each.
+    // Few tokens against the tiles split along the contraction, us a call at 1
+    // / 2 / 4 / 8 tokens: 8192 -> 1024 8 / 8 / 8 / 14 against 19, 8192 -> 8192
+    // 28 / 30 / 33 / 56 against 36, 8192 -> 28672 92 / 97 / 98 / 111 against
+    // 120 to 130.  At 5 to 8 tokens the rule is right at the ends only: with
+    // some thousand outputs the tiles are faster (2880 -> 5760 18 against 23).
+    // Ragged groups stay with the tiles, unsplit, which read the weights of
+    // the groups that have tokens at 5.2 to 6.0 TB/s where those are 26 or
+    // more (7168 -> 2048); fewer leave CUs without work: 19 groups 4.5 TB/s, 8
+    // 2.3, and one token of one group takes 46 us for 29 MB.
     const bool few = kind == kLinFwd && !g.offsets && !g.z8.codes && g.K % 8 == 0 && dma_ok(g, kind);
     if (few && g.T <= kFewTokens && (pin == kPathAuto || pin == kPathFew)) {
         p.path = kPathFew;

@@ -59,7 +59,7 @@ __device__ __forceinline__ float exp_of(float x) { return __builtin_amdgcn_exp2f
 // a >= 0, as exp(-a^2 / 2) t P(t) with t = 1 / (1 + 0.33 a): erfcx falls like
 // 1 / a, so t P(t) carries it with a degree-7 polynomial.  The coefficients
 // are a minimax fit of the relative error over all a (1.0e-6; 1.6e-6 in fp32
-// arithmetic for a < 5), far below the 2^-9 of the bf16 result.  ex returns
+// arithmetic for a < 5), far below the 2^-8 of the bf16 result.  ex returns
 // exp(-a^2 / 2), which the slope needs too.
 __device__ __forceinline__ float normal_tail(float a, float& ex) {
     const float t = __builtin_amdgcn_rcpf(__builtin_fmaf(0.33f, a, 1.f));
