@@ -12,7 +12,9 @@ Names follow the C ABI: ``plan_load`` / ``Plan.query`` / ``Plan.slice`` /
 ``ve_dbuffer_copy_in``, ``ve_shard_adam8bit_step``, ``ve_dbuffer_group_op``
 and ``ve_plan_layout``; ``linear_forward`` / ``linear_backward`` /
 ``act8_pack`` / ``act8_unpack`` wrap the linear layer's entry points and take
-torch tensors with any row stride.
+torch tensors with any row stride; ``expert_*`` sort rows by expert for the
+grouped products and bring them back, and ``fp8_*`` are the same products on
+matrices packed in 8-bit floating point.
 """
 
 from __future__ import annotations
@@ -37,6 +39,11 @@ EXPORTS = ("ve_plan_load", "ve_plan_free", "ve_plan_query", "ve_dbuffer_copy_in"
            "ve_muon_workspace_bytes", "ve_muon_newton_schulz", "ve_muon_newton_schulz_noalloc",
            "ve_gemm_bf16_nt", "ve_act8_pack", "ve_act8_unpack", "ve_linear_forward_workspace", "ve_linear_forward",
            "ve_linear_backward_workspace", "ve_linear_backward",
+           "ve_fp8_columns", "ve_fp8_pack", "ve_fp8_pack_weight", "ve_fp8_unpack",
+           "ve_fp8_linear_forward_workspace", "ve_fp8_linear_forward",
+           "ve_fp8_linear_backward_workspace", "ve_fp8_linear_backward",
+           "ve_expert_sort_workspace", "ve_expert_sort", "ve_expert_gather", "ve_expert_combine",
+           "ve_expert_combine_backward",
            "ve_stream_copy", "ve_set_option", "ve_get_option", "ve_last_error")
 
 # ve_group_op
@@ -87,6 +94,60 @@ class _LinearBackward(C.Structure):
         ("dbias", C.c_void_p), ("dbias_group", C.c_int64), ("grad_fp32", C.c_int32), ("accumulate", C.c_int32)]
 
 
+class _Fp8(C.Structure):
+    _fields_ = [("codes", C.c_void_p), ("ld_codes", C.c_int64), ("scales", C.c_void_p), ("ld_scales", C.c_int64),
+                ("format", C.c_int32), ("block_rows", C.c_int32)]
+
+
+class _Fp8Pack(C.Structure):
+    _fields_ = [("rows", C.c_int64), ("cols", C.c_int64), ("groups", C.c_int32), ("activation", C.c_int32),
+                ("offsets", C.c_void_p), ("x", C.c_void_p), ("ldx", C.c_int64), ("z", C.c_void_p), ("ldz", C.c_int64),
+                ("out", _Fp8), ("out_t", _Fp8)]
+
+
+class _Fp8PackWeight(C.Structure):
+    _fields_ = [("rows", C.c_int64), ("cols", C.c_int64), ("groups", C.c_int32),
+                ("w", C.c_void_p), ("ldw", C.c_int64), ("w_group", C.c_int64),
+                ("out", _Fp8), ("out_codes_group", C.c_int64), ("out_scales_group", C.c_int64),
+                ("out_t", _Fp8), ("out_t_codes_group", C.c_int64), ("out_t_scales_group", C.c_int64)]
+
+
+class _Fp8Forward(C.Structure):
+    _fields_ = _SHAPE_FIELDS + [
+        ("x", _Fp8), ("w", _Fp8), ("w_codes_group", C.c_int64), ("w_scales_group", C.c_int64),
+        ("bias", C.c_void_p), ("bias_group", C.c_int64), ("residual", C.c_void_p), ("ldr", C.c_int64),
+        ("y", C.c_void_p), ("ldy", C.c_int64), ("z", C.c_void_p), ("ldz", C.c_int64)]
+
+
+class _Fp8Backward(C.Structure):
+    _fields_ = [("tokens", C.c_int64), ("in_features", C.c_int64), ("out_features", C.c_int64), ("groups", C.c_int32),
+                ("offsets", C.c_void_p),
+                ("dy", _Fp8), ("w_t", _Fp8), ("w_codes_group", C.c_int64), ("w_scales_group", C.c_int64),
+                ("dx", C.c_void_p), ("lddx", C.c_int64), ("dx_add", C.c_void_p), ("ld_add", C.c_int64),
+                ("dy_t", _Fp8), ("x_t", _Fp8), ("dw", C.c_void_p), ("lddw", C.c_int64), ("dw_group", C.c_int64),
+                ("grad_fp32", C.c_int32), ("accumulate", C.c_int32)]
+
+
+_SLOT_FIELDS = [("tokens", C.c_int64), ("cols", C.c_int64), ("slots", C.c_int32), ("position", C.c_void_p),
+                ("weights", C.c_void_p)]
+
+
+class _ExpertGather(C.Structure):
+    _fields_ = _SLOT_FIELDS + [("x", C.c_void_p), ("ldx", C.c_int64), ("rows_len", C.c_int64), ("rows", C.c_void_p),
+                               ("ld_rows", C.c_int64), ("rows8", _Fp8)]
+
+
+class _ExpertCombine(C.Structure):
+    _fields_ = _SLOT_FIELDS + [("rows_len", C.c_int64), ("rows", C.c_void_p), ("ld_rows", C.c_int64),
+                               ("residual", C.c_void_p), ("ldr", C.c_int64), ("y", C.c_void_p), ("ldy", C.c_int64)]
+
+
+class _ExpertCombineBackward(C.Structure):
+    _fields_ = _SLOT_FIELDS + [("dy", C.c_void_p), ("lddy", C.c_int64), ("rows_len", C.c_int64), ("rows", C.c_void_p),
+                               ("ld_rows", C.c_int64), ("drows", C.c_void_p), ("ld_drows", C.c_int64),
+                               ("dweights", C.c_void_p)]
+
+
 # ve_shard_state: eight device pointers, in this order
 STATE_FIELDS = ("grad_ptrs", "grad_shard", "master", "m_q", "v_q", "m_scale", "v_scale", "param_shard")
 
@@ -121,12 +182,26 @@ def lib() -> C.CDLL:
         L.ve_linear_forward.argtypes = [P, P, C.c_int64, P]
         L.ve_linear_backward_workspace.argtypes = [P, P]
         L.ve_linear_backward.argtypes = [P, P, C.c_int64, P]
+        L.ve_fp8_columns.argtypes = [C.c_int64, C.c_int32]
+        L.ve_fp8_pack.argtypes = [P, P]
+        L.ve_fp8_pack_weight.argtypes = [P, P]
+        L.ve_fp8_unpack.argtypes = [P, C.c_int64, C.c_int64, P, C.c_int64, P]
+        L.ve_fp8_linear_forward_workspace.argtypes = [P, P]
+        L.ve_fp8_linear_forward.argtypes = [P, P, C.c_int64, P]
+        L.ve_fp8_linear_backward_workspace.argtypes = [P, P]
+        L.ve_fp8_linear_backward.argtypes = [P, P, C.c_int64, P]
+        L.ve_expert_sort_workspace.argtypes = [C.c_int64, C.c_int32, C.c_int32, P]
+        L.ve_expert_sort.argtypes = [P, C.c_int32, C.c_int64, C.c_int32, C.c_int32, P, P, P, P, C.c_int64, P]
+        L.ve_expert_gather.argtypes = [P, P]
+        L.ve_expert_combine.argtypes = [P, P]
+        L.ve_expert_combine_backward.argtypes = [P, P]
         L.ve_stream_copy.argtypes = [P, P, C.c_int64, P]
         L.ve_set_option.argtypes = [C.c_char_p, C.c_int64]
         L.ve_get_option.argtypes = [C.c_char_p, P]
         L.ve_muon_newton_schulz_noalloc.argtypes = [P, P, C.c_int64, C.c_int64, C.c_int32, C.c_float, P]
         for name in EXPORTS[:-1]:
             getattr(L, name).restype = C.c_int
+        L.ve_fp8_columns.restype = C.c_int64
         _lib = L
     return _lib
 
@@ -522,24 +597,33 @@ def act8_unpack(q: Act8, out, stream=None):
 
 def _shape(a, tokens, w, offsets, activation, device, wname="w"):
     """Fill the shape of an argument record; returns groups (None without offsets)."""
-    groups = None
-    if offsets is not None:
-        _types()
-        if offsets.dim() != 1 or offsets.shape[0] < 2 or offsets.dtype != _torch.int64:
-            raise ValueError("offsets: a 1-D int64 tensor of groups + 1 elements")
-        if offsets.device != device or not offsets.is_contiguous():
-            raise ValueError(f"offsets: must be contiguous on {device}")
-        groups = offsets.shape[0] - 1
-        a.offsets = offsets.data_ptr()
+    groups = _offsets(a, offsets, device)
     if w.dim() != (2 if groups is None else 3):
         raise ValueError(f"{wname}: [out, in] features, or [groups, out, in] with offsets")
     a.tokens, a.in_features, a.out_features = tokens, w.shape[-1], w.shape[-2]
-    a.groups = 1 if groups is None else groups
-    act = ACTIVATIONS.get(activation, activation)
-    if not isinstance(act, int):
-        raise ValueError(f"unknown activation {activation!r}; one of {sorted(ACTIVATIONS)}")
-    a.activation = act
+    a.activation = _activation(activation)
     return groups
+
+
+def _offsets(a, offsets, device):
+    """Fill an argument record's groups; returns them (None without offsets)."""
+    a.groups = 1
+    if offsets is None:
+        return None
+    _types()
+    if offsets.dim() != 1 or offsets.shape[0] < 2 or offsets.dtype != _torch.int64:
+        raise ValueError("offsets: a 1-D int64 tensor of groups + 1 elements")
+    if offsets.device != device or not offsets.is_contiguous():
+        raise ValueError(f"offsets: must be contiguous on {device}")
+    a.groups, a.offsets = offsets.shape[0] - 1, offsets.data_ptr()
+    return a.groups
+
+
+def _activation(name) -> int:
+    act = ACTIVATIONS.get(name, name)
+    if not isinstance(act, int):
+        raise ValueError(f"unknown activation {name!r}; one of {sorted(ACTIVATIONS)}")
+    return act
 
 
 def linear_forward(x, w, y, bias=None, activation="none", residual=None, z=None, z8=None, offsets=None,
@@ -653,6 +737,362 @@ def _backward(dy, w, x, z, activation, dx, dx_add, dw, dbias, accumulate, offset
         _check(L.ve_linear_backward_workspace(C.byref(a), C.byref(need)))
         return need.value
     _run(L.ve_linear_backward, L.ve_linear_backward_workspace, a, dev, stream, workspace)
+
+
+class Fp8:
+    """A matrix (or groups of them) in 8-bit floating point (``ve_fp8``):
+    ``codes`` [rows, cols] of a float8 dtype (``torch.float8_e4m3fn`` or
+    ``torch.float8_e5m2``) and ``scales`` [ceil(cols / 128), ceil(rows /
+    block_rows)], uint8, both with a leading group dimension for grouped
+    weights.  Rows of codes start on 16 bytes and go on with zeros to the next
+    multiple of 16, rows of scales start on 4 bytes and go on to the next
+    multiple of 4: :func:`new_fp8` allocates such."""
+
+    __slots__ = ("codes", "scales", "block_rows")
+
+    def __init__(self, codes, scales, block_rows: int = 1):
+        self.codes, self.scales, self.block_rows = codes, scales, int(block_rows)
+
+    @property
+    def shape(self):
+        return self.codes.shape
+
+    @property
+    def device(self):
+        return self.codes.device
+
+    def _fill(self, rows, cols, name, device, groups=None):
+        """(record, group strides of codes and of scales)"""
+        _types()
+        c, s, b = self.codes, self.scales, self.block_rows
+        if b not in (1, 128):
+            raise ValueError(f"{name}: {b} rows share a scale, not 1 or 128")
+        if c.dtype == _torch.float8_e4m3fn:
+            fmt = 0
+        elif c.dtype == _torch.float8_e5m2:
+            fmt = 1
+        else:
+            raise ValueError(f"{name}.codes: need a float8_e4m3fn or float8_e5m2 tensor")
+        ptr, ld, cg = _rows8(c, groups, rows, cols, 16, f"{name}.codes", device)
+        if s.dtype != _torch.uint8:
+            raise ValueError(f"{name}.scales: need uint8 elements")
+        sptr, lds, sg = _rows8(s, groups, -(-cols // 128), -(-rows // b), 4, f"{name}.scales", device)
+        return _Fp8(ptr, ld, sptr, lds, fmt, b), cg, sg
+
+
+def _rows8(t, groups, rows, cols, unit, name, device):
+    """(pointer, leading dimension, group stride) of a tensor of bytes whose
+    rows start on `unit` bytes and have memory up to the next multiple."""
+    shape = (rows, cols) if groups is None else (groups, rows, cols)
+    if t.shape != shape:
+        raise ValueError(f"{name}: shape {tuple(t.shape)} != {shape}")
+    if t.device != device or not t.is_cuda:
+        raise ValueError(f"{name}: must be a device tensor on {device}")
+    st = t.stride()
+    if st[-1] != 1 and cols > 1:
+        raise ValueError(f"{name}: rows must be contiguous")
+    whole = -(-cols // unit) * unit
+    ld = st[-2] if rows > 1 else whole
+    group = st[0] if groups is not None else 0
+    end = t.storage_offset() + ((groups or 1) - 1) * group + (rows - 1) * ld + whole
+    if t.numel() and end > t.untyped_storage().nbytes():
+        raise ValueError(f"{name}: the last row's memory must go on to a multiple of {unit} bytes")
+    return t.data_ptr(), ld, group
+
+
+def fp8_columns(rows: int, groups: int = 1) -> int:
+    """``ve_fp8_columns``: columns of a transposed matrix of `rows` tokens in
+    `groups` groups, each of which has whole runs of 128."""
+    return lib().ve_fp8_columns(rows, groups)
+
+
+def new_fp8(rows: int, cols: int, block_rows: int = 1, format: str = "e4m3", groups=None, device="cuda") -> Fp8:
+    """Allocate an :class:`Fp8` for a rows x cols matrix (for `groups` of them):
+    zeros."""
+    import torch
+    dtype = {"e4m3": torch.float8_e4m3fn, "e5m2": torch.float8_e5m2}[format]
+    lead, n = () if groups is None else (groups,), -(-rows // block_rows)
+    codes = torch.zeros(*lead, rows, -(-cols // 16) * 16, dtype=torch.uint8, device=device)
+    scales = torch.zeros(*lead, -(-cols // 128), -(-n // 4) * 4, dtype=torch.uint8, device=device)
+    return Fp8(codes.view(dtype)[..., :cols], scales[..., :n], block_rows)
+
+
+def fp8_pack(x, out: Fp8 = None, out_t: Fp8 = None, z=None, activation="none", offsets=None, stream=None):
+    """``ve_fp8_pack``: the 2-D bf16 matrix ``x`` (times the activation's slope
+    at ``z``) in runs of 128 columns (``out`` [rows, cols]) and, transposed, in
+    runs of 128 rows of a group (``out_t`` [cols, fp8_columns(rows, groups)])."""
+    a, dev = _Fp8Pack(), x.device
+    if x.dim() != 2:
+        raise ValueError("x: a 2-D matrix")
+    a.rows, a.cols = x.shape
+    a.x, a.ldx = _matrix(x, a.rows, a.cols, "x", dev)
+    _offsets(a, offsets, dev)
+    a.activation = _activation(activation)
+    if a.activation:
+        if z is None:
+            raise ValueError("the activation's slope needs z")
+        a.z, a.ldz = _matrix(z, a.rows, a.cols, "z", dev)
+    if out is not None:
+        a.out = out._fill(a.rows, a.cols, "out", dev)[0]
+    if out_t is not None:
+        a.out_t = out_t._fill(a.cols, lib().ve_fp8_columns(a.rows, a.groups), "out_t", dev)[0]
+    _call(dev, lib().ve_fp8_pack, C.byref(a), _stream_on(dev, stream))
+
+
+def fp8_pack_weight(w, out: Fp8 = None, out_t: Fp8 = None, stream=None):
+    """``ve_fp8_pack_weight``: bf16 ``w`` [out, in] (or [groups, out, in]) in
+    blocks of 128 x 128, as it lies (``out``) and transposed (``out_t``)."""
+    a, dev = _Fp8PackWeight(), w.device
+    if w.dim() not in (2, 3):
+        raise ValueError("w: [out, in] features, or [groups, out, in]")
+    g = w.shape[0] if w.dim() == 3 else None
+    a.rows, a.cols, a.groups = w.shape[-2], w.shape[-1], 1 if g is None else g
+    a.w, a.ldw, a.w_group = _groups_of(w, g, a.rows, a.cols, "w", dev)
+    if out is not None:
+        a.out, a.out_codes_group, a.out_scales_group = out._fill(a.rows, a.cols, "out", dev, g)
+    if out_t is not None:
+        a.out_t, a.out_t_codes_group, a.out_t_scales_group = out_t._fill(a.cols, a.rows, "out_t", dev, g)
+    _call(dev, lib().ve_fp8_pack_weight, C.byref(a), _stream_on(dev, stream))
+
+
+def fp8_unpack(q: Fp8, out, stream=None):
+    """``ve_fp8_unpack``: restore a packed matrix as bf16 into ``out`` (of
+    grouped weights, one group after the other)."""
+    if out.dim() == 3:
+        if q.codes.dim() != 3 or q.codes.shape[0] != out.shape[0]:
+            raise ValueError("q: as many groups as out")
+        for e in range(out.shape[0]):
+            fp8_unpack(Fp8(q.codes[e], q.scales[e], q.block_rows), out[e], stream)
+        return out
+    rows, cols = out.shape
+    ptr, ld = _matrix(out, rows, cols, "out", out.device)
+    s = q._fill(rows, cols, "q", out.device)[0]
+    _call(out.device, lib().ve_fp8_unpack, C.byref(s), rows, cols, ptr, ld, _stream_on(out.device, stream))
+    return out
+
+
+def fp8_linear_forward(x: Fp8, w: Fp8, y, bias=None, activation="none", residual=None, z=None, offsets=None,
+                       workspace=None, stream=None):
+    """``ve_fp8_linear_forward``: y = act(x w^T + bias) + residual of packed
+    ``x`` [tokens, in] (block_rows 1) and ``w`` [out, in] or [groups, out, in]
+    (block_rows 128, E4M3); the rest as for :func:`linear_forward`."""
+    return _fp8_forward(x, w, y, bias, activation, residual, z, offsets, workspace, stream, False)
+
+
+def fp8_linear_forward_workspace(x: Fp8, w: Fp8, y, bias=None, activation="none", residual=None, z=None,
+                                 offsets=None) -> int:
+    """``ve_fp8_linear_forward_workspace`` of the same call (bytes)."""
+    return _fp8_forward(x, w, y, bias, activation, residual, z, offsets, None, None, True)
+
+
+def _fp8_forward(x, w, y, bias, activation, residual, z, offsets, workspace, stream, query):
+    a, dev = _Fp8Forward(), x.device
+    if x.codes.dim() != 2:
+        raise ValueError("x: [tokens, in] features")
+    g = _shape(a, x.codes.shape[0], w.codes, offsets, activation, dev)
+    T, K, N = a.tokens, a.in_features, a.out_features
+    a.x = x._fill(T, K, "x", dev)[0]
+    a.w, a.w_codes_group, a.w_scales_group = w._fill(N, K, "w", dev, g)
+    a.y, a.ldy = _matrix(y, T, N, "y", dev)
+    if bias is not None:
+        a.bias, a.bias_group = _vectors_of(bias, g, N, "bias", dev)
+    if residual is not None:
+        a.residual, a.ldr = _matrix(residual, T, N, "residual", dev)
+    if z is not None:
+        a.z, a.ldz = _matrix(z, T, N, "z", dev)
+    L = lib()
+    if query:
+        need = C.c_int64()
+        _check(L.ve_fp8_linear_forward_workspace(C.byref(a), C.byref(need)))
+        return need.value
+    _run(L.ve_fp8_linear_forward, L.ve_fp8_linear_forward_workspace, a, dev, stream, workspace)
+    return y
+
+
+def fp8_linear_backward(dy: Fp8 = None, w_t: Fp8 = None, dx=None, dx_add=None, dy_t: Fp8 = None, x_t: Fp8 = None,
+                        dw=None, accumulate=False, offsets=None, tokens=None, workspace=None, stream=None):
+    """``ve_fp8_linear_backward``: ``dx`` (bf16, plus ``dx_add``) from ``dy``
+    [tokens, out] and ``w_t`` ([groups,] in, out), and ``dw`` (bf16 or fp32,
+    added to what it holds with ``accumulate``) from ``dy_t`` [out, columns]
+    and ``x_t`` [in, columns], columns = fp8_columns(tokens, groups), as
+    :func:`fp8_pack` and :func:`fp8_pack_weight` transpose them.  Either
+    gradient may be None; ``tokens`` is needed where ``dx`` is."""
+    _fp8_backward(dy, w_t, dx, dx_add, dy_t, x_t, dw, accumulate, offsets, tokens, workspace, stream, False)
+
+
+def fp8_linear_backward_workspace(dy: Fp8 = None, w_t: Fp8 = None, dx=None, dx_add=None, dy_t: Fp8 = None,
+                                  x_t: Fp8 = None, dw=None, accumulate=False, offsets=None, tokens=None) -> int:
+    """``ve_fp8_linear_backward_workspace`` of the same call (bytes)."""
+    return _fp8_backward(dy, w_t, dx, dx_add, dy_t, x_t, dw, accumulate, offsets, tokens, None, None, True)
+
+
+def _fp8_backward(dy, w_t, dx, dx_add, dy_t, x_t, dw, accumulate, offsets, tokens, workspace, stream, query):
+    if dx is None and dw is None:
+        if query:
+            return 0
+        return None
+    a, dev = _Fp8Backward(), (dw if dx is None else dx).device
+    g = _offsets(a, offsets, dev)
+    if dx is not None:
+        if dy is None or w_t is None:
+            raise ValueError("dx needs dy and w_t")
+        if dx.dim() != 2 or dy.codes.dim() != 2:
+            raise ValueError("dx: [tokens, in] features, dy: [tokens, out]")
+        T, K, N = dx.shape[0], dx.shape[1], dy.codes.shape[1]
+        if tokens is not None and tokens != T:
+            raise ValueError(f"tokens {tokens}, but dx has {T}")
+        a.dy = dy._fill(T, N, "dy", dev)[0]
+        a.w_t, a.w_codes_group, a.w_scales_group = w_t._fill(K, N, "w_t", dev, g)
+        a.dx, a.lddx = _matrix(dx, T, K, "dx", dev)
+        if dx_add is not None:
+            a.dx_add, a.ld_add = _matrix(dx_add, T, K, "dx_add", dev)
+    else:
+        if dx_add is not None:
+            raise ValueError("dx_add without dx")
+        if tokens is None:
+            raise ValueError("dw alone needs tokens")
+        T, N, K = int(tokens), dw.shape[-2], dw.shape[-1]
+    a.tokens, a.in_features, a.out_features = T, K, N
+    if dw is not None:
+        if dy_t is None or x_t is None:
+            raise ValueError("dw needs dy_t and x_t")
+        cols = lib().ve_fp8_columns(T, a.groups)
+        a.dy_t = dy_t._fill(N, cols, "dy_t", dev)[0]
+        a.x_t = x_t._fill(K, cols, "x_t", dev)[0]
+        item = dw.element_size()
+        if item not in (2, 4):
+            raise ValueError("dw: bf16 or fp32")
+        a.dw, a.lddw, a.dw_group = _groups_of(dw, g, N, K, "dw", dev, item)
+        a.grad_fp32, a.accumulate = int(item == 4), int(bool(accumulate))
+    L = lib()
+    if query:
+        need = C.c_int64()
+        _check(L.ve_fp8_linear_backward_workspace(C.byref(a), C.byref(need)))
+        return need.value
+    _run(L.ve_fp8_linear_backward, L.ve_fp8_linear_backward_workspace, a, dev, stream, workspace)
+
+
+def _slots(t, shape, dtypes, name, device):
+    """Pointer of a contiguous device tensor of [tokens, slots] values."""
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name}: need {' or '.join(str(d) for d in dtypes)} elements")
+    if t.device != device or not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{name}: must be a contiguous device tensor on {device}")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name}: shape {tuple(t.shape)} != {tuple(shape)}")
+    return t.data_ptr()
+
+
+def expert_sort(experts, offsets, position, order=None, workspace=None, stream=None):
+    """``ve_expert_sort``: slots in the order of their expert.
+
+    ``experts`` [tokens, slots], int32 or int64, a router's choice (slots of
+    experts outside [0, groups) take no part); ``offsets`` [groups + 1], int64,
+    receives the offsets of the grouped products; ``position`` [tokens, slots],
+    int32, each slot's place or -1; ``order`` [tokens * slots], int32 (or None),
+    the slot at each place.  ``workspace``: uint8, at least
+    :func:`expert_sort_workspace` bytes (allocated here if None)."""
+    _types()
+    dev, t = experts.device, _torch
+    if experts.dim() != 2 or offsets.dim() != 1 or offsets.shape[0] < 2:
+        raise ValueError("experts: [tokens, slots], offsets: [groups + 1]")
+    T, k = experts.shape
+    e = _slots(experts, None, (t.int64, t.int32), "experts", dev)
+    p = _slots(position, experts.shape, (t.int32,), "position", dev)
+    o = _slots(offsets, None, (t.int64,), "offsets", dev)
+    r = 0 if order is None else _slots(order, (T * k,), (t.int32,), "order", dev)
+    L, handle = lib(), _stream_on(dev, stream)
+    n = offsets.shape[0] - 1
+    if workspace is None:
+        need = C.c_int64()
+        _check(L.ve_expert_sort_workspace(T, k, n, C.byref(need)))
+        ws, size = (_scratch(need.value, dev, stream), need.value) if need.value else (None, 0)
+    else:
+        if workspace.device != dev:
+            raise ValueError("workspace: must be on the tensors' device")
+        _require_buffer(workspace, 0, 1, "workspace")
+        ws, size = workspace, workspace.numel()
+    _call(dev, L.ve_expert_sort, e, experts.element_size(), T, k, n, o, p, r, 0 if ws is None else ws.data_ptr(), size,
+          handle)
+
+
+def expert_sort_workspace(tokens: int, slots: int, groups: int) -> int:
+    """``ve_expert_sort_workspace`` (bytes)."""
+    need = C.c_int64()
+    _check(lib().ve_expert_sort_workspace(tokens, slots, groups, C.byref(need)))
+    return need.value
+
+
+def _slot_args(a, tokens, cols, position, weights, device):
+    _types()
+    if position.dim() != 2 or position.shape[0] != tokens:
+        raise ValueError(f"position: [{tokens} tokens, slots]")
+    a.tokens, a.cols, a.slots = tokens, cols, position.shape[1]
+    a.position = _slots(position, None, (_torch.int32,), "position", device)
+    if weights is not None:
+        a.weights = _slots(weights, position.shape, (_torch.float32,), "weights", device)
+
+
+def expert_gather(x, position, out, weights=None, stream=None):
+    """``ve_expert_gather``: every slot's row of ``out`` is its token's row of
+    the bf16 ``x`` [tokens, cols], times its weight (fp32 [tokens, slots]) if
+    given.  ``out`` [rows, cols] is a bf16 tensor or an :class:`Fp8`
+    (block_rows 1, no weights), whose rows are packed on the way.  The gradient
+    is :func:`expert_combine` of the rows' gradients."""
+    a, dev = _ExpertGather(), x.device
+    if x.dim() != 2 or len(out.shape) != 2:
+        raise ValueError("x: [tokens, cols], out: [rows, cols]")
+    T, cols = x.shape
+    _slot_args(a, T, cols, position, weights, dev)
+    a.x, a.ldx = _matrix(x, T, cols, "x", dev)
+    a.rows_len = out.shape[0]
+    if isinstance(out, Fp8):
+        a.rows8 = out._fill(a.rows_len, cols, "out", dev)[0]
+    else:
+        a.rows, a.ld_rows = _matrix(out, a.rows_len, cols, "out", dev)
+    _call(dev, lib().ve_expert_gather, C.byref(a), _stream_on(dev, stream))
+    return out
+
+
+def expert_combine(rows, position, y, weights=None, residual=None, stream=None):
+    """``ve_expert_combine``: ``y`` [tokens, cols] = the weighted sums of the
+    slots' rows, plus ``residual`` (which may be ``y``)."""
+    a, dev = _ExpertCombine(), y.device
+    if y.dim() != 2 or rows.dim() != 2:
+        raise ValueError("y: [tokens, cols], rows: [rows, cols]")
+    T, cols = y.shape
+    _slot_args(a, T, cols, position, weights, dev)
+    a.rows_len = rows.shape[0]
+    a.rows, a.ld_rows = _matrix(rows, a.rows_len, cols, "rows", dev)
+    if residual is not None:
+        a.residual, a.ldr = _matrix(residual, T, cols, "residual", dev)
+    a.y, a.ldy = _matrix(y, T, cols, "y", dev)
+    _call(dev, lib().ve_expert_combine, C.byref(a), _stream_on(dev, stream))
+    return y
+
+
+def expert_combine_backward(dy, position, rows=None, weights=None, drows=None, dweights=None, stream=None):
+    """``ve_expert_combine_backward``: ``drows`` [rows, cols] (bf16) and
+    ``dweights`` [tokens, slots] (fp32, needs ``rows``) from ``dy`` [tokens,
+    cols]; either may be None."""
+    a, dev = _ExpertCombineBackward(), dy.device
+    if dy.dim() != 2:
+        raise ValueError("dy: [tokens, cols]")
+    T, cols = dy.shape
+    _slot_args(a, T, cols, position, weights, dev)
+    a.dy, a.lddy = _matrix(dy, T, cols, "dy", dev)
+    lens = {t.shape[0] for t in (rows, drows) if t is not None}
+    if len(lens) > 1:
+        raise ValueError("rows and drows: as many rows")
+    a.rows_len = lens.pop() if lens else 0
+    if dweights is not None:
+        if rows is None:
+            raise ValueError("dweights needs rows")
+        a.rows, a.ld_rows = _matrix(rows, a.rows_len, cols, "rows", dev)
+        a.dweights = _slots(dweights, position.shape, (_torch.float32,), "dweights", dev)
+    if drows is not None:
+        a.drows, a.ld_drows = _matrix(drows, a.rows_len, cols, "drows", dev)
+    _call(dev, lib().ve_expert_combine_backward, C.byref(a), _stream_on(dev, stream))
 
 
 def stream_copy(dst, src, stream=None):

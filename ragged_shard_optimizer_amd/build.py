@@ -24,7 +24,9 @@ OUT = os.path.join(PKG, "_build", "libve.so")
 SOURCES = [os.path.join(CSRC, f) for f in ("ve_host.cpp", "ve_planner.cpp", "ve_muon_host.cpp", "ve_kernels.hip", "ve_group.hip",
                                            "ve_muon.hip", "ve_stream.hip",
                                            "ve_muon_static.hip",
-                                           "ve_linear_host.cpp", "ve_linear.hip", "ve_act8.hip")]
+                                           "ve_linear_host.cpp", "ve_linear.hip", "ve_act8.hip",
+                                           "ve_expert_host.cpp", "ve_expert.hip",
+                                           "ve_fp8_host.cpp", "ve_fp8_pack.hip", "ve_fp8.hip")]
 ARCH = "gfx950"
 
 HIPCC_FLAGS = [
