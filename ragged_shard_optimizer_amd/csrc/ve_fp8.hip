@@ -75,20 +75,332 @@ __device__ __forceinline__ i32x8 fragment(const uint16_t* st, int r0, int kk, in
     return i32x8{(int)lo.x, (int)lo.y, (int)lo.z, (int)lo.w, (int)hi.x, (int)hi.y, (int)hi.z, (int)hi.w};
 }
 
-// Exponents of the `rows` (at most 128) rows from r on, in one contraction
-// block, whose exponents start at p: dword l of the lane l (aligned down).
-__device__ __forceinline__ uint32_t load_exponents(const uint8_t* p, int64_t all, int r, int lane) {
-    const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc((void*)p, (short)0, (int)all, 0x00020000);
-    return (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(rs, lane <= 32 ? (r & ~3) + 4 * lane : (int)0x80000000, 0, 0);
+// Exponents of an operand's rows in one contraction block after the other: a
+// wave's at most 128 rows from `row` on are 33 aligned dwords, dword l in lane
+// l.
+struct Exponents {
+    const uint8_t* p;  // the block's first
+    int ld, row, all;  // to the next block; the wave's first row; rows up to a multiple of 4
+    __device__ __forceinline__ void init(const uint8_t* base, int64_t ld_, int row_, int64_t all_) {
+        p = (const uint8_t*)uniform64((int64_t)base);
+        ld = __builtin_amdgcn_readfirstlane((int)ld_);
+        row = __builtin_amdgcn_readfirstlane(row_);
+        all = __builtin_amdgcn_readfirstlane((int)all_);
+    }
+    __device__ __forceinline__ uint32_t load(int lane, bool live) const {
+        const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc((void*)p, (short)0, live ? all : 0, 0x00020000);
+        return (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(rs, lane <= 32 ? (row & ~3) + 4 * lane : (int)0x80000000, 0, 0);
+    }
+    __device__ __forceinline__ void next() { p += ld; }
+    __device__ __forceinline__ void stash(uint32_t& keep, int at) const {
+        put_lane(keep, at, (uint32_t)(uintptr_t)p);
+        put_lane(keep, at + 1, (uint32_t)((uintptr_t)p >> 32));
+        put_lane(keep, at + 2, (uint32_t)ld);
+        put_lane(keep, at + 3, (uint32_t)row);
+        put_lane(keep, at + 4, (uint32_t)all);
+    }
+    __device__ __forceinline__ void unstash(uint32_t keep, int at) {
+        const uint64_t lo = get_lane(keep, at), hi = get_lane(keep, at + 1);
+        p = (const uint8_t*)(uintptr_t)((hi << 32) | lo);
+        ld = (int)get_lane(keep, at + 2);
+        row = (int)get_lane(keep, at + 3);
+        all = (int)get_lane(keep, at + 4);
+    }
+};
+// ... to the dword with a lane's exponent of row `row` + 32 a + lane % 32, which
+// is `spread_shift` bits up.
+__device__ __forceinline__ uint32_t spread_dword(uint32_t raw, int row, int a, int lane) {
+    return (uint32_t)__builtin_amdgcn_ds_bpermute((8 * a + (((row & 3) + (lane & 31)) >> 2)) * 4, (int)raw);
 }
-// ... to a lane's exponent of row r + 32 a + lane % 32 (in the low byte).
-__device__ __forceinline__ int spread(uint32_t raw, int r, int a, int lane) {
-    const int b = (r & 3) + (lane & 31);
-    return (int)((uint32_t)__builtin_amdgcn_ds_bpermute((8 * a + (b >> 2)) * 4, (int)raw) >> (8 * (b & 3)));
+__device__ __forceinline__ uint32_t spread_shift(int row, int lane) { return 8 * ((row + lane) & 3); }
+__device__ __forceinline__ int spread(uint32_t raw, int row, int a, int lane) {
+    return (int)(spread_dword(raw, row, a, lane) >> spread_shift(row, lane));
 }
 
-template <class CF, int KIND, int FORMAT, bool EXACT>
+// The arguments, read from memory again.
+__device__ __forceinline__ Fp8Args fp8_args_again() {
+    auto p = (const __attribute__((address_space(4))) uint32_t*)__builtin_amdgcn_kernarg_segment_ptr();
+    asm volatile("" : "+s"(p));
+    static_assert(sizeof(Fp8Args) % 4 == 0, "whole words");
+    uint32_t w[sizeof(Fp8Args) / 4];
+#pragma unroll
+    for (int i = 0; i < (int)(sizeof(Fp8Args) / 4); ++i) w[i] = p[i];
+    Fp8Args h;
+    __builtin_memcpy(&h, w, sizeof(h));
+    return h;
+}
+
+// Workgroups that stay on their CUs and run one stream of steps over their
+// items, as the bf16 product's (ve_linear.hip): a step has the same bytes,
+// the same LDS reads and as many cycles of MFMA, for twice the contraction.
+// The exponents of a step are two loads of a dword a lane, two steps ahead,
+// which the lanes exchange once the step's tile is there.
+template <class CF, int KIND, int FORMAT>
 __global__ void __launch_bounds__(CF::THREADS, CF::PER_CU) k_fp8(Fp8Args g) {
+    constexpr int TM = CF::TM, TN = CF::TN, WM = CF::WM, WN = CF::WN;
+    constexpr int NF = TM + TN, MM = TM * TN, H = MM / 2;
+    constexpr int EB = KIND == kLinDw ? TN : 1;  // exponents of the columns: each lane's, or the wave's
+    __shared__ __attribute__((aligned(1024))) unsigned char smem[CF::SMEM];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+    const int wr = wave / CF::WAVES_N, wc = wave % CF::WAVES_N;
+    uint16_t* ops = (uint16_t*)smem;
+    unsigned char* sw = smem + CF::STAGES_BYTES + wave * CF::OUT_BYTES;
+    auto stage = [&](uint32_t s) { return ops + (s & 1) * CF::STAGE_ELEMS; };
+
+    const uint32_t total = all_tiles<CF, KIND>(g);
+    uint32_t ci = blockIdx.x, li = ci;  // items computed and loaded
+    Work cw;
+    bool cok = fetch<CF, KIND, true>(g, total, ci, cw);
+    if (!cok) return;
+    typedef Operand<false, CF::BM, CF::WAVES, true> OpA;
+    typedef Operand<false, CF::BN, CF::WAVES, true> OpB;
+    OpA A;
+    OpB B;
+    Exponents XA, XB;
+    constexpr int PA = OpA::PIECES, PB = OpB::PIECES, P = PA + PB, SPAN = MM;
+    static_assert(SPAN <= H + MM, "loads of a step must be issued before its barrier");
+
+    // The loads' position: step lk of the item's steps up to lend; lok: there
+    // is an item.
+    int lk = 0, lend = 0;
+    bool lok = true;
+    uint32_t item = 0;
+    auto next_loaded = [&](bool first) {  // the next item with steps
+        const Fp8Args h = fp8_args_again();
+        Work w;
+        do {
+            if (!first) li += gridDim.x;
+            first = false;
+            lok = __builtin_amdgcn_readfirstlane(fetch<CF, KIND, true>(h, total, li, w)) != 0;
+            w.nk = __builtin_amdgcn_readfirstlane(w.nk);
+        } while (lok && w.nk == 0);
+        if (!lok) return;
+        // what the item's epilogue will need, in lanes of a vector register
+        put_lane(item, 0, (uint32_t)w.e);
+        put_lane(item, 1, (uint32_t)w.row0);
+        put_lane(item, 2, (uint32_t)w.rows);
+        put_lane(item, 3, (uint32_t)w.col0);
+        put_lane(item, 4, (uint32_t)w.nk);
+        put_lane(item, 5, (uint32_t)w.slice);
+        put_lane(item, 6, w.t);
+        lk = __builtin_amdgcn_readfirstlane(w.kbeg);
+        lend = __builtin_amdgcn_readfirstlane(w.kbeg + w.nk);
+        const int cols = min((int)h.N - w.col0, CF::BN);
+        const int ra = w.row0 + wr * WM, rb = w.col0 + wc * WN;
+        if constexpr (KIND == kLinDw) {
+            A.init(h.A + w.row0 * h.lda + w.begin, h.lda, w.rows, w.len, lane, wave);
+            B.init(h.B + w.col0 * h.ldb + w.begin, h.ldb, cols, w.len, lane, wave);
+            XA.init(h.sa + (w.begin / BK + lk) * h.ld_sa, h.ld_sa, ra, h.sa_rows);
+            XB.init(h.sb + (w.begin / BK + lk) * h.ld_sb, h.ld_sb, rb, h.sb_rows);
+        } else {
+            A.init(h.A + w.row0 * h.lda, h.lda, w.rows, (int)h.K, lane, wave);
+            B.init(h.B + w.e * h.b_group + w.col0 * h.ldb, h.ldb, cols, (int)h.K, lane, wave);
+            XA.init(h.sa + lk * h.ld_sa, h.ld_sa, ra, h.sa_rows);
+            XB.init(h.sb + w.e * h.sb_group + lk * h.ld_sb, h.ld_sb, rb >> 7, h.sb_rows);
+        }
+        A.make_uniform();
+        B.make_uniform();
+    };
+    uint32_t raw_a = 0, raw_b = 0;  // exponents of the step that the loads are at
+    int at_a = 0, at_b = 0;         // and their first rows
+    auto begin = [&]() {
+        A.begin(lk, lok);
+        B.begin(lk, lok);
+    };
+    auto begin_exponents = [&]() {
+        raw_a = XA.load(lane, lok);
+        raw_b = XB.load(lane, lok);
+        at_a = XA.row;
+        at_b = XB.row;
+    };
+    auto advance = [&]() {
+        XA.next();
+        XB.next();
+        if (lok && ++lk >= lend) next_loaded(false);
+    };
+    auto advance_inside = [&]() {
+        XA.next();
+        XB.next();
+        ++lk;
+    };
+    // the pieces of slot s (s MFMAs behind the barrier)
+    auto pieces = [&](int slot, uint32_t s) {
+#pragma unroll
+        for (int p = 0; p < P; ++p)
+            if (p * SPAN / P == slot) {
+                if (p < PA) A.piece(stage(s), p);
+                else B.piece(stage(s) + CF::A_ELEMS, p - PA);
+            }
+    };
+    auto barrier = [&]() {
+        asm volatile("" ::: "memory");
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+    };
+
+    f32x16 acc[TM][TN];
+    i32x8 fa[2][TM], fb[2][TN];
+    int ea[TM], eb[EB];             // exponents of the step
+    uint32_t na[TM], nb[EB];        // of the next: dwords, and where in them
+    uint32_t shift_a, shift_b;
+    auto exchange = [&]() {
+#pragma unroll
+        for (int a = 0; a < TM; ++a) na[a] = spread_dword(raw_a, at_a, a, lane);
+        shift_a = spread_shift(at_a, lane);
+        if constexpr (KIND == kLinDw) {
+#pragma unroll
+            for (int b = 0; b < TN; ++b) nb[b] = spread_dword(raw_b, at_b, b, lane);
+            shift_b = spread_shift(at_b, lane);
+        } else {
+            nb[0] = get_lane(raw_b, 0);
+            shift_b = 8 * (at_b & 3);
+        }
+    };
+    auto exponents = [&]() {
+#pragma unroll
+        for (int a = 0; a < TM; ++a) ea[a] = (int)(na[a] >> shift_a);
+#pragma unroll
+        for (int b = 0; b < EB; ++b) eb[b] = (int)(nb[b] >> shift_b);
+    };
+    // fragment f of half kk in the order the MFMAs need them: A0, all B, the other A
+    auto frag1 = [&](int f, int kk, uint32_t s) {
+        const uint16_t* st = stage(s);
+        if (f == 0 || f > TN) {
+            const int a = f == 0 ? 0 : f - TN;
+            fa[kk][a] = fragment<OpA>(st, wr * WM + a * 32, kk, lane);
+        } else {
+            fb[kk][f - 1] = fragment<OpB>(st + CF::A_ELEMS, wc * WN + (f - 1) * 32, kk, lane);
+        }
+    };
+    auto mfma = [&](int kk, int m) {
+        const int a = m / TN, b = m % TN;
+        acc[a][b] = mfma_fp8(fb[kk][b], fa[kk][a], acc[a][b], eb[b % EB], ea[a], FORMAT);
+    };
+
+    next_loaded(true);
+    if (!lok) {  // items without steps only: their rows of dw are zeros, or kept
+        A.init(g.A, g.lda, 1, 1, lane, wave);
+        B.init(g.B, g.ldb, 1, 1, lane, wave);
+        XA.init(g.sa, 0, 0, 0);
+        XB.init(g.sb, 0, 0, 0);
+    }
+    begin();
+    begin_exponents();
+#pragma unroll
+    for (int q = 0; q < PA; ++q) A.piece(stage(0), q);
+#pragma unroll
+    for (int q = 0; q < PB; ++q) B.piece(stage(0) + CF::A_ELEMS, q);
+    __builtin_amdgcn_s_waitcnt(kWaitAll);
+    exchange();
+    exponents();
+    advance();
+    begin();
+    begin_exponents();
+#pragma unroll
+    for (int m = 0; m < H; ++m) pieces(m, 1);
+    barrier();
+#pragma unroll
+    for (int f = 0; f < NF; ++f) frag1(f, 0, 0);
+
+    uint32_t s = 0;  // steps computed, over all items
+    while (cok) {
+#pragma unroll
+        for (int a = 0; a < TM; ++a)
+#pragma unroll
+            for (int b = 0; b < TN; ++b)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) acc[a][b][r] = 0.f;
+        // Every MFMA is followed by its share of what feeds the later ones,
+        // in this order (the scheduling barriers keep it).  In the middle of a
+        // step's second half all its reads are complete: the barrier there
+        // frees its stage and makes the next one visible, and from there on
+        // the loads of the step after the next go out into the freed stage.
+        auto step = [&](auto&& next) {
+#pragma unroll
+            for (int m = 0; m < MM; ++m) {
+                mfma(0, m);
+#pragma unroll
+                for (int f = m * NF / MM; f < (m + 1) * NF / MM; ++f) frag1(f, 1, s);
+                pieces(H + m, s + 1);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            next();
+#pragma unroll
+            for (int m = 0; m < H; ++m) mfma(1, m);
+            __builtin_amdgcn_sched_barrier(0);
+            // this wave's loads and LDS reads are complete, then everyone's
+            __builtin_amdgcn_s_waitcnt(kWaitAll);
+            barrier();
+            exchange();
+            begin();
+            begin_exponents();
+#pragma unroll
+            for (int m = H; m < MM; ++m) {
+                mfma(1, m);
+#pragma unroll
+                for (int f = (m - H) * NF / H; f < (m - H + 1) * NF / H; ++f) frag1(f, 0, s + 1);
+                pieces(m - H, s + 2);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            exponents();
+            ++s;
+        };
+        // Nothing of the previous item's epilogue may be pending for the
+        // compiler here (it would wait in every step); the other workgroup of
+        // the CU fills the time.
+        if constexpr (CF::PER_CU > 1) __builtin_amdgcn_s_waitcnt(wait_vm(0));
+        // the loads leave this item behind in its last two steps
+        const int nk = __builtin_amdgcn_readfirstlane(cw.nk);
+        int kt = 0;
+        for (; kt + 2 < nk; ++kt) step(advance_inside);
+        for (; kt < nk; ++kt) step(advance);
+        // the loads' position waits in a vector register while the epilogue
+        // needs the scalar ones
+        uint32_t keep = 0;
+        A.stash(keep, 0);
+        B.stash(keep, 5);
+        XA.stash(keep, 10);
+        XB.stash(keep, 15);
+        put_lane(keep, 20, (uint32_t)lk);
+        put_lane(keep, 21, (uint32_t)lend);
+        put_lane(keep, 22, (uint32_t)lok);
+        put_lane(keep, 23, li);
+        put_lane(keep, 24, (uint32_t)at_a);
+        put_lane(keep, 25, (uint32_t)at_b);
+        if (cw.rows > 0) epilogue<CF, KIND>(fp8_args_again().finish, cw, acc, sw, wr, wc, lane);
+        ci += gridDim.x;
+        if (get_lane(keep, 22) != 0 && get_lane(keep, 23) == ci) {  // the item the loads are at
+            cw.e = (int)get_lane(item, 0);
+            cw.row0 = (int)get_lane(item, 1);
+            cw.rows = (int)get_lane(item, 2);
+            cw.col0 = (int)get_lane(item, 3);
+            cw.nk = (int)get_lane(item, 4);
+            cw.slice = (int)get_lane(item, 5);
+            cw.t = get_lane(item, 6);
+        } else {
+            cok = fetch<CF, KIND, true>(fp8_args_again(), total, ci, cw);
+        }
+        A.unstash(keep, 0);
+        B.unstash(keep, 5);
+        XA.unstash(keep, 10);
+        XB.unstash(keep, 15);
+        lk = (int)get_lane(keep, 20);
+        lend = (int)get_lane(keep, 21);
+        lok = get_lane(keep, 22) != 0;
+        li = get_lane(keep, 23);
+        at_a = (int)get_lane(keep, 24);
+        at_b = (int)get_lane(keep, 25);
+        begin();
+    }
+    // the loads past the last step (of nothing) land before the end
+    __builtin_amdgcn_s_waitcnt(kWaitAll);
+}
+
+// dw in fp32: one item a workgroup, codes turned to bf16 between LDS and the
+// MFMAs.
+template <class CF, int FORMAT>
+__global__ void __launch_bounds__(CF::THREADS, CF::PER_CU) k_fp8_exact(Fp8Args g) {
+    constexpr int KIND = kLinDw;
     constexpr int TM = CF::TM, TN = CF::TN, WM = CF::WM, WN = CF::WN;
     __shared__ __attribute__((aligned(1024))) unsigned char smem[CF::SMEM];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
@@ -100,16 +412,11 @@ __global__ void __launch_bounds__(CF::THREADS, CF::PER_CU) k_fp8(Fp8Args g) {
     OpA A;
     OpB B;
     const int cols = min((int)g.N - w.col0, CF::BN);
-    if (KIND == kLinDw) {
-        A.init(g.A + w.row0 * g.lda + w.begin, g.lda, w.rows, w.len, lane, wave);
-        B.init(g.B + w.col0 * g.ldb + w.begin, g.ldb, cols, w.len, lane, wave);
-    } else {
-        A.init(g.A + w.row0 * g.lda, g.lda, w.rows, (int)g.K, lane, wave);
-        B.init(g.B + w.e * g.b_group + w.col0 * g.ldb, g.ldb, cols, (int)g.K, lane, wave);
-    }
-    const uint8_t* sa = g.sa + (KIND == kLinDw ? w.begin / BK * g.ld_sa : 0);
-    const uint8_t* sb = g.sb + (KIND == kLinDw ? w.begin / BK * g.ld_sb : w.e * g.sb_group);
-    const int ra = w.row0 + wr * WM, rb = KIND == kLinDw ? w.col0 + wc * WN : (w.col0 + wc * WN) >> 7;
+    A.init(g.A + w.row0 * g.lda + w.begin, g.lda, w.rows, w.len, lane, wave);
+    B.init(g.B + w.col0 * g.ldb + w.begin, g.ldb, cols, w.len, lane, wave);
+    Exponents XA, XB;
+    XA.init(g.sa + (w.begin / BK + w.kbeg) * g.ld_sa, g.ld_sa, w.row0 + wr * WM, g.sa_rows);
+    XB.init(g.sb + (w.begin / BK + w.kbeg) * g.ld_sb, g.ld_sb, w.col0 + wc * WN, g.sb_rows);
     f32x16 acc[TM][TN];
 #pragma unroll
     for (int a = 0; a < TM; ++a)
@@ -125,16 +432,16 @@ __global__ void __launch_bounds__(CF::THREADS, CF::PER_CU) k_fp8(Fp8Args g) {
         for (int q = 0; q < OpA::PIECES; ++q) A.piece(st, q);
 #pragma unroll
         for (int q = 0; q < OpB::PIECES; ++q) B.piece(st + CF::A_ELEMS, q);
-        const uint32_t raw_a = load_exponents(sa + kt * g.ld_sa, g.sa_rows, ra, lane);
-        const uint32_t raw_b = load_exponents(sb + kt * g.ld_sb, g.sb_rows, rb, lane);
+        const uint32_t raw_a = XA.load(lane, true), raw_b = XB.load(lane, true);
+        XA.next();
+        XB.next();
         __builtin_amdgcn_s_waitcnt(kWaitAll);
         __syncthreads();
         int ea[TM], eb[TN];
 #pragma unroll
-        for (int a = 0; a < TM; ++a) ea[a] = spread(raw_a, ra, a, lane);
+        for (int a = 0; a < TM; ++a) ea[a] = spread(raw_a, XA.row, a, lane);
 #pragma unroll
-        for (int b = 0; b < TN; ++b)
-            eb[b] = KIND == kLinDw ? spread(raw_b, rb, b, lane) : (int)(get_lane(raw_b, 0) >> (8 * (rb & 3)));
+        for (int b = 0; b < TN; ++b) eb[b] = spread(raw_b, XB.row, b, lane);
 #pragma unroll
         for (int kk = 0; kk < 2; ++kk) {
             i32x8 fa[TM], fb[TN];
@@ -142,25 +449,18 @@ __global__ void __launch_bounds__(CF::THREADS, CF::PER_CU) k_fp8(Fp8Args g) {
             for (int a = 0; a < TM; ++a) fa[a] = fragment<OpA>(st, wr * WM + a * 32, kk, lane);
 #pragma unroll
             for (int b = 0; b < TN; ++b) fb[b] = fragment<OpB>(st + CF::A_ELEMS, wc * WN + b * 32, kk, lane);
-            if constexpr (EXACT) {
-                Wide wa[TM], wb[TN];
+            Wide wa[TM], wb[TN];
 #pragma unroll
-                for (int a = 0; a < TM; ++a) wa[a] = widen(fa[a], ea[a], FORMAT);
+            for (int a = 0; a < TM; ++a) wa[a] = widen(fa[a], ea[a], FORMAT);
 #pragma unroll
-                for (int b = 0; b < TN; ++b) wb[b] = widen(fb[b], eb[b], VE_E4M3);
+            for (int b = 0; b < TN; ++b) wb[b] = widen(fb[b], eb[b], VE_E4M3);
 #pragma unroll
-                for (int q = 0; q < 4; ++q)
-#pragma unroll
-                    for (int a = 0; a < TM; ++a)
-#pragma unroll
-                        for (int b = 0; b < TN; ++b)
-                            acc[a][b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(wb[b].v[q], wa[a].v[q], acc[a][b], 0, 0, 0);
-            } else {
+            for (int q = 0; q < 4; ++q)
 #pragma unroll
                 for (int a = 0; a < TM; ++a)
 #pragma unroll
-                    for (int b = 0; b < TN; ++b) acc[a][b] = mfma_fp8(fb[b], fa[a], acc[a][b], eb[b], ea[a], FORMAT);
-            }
+                    for (int b = 0; b < TN; ++b)
+                        acc[a][b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(wb[b].v[q], wa[a].v[q], acc[a][b], 0, 0, 0);
         }
         __syncthreads();
     }
@@ -174,22 +474,73 @@ hipError_t launch_kind(Fp8Args g, const LinPlan& p, hipStream_t s) {
     g.tiles = tiles_of<CF>(g, (LinKind)KIND);
     if (g.tiles == 0) return hipSuccess;
     g.finish = finish_of(g, (LinKind)KIND);
-    const dim3 grid((unsigned)items_of(g, (LinKind)KIND));
-    if (KIND == kLinDw && g.wide) {
-        if (g.format == VE_E4M3) hipLaunchKernelGGL((k_fp8<CF, kLinDw, VE_E4M3, true>), grid, dim3(CF::THREADS), 0, s, g);
-        else hipLaunchKernelGGL((k_fp8<CF, kLinDw, VE_E5M2, true>), grid, dim3(CF::THREADS), 0, s, g);
-    } else {
-        if (g.format == VE_E4M3) hipLaunchKernelGGL((k_fp8<CF, KIND, VE_E4M3, false>), grid, dim3(CF::THREADS), 0, s, g);
-        else hipLaunchKernelGGL((k_fp8<CF, KIND, VE_E5M2, false>), grid, dim3(CF::THREADS), 0, s, g);
-    }
+    const int64_t items = items_of(g, (LinKind)KIND);
+    const dim3 grid((unsigned)std::min<int64_t>(items, kCUs * CF::PER_CU)), block(CF::THREADS);
+    if (g.format == VE_E4M3) hipLaunchKernelGGL((k_fp8<CF, KIND, VE_E4M3>), grid, block, 0, s, g);
+    else hipLaunchKernelGGL((k_fp8<CF, KIND, VE_E5M2>), grid, block, 0, s, g);
+    if (p.ksplit > 1)
+        hipLaunchKernelGGL((k_join<CF, KIND>), dim3((unsigned)(g.tiles * (CF::BM * (CF::BN / 8) / 256))), dim3(256), 0, s, g);
     return hipGetLastError();
+}
+
+hipError_t launch_exact(Fp8Args g, hipStream_t s) {
+    typedef Cfg128 CF;
+    g.tiles_n = (int)((g.N + CF::BN - 1) / CF::BN);
+    g.ksplit = 1;
+    g.tiles = tiles_of<CF>(g, kLinDw);
+    if (g.tiles == 0) return hipSuccess;
+    g.finish = finish_of(g, kLinDw);
+    const dim3 grid((unsigned)items_of(g, kLinDw)), block(CF::THREADS);
+    if (g.format == VE_E4M3) hipLaunchKernelGGL((k_fp8_exact<CF, VE_E4M3>), grid, block, 0, s, g);
+    else hipLaunchKernelGGL((k_fp8_exact<CF, VE_E5M2>), grid, block, 0, s, g);
+    return hipGetLastError();
+}
+
+// Microseconds of a product as `items` tiles (or slices) of `steps` steps, as
+// for the bf16 products.  Measured: a step of 256 x 256 takes 1.48 us and its
+// start and epilogue 5; of a pair of 128 x 128 tiles 1.06 and 4, of a single
+// one 0.8.
+double fp8_us(bool big, int64_t items, int64_t steps, int64_t bytes) {
+    const double n = (double)((items + kCUs - 1) / kCUs), st = (double)steps;
+    const double sums = bytes ? (double)bytes * 2 / 5e6 + 4 : 0;
+    if (big) return n * (1.48 * st + 5) + sums;
+    const double pairs = (double)((int64_t)n / 2), one = n - 2 * pairs;
+    return pairs * (1.06 * st + 4) + one * (0.8 * st + 4) + sums;
 }
 
 }  // namespace
 
-LinPlan plan_fp8(const Fp8Args&, LinKind) { return LinPlan{kPath128, 1, 0, 0}; }
+LinPlan plan_fp8(const Fp8Args& g, LinKind kind) {
+    LinPlan p{kPath128, 1, 0, 0};
+    if (kind == kLinDw && g.wide) return p;
+    const int64_t pin = option(kOptLinearPath);
+    const int64_t K = kind != kLinDw ? g.K : g.offsets ? (g.T / g.E + 127) / 128 * 64 : g.T;
+    const int64_t nk = std::max<int64_t>(1, (K + BK - 1) / BK);
+    const bool may_split = !g.offsets && option(kOptLinearSplit) != 0;
+    double best = 0;
+    for (int path : {(int)kPath128, (int)kPath256}) {
+        if ((pin == kPath128 || pin == kPath256) && pin != path) continue;
+        const int64_t tiles = path == kPath256 ? tiles_of<Cfg256>(g, kind) : tiles_of<Cfg128>(g, kind);
+        const int64_t slots = kCUs * (path == kPath256 ? Cfg256::PER_CU : Cfg128::PER_CU), area = path == kPath256 ? 65536 : 16384;
+        for (int64_t ks = 1; ks <= 32; ++ks) {
+            if (ks > 1 && (!may_split || nk / ks < 4 || tiles * ks > slots)) break;
+            const double us = fp8_us(path == kPath256, tiles * ks, (nk + ks - 1) / ks, ks > 1 ? tiles * ks * area * 4 : 0);
+            if (best == 0 || us < best) {
+                best = us;
+                p.us = us;
+                p.path = path;
+                p.ksplit = (int)ks;
+                p.partial_bytes = ks > 1 ? ks * tiles * area * 4 : 0;
+            }
+        }
+    }
+    return p;
+}
 
 hipError_t launch_fp8(Fp8Args g, LinKind kind, const LinPlan& p, hipStream_t s) {
+    if (kind == kLinDw && g.wide) return launch_exact(g, s);
+    if (p.path == kPath256)
+        return kind == kLinDw ? launch_kind<Cfg256, kLinDw>(g, p, s) : launch_kind<Cfg256, kLinFwd>(g, p, s);
     return kind == kLinDw ? launch_kind<Cfg128, kLinDw>(g, p, s) : launch_kind<Cfg128, kLinFwd>(g, p, s);
 }
 
