@@ -117,6 +117,281 @@ __device__ __forceinline__ int spread(uint32_t raw, int row, int a, int lane) {
     return (int)(spread_dword(raw, row, a, lane) >> spread_shift(row, lane));
 }
 
+// The groups' rows (kLinFwd) or columns (kLinDw: whole runs of 128), which a
+// wave keeps in registers, group l in lane l, where there are at most 64: a
+// search then needs no memory (2 us less an item of 4 steps).
+template <class CF, int KIND>
+struct Groups {
+    int begin, len, before, tiles;  // before, tiles: row tiles (kLinFwd), runs (kLinDw)
+    bool kept;
+    __device__ __forceinline__ void init(const Fp8Args& g) {
+        begin = len = before = tiles = 0;
+        kept = g.offsets && g.E <= 64;
+        if (!kept) return;
+        const int lane = (int)(threadIdx.x & 63);
+        int64_t b = 0, n = 0;
+        if (lane < g.E) group_rows(g.offsets, lane, g.T, b, n);
+        tiles = (int)((n + (KIND == kLinDw ? 127 : CF::BM - 1)) / (KIND == kLinDw ? 128 : CF::BM));
+        before = tiles;
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) {
+            const int o = __shfl_up(before, d, 64);
+            if (lane >= d) before += o;
+        }
+        before -= tiles;
+        begin = (int)b;
+        len = (int)n;
+    }
+    // tiles of the launch
+    __device__ __forceinline__ uint32_t total(const Fp8Args& g) const {
+        if (KIND == kLinDw || !g.offsets) return (uint32_t)g.tiles;
+        const int64_t rows = kept ? (int)get_lane((uint32_t)(before + tiles), 63) : ragged_total(g.offsets, g.E, g.T, CF::BM);
+        return (uint32_t)min(g.tiles, rows * g.tiles_n);
+    }
+    // kLinFwd: the group of tile t; false: past the last
+    __device__ __forceinline__ bool find(const Fp8Args& g, uint32_t t, RaggedGroup& r) const {
+        if (!kept) return ragged_find(g.offsets, g.E, g.T, CF::BM, t, g.tiles_n, r);
+        const uint64_t hit = __ballot((int64_t)(before + tiles) * g.tiles_n > t);
+        if (!hit) return false;
+        r.e = __builtin_ctzll(hit);
+        r.begin = (int)get_lane((uint32_t)begin, r.e);
+        r.len = (int)get_lane((uint32_t)len, r.e);
+        r.tiles = (int)get_lane((uint32_t)tiles, r.e);
+        r.before = (int)get_lane((uint32_t)before, r.e);
+        return true;
+    }
+    // kLinDw: group e's columns, in pairs
+    __device__ __forceinline__ void columns(const Fp8Args& g, int e, int& first, int& pairs) const {
+        first = 0;
+        pairs = (int)g.T;
+        if (!g.offsets) return;
+        int64_t runs = 0, n = 0;
+        if (kept) {
+            runs = (int)get_lane((uint32_t)before, e);
+            n = (int)get_lane((uint32_t)tiles, e);
+        } else {
+            int mine = 0;
+            for (int i = (int)(threadIdx.x & 63); i < e; i += 64) {
+                int64_t b, l;
+                group_rows(g.offsets, i, g.T, b, l);
+                mine += (int)((l + 127) / 128);
+            }
+#pragma unroll
+            for (int d = 32; d; d >>= 1) mine += __shfl_xor(mine, d, 64);
+            runs = __builtin_amdgcn_readfirstlane(mine);
+            int64_t b, l;
+            group_rows(g.offsets, e, g.T, b, l);
+            n = __builtin_amdgcn_readfirstlane((int)((l + 127) / 128));
+        }
+        // (offsets that break the rules do not lead out of the matrix)
+        first = (int)min(runs * 64, g.K);
+        pairs = (int)min(n * 64, g.K - first);
+    }
+};
+
+// Item i of the launch, as for the bf16 products (fetch in ve_linear_tiles.h):
+// false if there is none, nor any later one of this workgroup.
+template <class CF, int KIND>
+__device__ __forceinline__ bool item_at(const Fp8Args& g, const Groups<CF, KIND>& groups, uint32_t total, uint32_t i, Work& w) {
+    uint32_t t, in;
+    int tm, ti, tj, K;
+    w.e = 0;
+    w.slice = 0;
+    w.begin = 0;
+    w.len = (int)g.T;
+    if (g.ksplit > 1) {
+        t = i / (uint32_t)g.ksplit;
+        w.slice = (int)(i - t * g.ksplit);
+        if (t >= total) return false;
+    } else if (KIND == kLinDw) {
+        const uint32_t in_e = total / (uint32_t)g.E, part = (in_e + 7) / 8, j = i / 8;
+        w.e = (int)(j / part);
+        if (w.e >= g.E) return false;
+        t = (i % 8) * part + j - w.e * part;
+        if (t >= in_e) {  // a hole: the run of this XCD is shorter
+            w.rows = 0;
+            w.nk = 0;
+            return true;
+        }
+    } else {
+        const uint32_t part = (total + 7) / 8, j = i / 8;
+        t = (i % 8) * part + j;
+        if (j >= part || t >= total) return false;
+    }
+    w.t = in = t;
+    if constexpr (KIND == kLinDw) {
+        tm = (int)((g.M + CF::BM - 1) / CF::BM);
+        groups.columns(g, w.e, w.begin, w.len);
+        K = w.len;
+    } else {
+        tm = (int)((g.T + CF::BM - 1) / CF::BM);
+        if (g.offsets) {
+            RaggedGroup r;
+            if (!groups.find(g, t, r)) return false;
+            w.e = r.e;
+            w.begin = (int)r.begin;
+            w.len = (int)r.len;
+            tm = r.tiles;
+            in = t - (uint32_t)r.before * g.tiles_n;
+        }
+        K = (int)g.K;
+    }
+    tile_in<CF>(g, in, tm, ti, tj);
+    w.col0 = tj * CF::BN;
+    const int i0 = ti * CF::BM;
+    w.rows = min((KIND == kLinDw ? (int)g.M : w.len) - i0, CF::BM);
+    w.row0 = KIND == kLinDw ? i0 : w.begin + i0;
+    w.kbeg = 0;
+    w.nk = (int)(((uint32_t)K + BK - 1) / BK);
+    if (g.ksplit > 1) {
+        const int per = (w.nk + g.ksplit - 1) / g.ksplit;
+        w.kbeg = min(w.slice * per, w.nk);
+        w.nk = min(per, w.nk - w.kbeg);
+    }
+    return true;
+}
+
+// Exchanges between the halves of a wave, and between its even and odd rows
+// of 16 lanes: a's upper half (odd rows) against b's lower half (even rows).
+__device__ __forceinline__ void swap_halves(uint32_t& a, uint32_t& b) {
+    const auto r = __builtin_amdgcn_permlane32_swap(a, b, false, false);
+    a = r[0];
+    b = r[1];
+}
+__device__ __forceinline__ void swap_rows(uint32_t& a, uint32_t& b) {
+    const auto r = __builtin_amdgcn_permlane16_swap(a, b, false, false);
+    a = r[0];
+    b = r[1];
+}
+
+// The bf16 epilogue of dw without LDS.  In a 32 x 32 block a lane of half h
+// has 4 consecutive columns 8 q + 4 h of row lane % 32 for each q.  As bf16 (2
+// dwords a q), exchanging q, q + 1 between the halves gives it 8 consecutive
+// ones, and exchanging the two pairs of q between the rows of 16 lanes gives
+// lanes 16 bytes each of 16 rows, 64 consecutive bytes a row.  Two blocks side
+// by side exchange those between lanes i and i + 8, so that a store covers 8
+// rows of 128 bytes, whole lines.  The exchanges undo themselves, which is how
+// what dw holds comes to the accumulators.  dw is written past the caches: its
+// next reader is far away, and the operands stay in them.  A contraction of
+// 512 tokens, 7168 -> 65536 (7,168 tiles of 4 steps): 345 us; 364 without the
+// streaming hint, 381 through LDS as the general epilogue, 441 in rows of 64
+// bytes.
+// What two blocks' lanes have of rows i (i < 16), 4 dwords each, to rows i and
+// i + 8 (i < 8) of both side by side, and back.
+__device__ __forceinline__ void swap_eights(uint32_t& a, uint32_t& b, bool low) {
+    const uint32_t give = low ? b : a;
+    const uint32_t got = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)give, 0x128, 0xf, 0xf, true);  // row_ror:8
+    const uint32_t na = low ? a : got, nb = low ? got : b;
+    a = na;
+    b = nb;
+}
+
+// The packed values of two blocks side by side, p[block][2 q + d], as four
+// stores (16 t + 8 u + lane % 8 the row, p[u][4 t + d] its dwords), and back.
+__device__ __forceinline__ void turn_blocks(uint32_t (&p)[2][8], bool low, bool back) {
+    auto inner = [&]() {
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            if (back) {
+#pragma unroll
+                for (int d = 0; d < 4; ++d) swap_rows(p[c][d], p[c][4 + d]);
+            }
+#pragma unroll
+            for (int d = 0; d < 2; ++d) {
+                swap_halves(p[c][d], p[c][2 + d]);
+                swap_halves(p[c][4 + d], p[c][6 + d]);
+            }
+            if (!back) {
+#pragma unroll
+                for (int d = 0; d < 4; ++d) swap_rows(p[c][d], p[c][4 + d]);
+            }
+        }
+    };
+    if (!back) inner();
+#pragma unroll
+    for (int i = 0; i < 8; ++i) swap_eights(p[0][i], p[1][i], low);
+    if (back) inner();
+}
+
+template <class CF, bool ADD>
+__device__ __forceinline__ void dw_epilogue(const Work& w, f32x16 (&acc)[CF::TM][CF::TN], int wr, int wc, int lane) {
+    constexpr int TM = CF::TM, TN = CF::TN;
+    const LinArgs g = args_again();
+    const int ld = (int)g.lddw, col0 = w.col0 + wc * CF::WN, r = lane & 7;
+    const bool low = (lane & 8) == 0;
+    // the lane's columns of two blocks in a store
+    const int sc = 8 * (lane >> 5) + 16 * ((lane >> 4) & 1) + 32 * ((lane >> 3) & 1);
+    VE_GLOBAL char* out =
+        (VE_GLOBAL char*)((uint16_t*)g.dw + w.e * g.dw_group + (int64_t)(w.row0 + wr * CF::WM) * g.lddw + col0);
+    const int left = w.rows - wr * CF::WM - r;  // rows from the lane's first on
+    u32x4 held[ADD ? 4 : 1];                    // of the next two blocks
+    auto load_held = [&](int a, int b) {
+        if constexpr (ADD) {
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                held[t] = u32x4{0, 0, 0, 0};
+                if (col0 + 64 * b + sc < (int)g.N && left > 32 * a + 8 * t)
+                    held[t] = *(const VE_GLOBAL u32x4*)(out + (uint32_t)((32 * a + 8 * t + r) * ld + 64 * b + sc) * 2);
+            }
+        }
+    };
+    load_held(0, 0);
+    // (not unrolled: the compiler would copy every accumulator at once)
+#pragma unroll 1
+    for (int b = 0; b < TN / 2; ++b) {
+        const bool in = col0 + 64 * b + sc < (int)g.N;
+#pragma unroll
+        for (int a = 0; a < TM; ++a) {
+            float v[2][16];
+#pragma unroll
+            for (int e = 0; e < TN / 2; ++e)
+                if (b == e) {
+#pragma unroll
+                    for (int c = 0; c < 2; ++c)
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) v[c][i] = acc[a][2 * e + c][i];
+                }
+            uint32_t p[2][8];
+            if constexpr (ADD) {
+#pragma unroll
+                for (int t = 0; t < 4; ++t)
+#pragma unroll
+                    for (int d = 0; d < 4; ++d) p[t & 1][4 * (t >> 1) + d] = held[t][d];
+                load_held(a + 1 < TM ? a + 1 : 0, a + 1 < TM ? b : b + 1);
+                turn_blocks(p, low, true);
+#pragma unroll
+                for (int c = 0; c < 2; ++c)
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) v[c][i] += i & 1 ? bf_hi(p[c][i >> 1]) : bf_lo(p[c][i >> 1]);
+            }
+#pragma unroll
+            for (int c = 0; c < 2; ++c)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) p[c][i] = pack_bf16x2(v[c][2 * i], v[c][2 * i + 1]);
+            turn_blocks(p, low, false);
+#pragma unroll
+            for (int t = 0; t < 4; ++t)
+                if (in && left > 32 * a + 8 * t) {
+                    const uint32_t* q = &p[t & 1][4 * (t >> 1)];
+                    stv<true>((VE_GLOBAL u32x4*)(out + (uint32_t)((32 * a + 8 * t + r) * ld + 64 * b + sc) * 2),
+                              u32x4{q[0], q[1], q[2], q[3]});
+                }
+        }
+    }
+}
+
+template <class CF, int KIND>
+__device__ __forceinline__ void fp8_epilogue(int finish, const Work& w, f32x16 (&acc)[CF::TM][CF::TN], unsigned char* sw,
+                                             int wr, int wc, int lane) {
+    if constexpr (KIND == kLinDw) {
+        if (finish == kFinishStore) dw_epilogue<CF, false>(w, acc, wr, wc, lane);
+        else if (finish == kFinishAdd) dw_epilogue<CF, true>(w, acc, wr, wc, lane);
+        else epilogue_of<CF, KIND, kFinishAll>(w, acc, sw, wr, wc, lane);
+    } else {
+        epilogue<CF, KIND>(finish, w, acc, sw, wr, wc, lane);
+    }
+}
+
 // The arguments, read from memory again.
 __device__ __forceinline__ Fp8Args fp8_args_again() {
     auto p = (const __attribute__((address_space(4))) uint32_t*)__builtin_amdgcn_kernarg_segment_ptr();
@@ -138,7 +413,7 @@ __device__ __forceinline__ Fp8Args fp8_args_again() {
 template <class CF, int KIND, int FORMAT>
 __global__ void __launch_bounds__(CF::THREADS, CF::PER_CU) k_fp8(Fp8Args g) {
     constexpr int TM = CF::TM, TN = CF::TN, WM = CF::WM, WN = CF::WN;
-    constexpr int NF = TM + TN, MM = TM * TN, H = MM / 2;
+    constexpr int NF = TM + TN, MM = TM * TN, H = MM / 2;  // H: MFMAs of a step's second half before its barrier
     constexpr int EB = KIND == kLinDw ? TN : 1;  // exponents of the columns: each lane's, or the wave's
     __shared__ __attribute__((aligned(1024))) unsigned char smem[CF::SMEM];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
@@ -147,10 +422,12 @@ __global__ void __launch_bounds__(CF::THREADS, CF::PER_CU) k_fp8(Fp8Args g) {
     unsigned char* sw = smem + CF::STAGES_BYTES + wave * CF::OUT_BYTES;
     auto stage = [&](uint32_t s) { return ops + (s & 1) * CF::STAGE_ELEMS; };
 
-    const uint32_t total = all_tiles<CF, KIND>(g);
+    Groups<CF, KIND> groups;
+    groups.init(g);
+    const uint32_t total = groups.total(g);
     uint32_t ci = blockIdx.x, li = ci;  // items computed and loaded
     Work cw;
-    bool cok = fetch<CF, KIND, true>(g, total, ci, cw);
+    bool cok = item_at<CF, KIND>(g, groups, total, ci, cw);
     if (!cok) return;
     typedef Operand<false, CF::BM, CF::WAVES, true> OpA;
     typedef Operand<false, CF::BN, CF::WAVES, true> OpB;
@@ -158,7 +435,7 @@ __global__ void __launch_bounds__(CF::THREADS, CF::PER_CU) k_fp8(Fp8Args g) {
     OpB B;
     Exponents XA, XB;
     constexpr int PA = OpA::PIECES, PB = OpB::PIECES, P = PA + PB, SPAN = MM;
-    static_assert(SPAN <= H + MM, "loads of a step must be issued before its barrier");
+    static_assert(SPAN <= MM - H + MM, "loads of a step must be issued before its barrier");
 
     // The loads' position: step lk of the item's steps up to lend; lok: there
     // is an item.
@@ -171,7 +448,7 @@ __global__ void __launch_bounds__(CF::THREADS, CF::PER_CU) k_fp8(Fp8Args g) {
         do {
             if (!first) li += gridDim.x;
             first = false;
-            lok = __builtin_amdgcn_readfirstlane(fetch<CF, KIND, true>(h, total, li, w)) != 0;
+            lok = __builtin_amdgcn_readfirstlane(item_at<CF, KIND>(h, groups, total, li, w)) != 0;
             w.nk = __builtin_amdgcn_readfirstlane(w.nk);
         } while (lok && w.nk == 0);
         if (!lok) return;
@@ -272,9 +549,12 @@ __global__ void __launch_bounds__(CF::THREADS, CF::PER_CU) k_fp8(Fp8Args g) {
             fb[kk][f - 1] = fragment<OpB>(st + CF::A_ELEMS, wc * WN + (f - 1) * 32, kk, lane);
         }
     };
-    auto mfma = [&](int kk, int m) {
+    f32x16 zero;
+#pragma unroll
+    for (int r = 0; r < 16; ++r) zero[r] = 0.f;
+    auto mfma = [&](bool first, int kk, int m) {
         const int a = m / TN, b = m % TN;
-        acc[a][b] = mfma_fp8(fb[kk][b], fa[kk][a], acc[a][b], eb[b % EB], ea[a], FORMAT);
+        acc[a][b] = mfma_fp8(fb[kk][b], fa[kk][a], first ? zero : acc[a][b], eb[b % EB], ea[a], FORMAT);
     };
 
     next_loaded(true);
@@ -297,36 +577,32 @@ __global__ void __launch_bounds__(CF::THREADS, CF::PER_CU) k_fp8(Fp8Args g) {
     begin();
     begin_exponents();
 #pragma unroll
-    for (int m = 0; m < H; ++m) pieces(m, 1);
+    for (int m = 0; m < MM - H; ++m) pieces(m, 1);
     barrier();
 #pragma unroll
     for (int f = 0; f < NF; ++f) frag1(f, 0, 0);
 
     uint32_t s = 0;  // steps computed, over all items
     while (cok) {
-#pragma unroll
-        for (int a = 0; a < TM; ++a)
-#pragma unroll
-            for (int b = 0; b < TN; ++b)
-#pragma unroll
-                for (int r = 0; r < 16; ++r) acc[a][b][r] = 0.f;
         // Every MFMA is followed by its share of what feeds the later ones,
         // in this order (the scheduling barriers keep it).  In the middle of a
         // step's second half all its reads are complete: the barrier there
         // frees its stage and makes the next one visible, and from there on
         // the loads of the step after the next go out into the freed stage.
-        auto step = [&](auto&& next) {
+        // An item's first step starts from 0 (clearing the accumulators first
+        // takes 0.5 us).
+        auto step = [&](bool first, auto&& next) {
 #pragma unroll
             for (int m = 0; m < MM; ++m) {
-                mfma(0, m);
+                mfma(first, 0, m);
 #pragma unroll
                 for (int f = m * NF / MM; f < (m + 1) * NF / MM; ++f) frag1(f, 1, s);
-                pieces(H + m, s + 1);
+                pieces(MM - H + m, s + 1);
                 __builtin_amdgcn_sched_barrier(0);
             }
             next();
 #pragma unroll
-            for (int m = 0; m < H; ++m) mfma(1, m);
+            for (int m = 0; m < H; ++m) mfma(false, 1, m);
             __builtin_amdgcn_sched_barrier(0);
             // this wave's loads and LDS reads are complete, then everyone's
             __builtin_amdgcn_s_waitcnt(kWaitAll);
@@ -336,9 +612,9 @@ __global__ void __launch_bounds__(CF::THREADS, CF::PER_CU) k_fp8(Fp8Args g) {
             begin_exponents();
 #pragma unroll
             for (int m = H; m < MM; ++m) {
-                mfma(1, m);
+                mfma(false, 1, m);
 #pragma unroll
-                for (int f = (m - H) * NF / H; f < (m - H + 1) * NF / H; ++f) frag1(f, 0, s + 1);
+                for (int f = (m - H) * NF / (MM - H); f < (m - H + 1) * NF / (MM - H); ++f) frag1(f, 0, s + 1);
                 pieces(m - H, s + 2);
                 __builtin_amdgcn_sched_barrier(0);
             }
@@ -351,9 +627,17 @@ __global__ void __launch_bounds__(CF::THREADS, CF::PER_CU) k_fp8(Fp8Args g) {
         if constexpr (CF::PER_CU > 1) __builtin_amdgcn_s_waitcnt(wait_vm(0));
         // the loads leave this item behind in its last two steps
         const int nk = __builtin_amdgcn_readfirstlane(cw.nk);
-        int kt = 0;
-        for (; kt + 2 < nk; ++kt) step(advance_inside);
-        for (; kt < nk; ++kt) step(advance);
+        if (nk > 0) {
+            step(true, advance);
+        } else {
+#pragma unroll
+            for (int a = 0; a < TM; ++a)
+#pragma unroll
+                for (int b = 0; b < TN; ++b) acc[a][b] = zero;
+        }
+        int kt = 1;
+        for (; kt + 2 < nk; ++kt) step(false, advance_inside);
+        for (; kt < nk; ++kt) step(false, advance);
         // the loads' position waits in a vector register while the epilogue
         // needs the scalar ones
         uint32_t keep = 0;
@@ -367,7 +651,7 @@ __global__ void __launch_bounds__(CF::THREADS, CF::PER_CU) k_fp8(Fp8Args g) {
         put_lane(keep, 23, li);
         put_lane(keep, 24, (uint32_t)at_a);
         put_lane(keep, 25, (uint32_t)at_b);
-        if (cw.rows > 0) epilogue<CF, KIND>(fp8_args_again().finish, cw, acc, sw, wr, wc, lane);
+        if (cw.rows > 0) fp8_epilogue<CF, KIND>(fp8_args_again().finish, cw, acc, sw, wr, wc, lane);
         ci += gridDim.x;
         if (get_lane(keep, 22) != 0 && get_lane(keep, 23) == ci) {  // the item the loads are at
             cw.e = (int)get_lane(item, 0);
@@ -378,7 +662,7 @@ __global__ void __launch_bounds__(CF::THREADS, CF::PER_CU) k_fp8(Fp8Args g) {
             cw.slice = (int)get_lane(item, 5);
             cw.t = get_lane(item, 6);
         } else {
-            cok = fetch<CF, KIND, true>(fp8_args_again(), total, ci, cw);
+            cok = item_at<CF, KIND>(fp8_args_again(), groups, total, ci, cw);
         }
         A.unstash(keep, 0);
         B.unstash(keep, 5);
@@ -406,7 +690,9 @@ __global__ void __launch_bounds__(CF::THREADS, CF::PER_CU) k_fp8_exact(Fp8Args g
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
     const int wr = wave / CF::WAVES_N, wc = wave % CF::WAVES_N;
     Work w;
-    if (!fetch<CF, KIND, true>(g, all_tiles<CF, KIND>(g), blockIdx.x, w) || w.rows == 0) return;
+    Groups<CF, KIND> groups;
+    groups.init(g);
+    if (!item_at<CF, KIND>(g, groups, (uint32_t)g.tiles, blockIdx.x, w) || w.rows == 0) return;
     typedef Operand<false, CF::BM, CF::WAVES, true> OpA;
     typedef Operand<false, CF::BN, CF::WAVES, true> OpB;
     OpA A;

@@ -229,24 +229,8 @@ __device__ __forceinline__ void tile_in(const LinArgs& g, uint32_t in, int tm, i
     ti = (int)(first + r - tj * rows);
 }
 
-// Runs of 128 rows of the groups before group e (a lane each 64 groups).
-__device__ __forceinline__ int runs_before(const int64_t* off, int e, int64_t T) {
-    int runs = 0;
-    for (int i = (int)(threadIdx.x & 63); i < e; i += 64) {
-        int64_t b, len;
-        group_rows(off, i, T, b, len);
-        runs += (int)((len + 127) / 128);
-    }
-#pragma unroll
-    for (int d = 32; d; d >>= 1) runs += __shfl_xor(runs, d, 64);
-    return __builtin_amdgcn_readfirstlane(runs);
-}
-
-// Tile t of a product (kLinDw: of group e): where it lies.  FP8, kLinDw: the
-// contraction is over the columns of transposed matrices, where every group's
-// are whole runs of 128 (g.T tokens with offsets, else columns, in pairs; g.K
-// columns in pairs).
-template <class CF, int KIND, bool FP8 = false>
+// Tile t of a product (kLinDw: of group e): where it lies.
+template <class CF, int KIND>
 __device__ __forceinline__ bool tile_at(const LinArgs& g, uint32_t t, int e, Work& w) {
     int tm, ti, tj;
     uint32_t in = t;
@@ -259,10 +243,6 @@ __device__ __forceinline__ bool tile_at(const LinArgs& g, uint32_t t, int e, Wor
         if (g.offsets) {
             int64_t begin, len;
             group_rows(g.offsets, e, g.T, begin, len);
-            if constexpr (FP8) {
-                begin = min((int64_t)runs_before(g.offsets, e, g.T) * 64, g.K);
-                len = min((len + 127) / 128 * 64, g.K - begin);
-            }
             w.begin = __builtin_amdgcn_readfirstlane((int)begin);
             w.len = __builtin_amdgcn_readfirstlane((int)len);
         }
@@ -290,7 +270,7 @@ __device__ __forceinline__ bool tile_at(const LinArgs& g, uint32_t t, int e, Wor
 // round-robin over the 8 XCDs, each with its own L2, so item i belongs to
 // XCD i % 8 and each XCD takes a contiguous run of the tile sequence; in
 // kLinDw of every group's tiles, because groups differ in length.
-template <class CF, int KIND, bool FP8 = false>
+template <class CF, int KIND>
 __device__ __forceinline__ bool fetch(const LinArgs& g, uint32_t total, uint32_t i, Work& w) {
     uint32_t t;
     int e = 0;
@@ -314,7 +294,7 @@ __device__ __forceinline__ bool fetch(const LinArgs& g, uint32_t total, uint32_t
         t = (i % 8) * part + j;
         if (j >= part || t >= total) return false;
     }
-    if (!tile_at<CF, KIND, FP8>(g, t, e, w)) return false;
+    if (!tile_at<CF, KIND>(g, t, e, w)) return false;
     const int K = KIND == kLinDw ? w.len : (int)g.K;
     w.kbeg = 0;
     w.nk = (int)(((uint32_t)K + BK - 1) / BK);
