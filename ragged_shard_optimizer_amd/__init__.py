@@ -794,9 +794,10 @@ def _rows8(t, groups, rows, cols, unit, name, device):
     whole = -(-cols // unit) * unit
     ld = st[-2] if rows > 1 else whole
     group = st[0] if groups is not None else 0
-    end = t.storage_offset() + ((groups or 1) - 1) * group + (rows - 1) * ld + whole
-    if t.numel() and end > t.untyped_storage().nbytes():
-        raise ValueError(f"{name}: the last row's memory must go on to a multiple of {unit} bytes")
+    if whole != cols and t.numel():
+        end = t.storage_offset() + ((groups or 1) - 1) * group + (rows - 1) * ld + whole
+        if end > t.untyped_storage().nbytes():
+            raise ValueError(f"{name}: the last row's memory must go on to a multiple of {unit} bytes")
     return t.data_ptr(), ld, group
 
 

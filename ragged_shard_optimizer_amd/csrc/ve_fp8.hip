@@ -753,6 +753,118 @@ __global__ void __launch_bounds__(CF::THREADS, CF::PER_CU) k_fp8_exact(Fp8Args g
     epilogue<CF, KIND>(g.finish, w, acc, smem + CF::STAGES_BYTES + wave * CF::OUT_BYTES, wr, wc, lane);
 }
 
+// Few rows a group (forward and dx): bound by reading the weights.  A
+// workgroup takes at most 16 output columns (per) of at most 16 MT rows of one group, and its
+// waves a share of the contraction each, straight from memory to the MFMAs
+// (16x16x128: a lane 32 codes of one row, read as 64 consecutive bytes of 16
+// rows at a time), U blocks in flight; then they join their sums.
+template <int MT> struct FewRows { static constexpr int BM = 16 * MT; };
+constexpr int kFewWaves = 8;
+template <int MT, int U, int FORMAT>
+__global__ void __launch_bounds__(64 * kFewWaves) k_fp8_few(Fp8Args g, int col_blocks, int per) {
+    constexpr int BM = 16 * MT;
+    __shared__ float sums[kFewWaves][BM][16];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+    const uint32_t t = blockIdx.x / (uint32_t)col_blocks;
+    const int n0 = (int)(blockIdx.x - t * col_blocks) * per;
+    int e = 0, rows = (int)min(g.T - (int64_t)t * BM, (int64_t)BM);
+    int64_t row0 = (int64_t)t * BM;
+    if (g.offsets) {
+        Groups<FewRows<MT>, kLinFwd> groups;
+        groups.init(g);
+        RaggedGroup r;
+        if (!groups.find(g, t, r)) return;
+        const int64_t in = (int64_t)(t - (uint32_t)r.before) * BM;
+        e = r.e;
+        row0 = r.begin + in;
+        rows = (int)min(r.len - in, (int64_t)BM);
+    }
+    const int r = lane & 15, cols = min((int)g.N - n0, per), bytes = (int)g.K * 2;
+    const int ldw = (int)g.ldb * 2, ldx = (int)g.lda * 2;
+    // reads past the last row or column leave the buffers and return 0
+    const __amdgpu_buffer_rsrc_t ws = __builtin_amdgcn_make_buffer_rsrc(
+        (void*)(g.B + e * g.b_group + n0 * g.ldb), (short)0, (cols - 1) * ldw + bytes, 0x00020000);
+    const __amdgpu_buffer_rsrc_t xs =
+        __builtin_amdgcn_make_buffer_rsrc((void*)(g.A + row0 * g.lda), (short)0, (rows - 1) * ldx + bytes, 0x00020000);
+    const uint8_t* sw = g.sb + e * g.sb_group + (n0 >> 7);
+    const uint8_t* sx = g.sa + row0;
+    f32x4 acc[MT];
+#pragma unroll
+    for (int m = 0; m < MT; ++m) acc[m] = f32x4{0.f, 0.f, 0.f, 0.f};
+    const int nb = (bytes + 127) / 128, first = nb * wave / kFewWaves, last = nb * (wave + 1) / kFewWaves;
+    for (int k0 = first; k0 < last; k0 += U) {
+        u32x4 w[U][2], x[U][MT][2];
+        int ew[U], ex[U][MT];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int kb = k0 + u;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int at = kb * 128 + 64 * h + 16 * (lane >> 4);
+                const bool in = kb < last && at < bytes;
+                w[u][h] = __builtin_bit_cast(
+                    u32x4, __builtin_amdgcn_raw_buffer_load_b128(ws, in ? r * ldw + at : (int)0x80000000, 0, 0));
+#pragma unroll
+                for (int m = 0; m < MT; ++m)
+                    x[u][m][h] = __builtin_bit_cast(
+                        u32x4, __builtin_amdgcn_raw_buffer_load_b128(xs, in ? (16 * m + r) * ldx + at : (int)0x80000000, 0, 0));
+            }
+            const int kc = min(kb, nb - 1);
+            ew[u] = ((const VE_GLOBAL uint8_t*)sw)[kc * g.ld_sb];
+#pragma unroll
+            for (int m = 0; m < MT; ++m) ex[u][m] = ((const VE_GLOBAL uint8_t*)sx)[kc * g.ld_sa + min(16 * m + r, rows - 1)];
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const i32x8 b = {(int)w[u][0].x, (int)w[u][0].y, (int)w[u][0].z, (int)w[u][0].w,
+                             (int)w[u][1].x, (int)w[u][1].y, (int)w[u][1].z, (int)w[u][1].w};
+#pragma unroll
+            for (int m = 0; m < MT; ++m) {
+                const i32x8 c = {(int)x[u][m][0].x, (int)x[u][m][0].y, (int)x[u][m][0].z, (int)x[u][m][0].w,
+                                 (int)x[u][m][1].x, (int)x[u][m][1].y, (int)x[u][m][1].z, (int)x[u][m][1].w};
+                acc[m] = FORMAT == VE_E4M3
+                             ? __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(b, c, acc[m], 0, 0, 0, ew[u], 0, ex[u][m])
+                             : __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(b, c, acc[m], 0, 1, 0, ew[u], 0, ex[u][m]);
+            }
+        }
+    }
+    // lane: columns 4 (lane / 16) .. + 3 of row lane % 16
+#pragma unroll
+    for (int m = 0; m < MT; ++m) *(f32x4*)&sums[wave][16 * m + r][4 * (lane >> 4)] = acc[m];
+    __syncthreads();
+    const int row = threadIdx.x >> 1, c8 = (threadIdx.x & 1) * 8;
+    if (row >= rows || row >= BM) return;
+    float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int q = 0; q < kFewWaves; ++q) {
+        const f32x4 a = *(const f32x4*)&sums[q][row][c8], b = *(const f32x4*)&sums[q][row][c8 + 4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            v[i] += a[i];
+            v[4 + i] += b[i];
+        }
+    }
+    const int cnt = min(max(cols - c8, 0), 8);
+    bias8<kLinFwd>(g, e, n0 + c8, cnt, v);
+    finish8<kLinFwd>(g, e, row0 + row, n0 + c8, cnt, v, 0);
+}
+
+template <int MT, int U>
+hipError_t launch_few(Fp8Args g, hipStream_t s) {
+    const int64_t tiles = g.offsets ? std::min<int64_t>(g.T, g.T / (16 * MT) + g.E) : (g.T + 16 * MT - 1) / (16 * MT);
+    // Fewer columns a workgroup where 16 leave CUs without work (one token 8192
+    // -> 1024: 7.7 us, with 16 columns 8.5), but not where that reads x of many
+    // rows more often (32 rows 2880 -> 2880: 10.4 against 7.8).
+    const int per = MT == 1 && tiles * ((g.N + 15) / 16) < 2 * kCUs ? 8 : 16;
+    const int col_blocks = (int)((g.N + per - 1) / per);
+    g.tiles_n = 1;
+    g.tiles = tiles;
+    const dim3 grid((unsigned)(tiles * col_blocks)), block(64 * kFewWaves);
+    if (g.format == VE_E4M3) hipLaunchKernelGGL((k_fp8_few<MT, U, VE_E4M3>), grid, block, 0, s, g, col_blocks, per);
+    else hipLaunchKernelGGL((k_fp8_few<MT, U, VE_E5M2>), grid, block, 0, s, g, col_blocks, per);
+    return hipGetLastError();
+}
+
 template <class CF, int KIND>
 hipError_t launch_kind(Fp8Args g, const LinPlan& p, hipStream_t s) {
     g.tiles_n = (int)((g.N + CF::BN - 1) / CF::BN);
@@ -800,6 +912,13 @@ LinPlan plan_fp8(const Fp8Args& g, LinKind kind) {
     LinPlan p{kPath128, 1, 0, 0};
     if (kind == kLinDw && g.wide) return p;
     const int64_t pin = option(kOptLinearPath);
+    // Few rows against the tiles, us a call: dense 8192 -> 8192 of 1 / 16 / 32
+    // / 64 rows 14 / 19 / 26 / 47 against 33 / 34 / 34 / 30; 64 groups 7168 ->
+    // 2048 of 1 / 4 / 8 rows on average 119 / 165 / 192 against 142 / 163 / 160.
+    if (kind == kLinFwd && (pin == kPathFew || (pin == kPathAuto && g.T <= (g.offsets ? 4 * (int64_t)g.E : 32)))) {
+        p.path = kPathFew;
+        return p;
+    }
     const int64_t K = kind != kLinDw ? g.K : g.offsets ? (g.T / g.E + 127) / 128 * 64 : g.T;
     const int64_t nk = std::max<int64_t>(1, (K + BK - 1) / BK);
     const bool may_split = !g.offsets && option(kOptLinearSplit) != 0;
@@ -825,6 +944,7 @@ LinPlan plan_fp8(const Fp8Args& g, LinKind kind) {
 
 hipError_t launch_fp8(Fp8Args g, LinKind kind, const LinPlan& p, hipStream_t s) {
     if (kind == kLinDw && g.wide) return launch_exact(g, s);
+    if (p.path == kPathFew) return g.offsets || g.T <= 16 ? launch_few<1, 8>(g, s) : launch_few<2, 4>(g, s);
     if (p.path == kPath256)
         return kind == kLinDw ? launch_kind<Cfg256, kLinDw>(g, p, s) : launch_kind<Cfg256, kLinFwd>(g, p, s);
     return kind == kLinDw ? launch_kind<Cfg128, kLinDw>(g, p, s) : launch_kind<Cfg128, kLinFwd>(g, p, s);
