@@ -541,10 +541,17 @@ typedef struct {
 } ve_fp8_pack_weight_args;
 ve_status ve_fp8_pack_weight(const ve_fp8_pack_weight_args* a, void* stream);
 
-/* Restore a packed matrix as bf16(code 2^e) (exact, but where it passes
- * bf16's range: codes next to the largest bf16 values may have rounded up to
- * 2^128, and E5M2 codes below 2^-127 2^-6 lose bits). */
-ve_status ve_fp8_unpack(const ve_fp8* in, int64_t rows, int64_t cols, uint16_t* x, int64_t ldx, void* stream);
+/* Restore a packed matrix, or `groups` of them, as bf16(code 2^e) (exact, but
+ * where it passes bf16's range: codes next to the largest bf16 values may
+ * have rounded up to 2^128, and E5M2 codes below 2^-127 2^-6 lose bits).
+ * *_group as for ve_fp8_pack_weight, not read with one group. */
+typedef struct {
+    int64_t rows, cols;               /* rows >= 0 (0: no-op) */
+    int32_t groups;                   /* 1 .. 65536 */
+    ve_fp8 in; int64_t in_codes_group, in_scales_group;
+    uint16_t* x; int64_t ldx, x_group;
+} ve_fp8_unpack_args;
+ve_status ve_fp8_unpack(const ve_fp8_unpack_args* a, void* stream);
 
 /* A linear layer's products on packed matrices, dense or grouped by expert:
  *   z[t,n] = sum_k x[t,k] w[e,n,k] + bias[e,n],  y[t,n] = bf16(act(z[t,n]) + residual[t,n])

@@ -112,6 +112,12 @@ class _Fp8PackWeight(C.Structure):
                 ("out_t", _Fp8), ("out_t_codes_group", C.c_int64), ("out_t_scales_group", C.c_int64)]
 
 
+class _Fp8Unpack(C.Structure):
+    _fields_ = [("rows", C.c_int64), ("cols", C.c_int64), ("groups", C.c_int32),
+                ("in_", _Fp8), ("in_codes_group", C.c_int64), ("in_scales_group", C.c_int64),
+                ("x", C.c_void_p), ("ldx", C.c_int64), ("x_group", C.c_int64)]
+
+
 class _Fp8Forward(C.Structure):
     _fields_ = _SHAPE_FIELDS + [
         ("x", _Fp8), ("w", _Fp8), ("w_codes_group", C.c_int64), ("w_scales_group", C.c_int64),
@@ -185,7 +191,7 @@ def lib() -> C.CDLL:
         L.ve_fp8_columns.argtypes = [C.c_int64, C.c_int32]
         L.ve_fp8_pack.argtypes = [P, P]
         L.ve_fp8_pack_weight.argtypes = [P, P]
-        L.ve_fp8_unpack.argtypes = [P, C.c_int64, C.c_int64, P, C.c_int64, P]
+        L.ve_fp8_unpack.argtypes = [P, P]
         L.ve_fp8_linear_forward_workspace.argtypes = [P, P]
         L.ve_fp8_linear_forward.argtypes = [P, P, C.c_int64, P]
         L.ve_fp8_linear_backward_workspace.argtypes = [P, P]
@@ -857,18 +863,16 @@ def fp8_pack_weight(w, out: Fp8 = None, out_t: Fp8 = None, stream=None):
 
 
 def fp8_unpack(q: Fp8, out, stream=None):
-    """``ve_fp8_unpack``: restore a packed matrix as bf16 into ``out`` (of
-    grouped weights, one group after the other)."""
-    if out.dim() == 3:
-        if q.codes.dim() != 3 or q.codes.shape[0] != out.shape[0]:
-            raise ValueError("q: as many groups as out")
-        for e in range(out.shape[0]):
-            fp8_unpack(Fp8(q.codes[e], q.scales[e], q.block_rows), out[e], stream)
-        return out
-    rows, cols = out.shape
-    ptr, ld = _matrix(out, rows, cols, "out", out.device)
-    s = q._fill(rows, cols, "q", out.device)[0]
-    _call(out.device, lib().ve_fp8_unpack, C.byref(s), rows, cols, ptr, ld, _stream_on(out.device, stream))
+    """``ve_fp8_unpack``: restore a packed matrix (or [groups, rows, cols] of
+    them) as bf16 into ``out``."""
+    a, dev = _Fp8Unpack(), out.device
+    if out.dim() not in (2, 3):
+        raise ValueError("out: [rows, cols], or [groups, rows, cols]")
+    g = out.shape[0] if out.dim() == 3 else None
+    a.rows, a.cols, a.groups = out.shape[-2], out.shape[-1], 1 if g is None else g
+    a.in_, a.in_codes_group, a.in_scales_group = q._fill(a.rows, a.cols, "q", dev, g)
+    a.x, a.ldx, a.x_group = _groups_of(out, g, a.rows, a.cols, "out", dev)
+    _call(dev, lib().ve_fp8_unpack, C.byref(a), _stream_on(dev, stream))
     return out
 
 

@@ -29,7 +29,8 @@ ve_status check_groups(int64_t rows, int64_t cols, int32_t groups) {
 ve_status check_group_strides(const ve_fp8& q, int64_t rows, int64_t cols, int32_t groups, int64_t codes, int64_t scales,
                               const char* name) {
     if (groups == 1) return VE_OK;
-    if (codes < (rows - 1) * q.ld_codes + cols || scales < (scale_rows(cols) - 1) * q.ld_scales + (rows + 127) / 128)
+    if (codes < (rows - 1) * q.ld_codes + cols ||
+        scales < (scale_rows(cols) - 1) * q.ld_scales + (rows + q.block_rows - 1) / q.block_rows)
         return fail(VE_ERR_INVALID_ARG, "%s: group stride smaller than a group", name);
     if (codes % 16 || scales % 4) return fail(VE_ERR_INVALID_ARG, "%s: groups must start on 16 bytes, scales on 4", name);
     return VE_OK;
@@ -281,22 +282,30 @@ ve_status ve_fp8_pack_weight(const ve_fp8_pack_weight_args* p, void* stream) {
     return status_of(launch_fp8_pack(g, (hipStream_t)stream), "fp8 weight pack");
 }
 
-ve_status ve_fp8_unpack(const ve_fp8* in, int64_t rows, int64_t cols, uint16_t* x, int64_t ldx, void* stream) {
-    if (!in) return fail(VE_ERR_INVALID_ARG, "in is NULL");
-    ve_status st = check_groups(rows, cols, 1);
+ve_status ve_fp8_unpack(const ve_fp8_unpack_args* p, void* stream) {
+    if (!p) return fail(VE_ERR_INVALID_ARG, "arguments are NULL");
+    const ve_fp8_unpack_args& a = *p;
+    ve_status st = check_groups(a.rows, a.cols, a.groups);
     if (st != VE_OK) return st;
-    if (ldx < cols) return fail(VE_ERR_INVALID_ARG, "leading dimension smaller than the row");
-    if (rows == 0) return VE_OK;
-    if (!x) return fail(VE_ERR_INVALID_ARG, "x is NULL");
-    if (in->block_rows != 1 && in->block_rows != 128)
-        return fail(VE_ERR_INVALID_ARG, "in: %d rows share a scale, not 1 or 128", in->block_rows);
-    if ((st = check_fp8(*in, rows, cols, in->block_rows, "in")) != VE_OK) return st;
-    if (rows > kMaxWorkgroups * 8192 / (cols + 128)) return fail(VE_ERR_UNSUPPORTED, "matrix too large for one launch");
-    st = check_apart({matrix_span("x", x, rows, cols, ldx, 2)},
-                     {fp8_codes_span("codes", *in, rows, cols), fp8_scales_span("scales", *in, rows, cols)});
+    const int64_t E = a.groups, R = a.rows, C = a.cols;
+    if (a.ldx < C) return fail(VE_ERR_INVALID_ARG, "leading dimension smaller than the row");
+    if (R == 0) return VE_OK;
+    if (!a.x) return fail(VE_ERR_INVALID_ARG, "x is NULL");
+    if (a.in.block_rows != 1 && a.in.block_rows != 128)
+        return fail(VE_ERR_INVALID_ARG, "in: %d rows share a scale, not 1 or 128", a.in.block_rows);
+    if ((st = check_fp8(a.in, R, C, a.in.block_rows, "in")) != VE_OK ||
+        (st = check_group_strides(a.in, R, C, a.groups, a.in_codes_group, a.in_scales_group, "in")) != VE_OK)
+        return st;
+    if (E > 1 && a.x_group < (R - 1) * a.ldx + C) return fail(VE_ERR_INVALID_ARG, "group stride smaller than a group");
+    if (!tiles_fit(R, C, 0, E)) return fail(VE_ERR_UNSUPPORTED, "matrices too large for one launch");
+    st = check_apart({group_span("x", a.x, E, R, C, a.ldx, a.x_group, 2)},
+                     {fp8_codes_span("codes", a.in, E, R, C, a.in_codes_group),
+                      fp8_scales_span("scales", a.in, E, R, C, a.in_scales_group)});
     if (st != VE_OK) return st;
+    ve_fp8_unpack_args g = a;
+    if (E == 1) g.in_codes_group = g.in_scales_group = g.x_group = 0;
     (void)hipGetLastError();
-    return status_of(launch_fp8_unpack(*in, rows, cols, x, ldx, (hipStream_t)stream), "fp8 unpack");
+    return status_of(launch_fp8_unpack(g, (hipStream_t)stream), "fp8 unpack");
 }
 
 ve_status ve_fp8_linear_forward_workspace(const ve_fp8_linear_forward_args* a, int64_t* bytes) {

@@ -23,6 +23,6 @@ struct Fp8PackArgs {
     int32_t tiles_n, tiles_m;  // set by the launcher
 };
 hipError_t launch_fp8_pack(Fp8PackArgs a, hipStream_t s);
-hipError_t launch_fp8_unpack(const ve_fp8& q, int64_t rows, int64_t cols, uint16_t* x, int64_t ldx, hipStream_t s);
+hipError_t launch_fp8_unpack(const ve_fp8_unpack_args& a, hipStream_t s);
 
 }  // namespace ve

@@ -221,14 +221,17 @@ __global__ void __launch_bounds__(256) k_fp8_pack(Fp8PackArgs a) {
     }
 }
 
-constexpr int kItems = 4;  // groups of 8 columns a thread handles, all loaded before the first is used
+constexpr int kItems = 2;  // groups of 16 columns a thread handles, all loaded before the first is used
 
-__global__ void __launch_bounds__(256) k_fp8_unpack(ve_fp8 q, int64_t rows, int cols, uint16_t* x, int64_t ldx, int per,
-                                                    bool vec) {
-    const int64_t first = (int64_t)blockIdx.x * (256 * kItems), row0 = first / per;
+// per: groups of 16 columns of a row; blocks: workgroups of a matrix
+__global__ void __launch_bounds__(256) k_fp8_unpack(ve_fp8_unpack_args a, int per, int blocks, bool vec) {
+    const uint32_t m = blockIdx.x / (uint32_t)blocks;
+    const int64_t first = (int64_t)(blockIdx.x - m * blocks) * (256 * kItems), row0 = first / per;
     const uint32_t rem = (uint32_t)(first - row0 * per);
-    const int shift = q.block_rows == 1 ? 0 : 7;
-    u32x2 w[kItems];
+    const int shift = a.in.block_rows == 1 ? 0 : 7, cols = (int)a.cols;
+    const uint8_t* codes = a.in.codes + m * a.in_codes_group;
+    const uint8_t* scales = a.in.scales + m * a.in_scales_group;
+    u32x4 w[kItems];
     uint32_t e[kItems];
     int64_t row[kItems];
     int col[kItems], cnt[kItems];
@@ -236,25 +239,29 @@ __global__ void __launch_bounds__(256) k_fp8_unpack(ve_fp8 q, int64_t rows, int 
     for (int k = 0; k < kItems; ++k) {
         const uint32_t i = rem + threadIdx.x + 256 * k, r = i / (uint32_t)per;
         row[k] = row0 + r;
-        col[k] = (int)(i - r * per) * 8;
-        cnt[k] = row[k] < rows ? min(cols - col[k], 8) : 0;
-        w[k] = u32x2{0, 0};
+        col[k] = (int)(i - r * per) * 16;
+        cnt[k] = row[k] < a.rows ? min(cols - col[k], 16) : 0;
+        w[k] = u32x4{0, 0, 0, 0};
         e[k] = 0;
         if (cnt[k] > 0) {
-            w[k] = *(const VE_GLOBAL u32x2*)(q.codes + row[k] * q.ld_codes + col[k]);
-            e[k] = q.scales[(int64_t)(col[k] >> 7) * q.ld_scales + (row[k] >> shift)];
+            w[k] = ldv<true>((const VE_GLOBAL u32x4*)(codes + row[k] * a.in.ld_codes + col[k]));
+            e[k] = ((const VE_GLOBAL uint8_t*)scales)[(int64_t)(col[k] >> 7) * a.in.ld_scales + (row[k] >> shift)];
         }
     }
 #pragma unroll
     for (int k = 0; k < kItems; ++k) {
         if (cnt[k] <= 0) continue;
-        float v[8];
-        fp8_decode4(w[k].x, q.format, v);
-        fp8_decode4(w[k].y, q.format, v + 4);
+        uint16_t* x = a.x + m * a.x_group + row[k] * a.ldx + col[k];
         const float s = fp8_scale(e[k]);
 #pragma unroll
-        for (int t = 0; t < 8; ++t) v[t] *= s;
-        store_bf16x8(x + row[k] * ldx + col[k], narrow8(v), cnt[k], vec);
+        for (int h = 0; h < 2; ++h) {
+            float v[8];
+            fp8_decode4(w[k][2 * h], a.in.format, v);
+            fp8_decode4(w[k][2 * h + 1], a.in.format, v + 4);
+#pragma unroll
+            for (int t = 0; t < 8; ++t) v[t] *= s;
+            store_bf16x8(x + 8 * h, narrow8(v), cnt[k] - 8 * h, vec);
+        }
     }
 }
 
@@ -272,11 +279,10 @@ hipError_t launch_fp8_pack(Fp8PackArgs a, hipStream_t s) {
     return hipGetLastError();
 }
 
-hipError_t launch_fp8_unpack(const ve_fp8& q, int64_t rows, int64_t cols, uint16_t* x, int64_t ldx, hipStream_t s) {
-    const int64_t per = (cols + 7) / 8, items = rows * per;
-    const bool vec = ((uintptr_t)x & 15) == 0 && ldx % 8 == 0;
-    hipLaunchKernelGGL(k_fp8_unpack, dim3((unsigned)((items + 256 * kItems - 1) / (256 * kItems))), dim3(256), 0, s, q, rows,
-                       (int)cols, x, ldx, (int)per, vec);
+hipError_t launch_fp8_unpack(const ve_fp8_unpack_args& a, hipStream_t s) {
+    const int64_t per = (a.cols + 15) / 16, blocks = (a.rows * per + 256 * kItems - 1) / (256 * kItems);
+    const bool vec = ((uintptr_t)a.x & 15) == 0 && a.ldx % 8 == 0 && (a.groups == 1 || a.x_group % 8 == 0);
+    hipLaunchKernelGGL(k_fp8_unpack, dim3((unsigned)(a.groups * blocks)), dim3(256), 0, s, a, (int)per, (int)blocks, vec);
     return hipGetLastError();
 }
 

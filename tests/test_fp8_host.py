@@ -67,17 +67,18 @@ def test_pack_weight_checks(kw, rc):
     assert ve.lib().ve_fp8_pack_weight(C.byref(a), None) == rc
 
 
-def test_unpack_checks():
-    f = ve.lib().ve_fp8_unpack
-    q = _q(2, 300, 100)
-    assert f(C.byref(q), 0, 100, None, 100, None) == OK
-    assert f(None, 300, 100, P, 100, None) == BAD
-    assert f(C.byref(q), 300, 100, None, 100, None) == BAD
-    assert f(C.byref(q), 300, 100, P, 99, None) == BAD
-    assert f(C.byref(q), -1, 100, P, 100, None) == BAD
-    assert f(C.byref(q), 300, 100, 2 * P + 16, 100, None) == BAD
-    for s in SPOILED:
-        assert f(C.byref(_q(2, 300, 100, **s)), 300, 100, P, 100, None) == BAD, s
+@pytest.mark.parametrize("kw,rc", [
+    (dict(rows=0, x=None), OK), (dict(x=None), BAD), (dict(ldx=99), BAD), (dict(rows=-1), BAD), (dict(groups=0), BAD),
+    (dict(x=2 * P + 16), BAD), (dict(groups=2, in_codes_group=300 * 112, in_scales_group=300, x_group=29999), BAD),
+    (dict(groups=2, in_codes_group=300 * 112 - 16, in_scales_group=300, x_group=30000), BAD),
+    (dict(groups=2, in_codes_group=300 * 112, in_scales_group=296, x_group=30000), BAD), (dict(rows=1 << 31), UNSUP),
+] + [(dict(in_=_q(2, 300, 100, **s)), BAD) for s in SPOILED])
+def test_unpack_checks(kw, rc):
+    a = ve._Fp8Unpack(rows=300, cols=100, groups=1, in_=_q(2, 300, 100), x=P, ldx=100)
+    for k, v in kw.items():
+        setattr(a, k, v)
+    assert ve.lib().ve_fp8_unpack(C.byref(a), None) == rc
+    assert ve.lib().ve_fp8_unpack(None, None) == BAD
 
 
 def _fwd(**kw):

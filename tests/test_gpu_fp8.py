@@ -236,6 +236,18 @@ def test_unpack(rows, cols, block, fmt, pad, shift):
     assert np.array_equal(got, ref, equal_nan=True)
 
 
+def test_unpack_of_groups():
+    import torch
+    ve = _ve()
+    rng = np.random.default_rng(5)
+    codes, e = rng.integers(0, 126, (3, 200, 130)).astype(np.uint8), rng.integers(100, 150, (3, 2, 2)).astype(np.uint8)
+    out = torch.full((3, 200, 136), 7.0, dtype=torch.bfloat16, device=DEV)
+    ve.fp8_unpack(device(codes, e, 128, pad=1), out[..., :130])
+    got = _host(out)
+    assert np.array_equal(got[..., :130], np.stack([fp8.unpack(c, x, 128) for c, x in zip(codes, e)]))
+    assert (got[..., 130:] == 7).all()
+
+
 # ---------------------------------------------------------------------------
 # products
 
