@@ -25,8 +25,9 @@
 namespace ve {
 namespace {
 
-constexpr int kSortThreads = 512, kSortWaves = kSortThreads / 64;
-constexpr uint32_t kSortChunk = 4096;   // slots of a workgroup, unless there are more than kSortBlocks of them
+constexpr int kSortThreads = 1024, kSortWaves = kSortThreads / 64;
+constexpr int kSortBatch = 4;            // slots a lane holds at once
+constexpr uint32_t kSortChunk = 2048;    // slots of a workgroup, unless there are more than kSortBlocks of them
 constexpr uint32_t kSortBlocks = 256;
 constexpr int kRowThreads = 256;        // of the row kernels: 8 columns each
 
@@ -40,14 +41,32 @@ __device__ __forceinline__ int expert_of(const SortArgs& a, uint32_t i) {
     return e >= 0 && e < a.experts_n ? e : -1;
 }
 
+// A wave's slots [begin, end) in batches: lane l of round r has slot at + 64 r
+// + l, and its expert or -1 (all loads of a batch in flight together).
+struct SlotBatch {
+    int e[kSortBatch];
+    __device__ __forceinline__ void load(const SortArgs& a, uint32_t at, uint32_t end, int lane) {
+#pragma unroll
+        for (int r = 0; r < kSortBatch; ++r) {
+            const uint32_t i = at + 64 * r + lane;
+            e[r] = i < end ? expert_of(a, i) : -1;
+        }
+    }
+};
+
+// Slots of each expert in a workgroup's chunk.
 __global__ void __launch_bounds__(kSortThreads) k_sort_count(SortArgs a) {
     extern __shared__ uint32_t hist[];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     for (int e = threadIdx.x; e < a.experts_n; e += kSortThreads) hist[e] = 0;
     __syncthreads();
-    const uint32_t first = blockIdx.x * a.chunk, last = min(first + a.chunk, a.n);
-    for (uint32_t i = first + threadIdx.x; i < last; i += kSortThreads) {
-        const int e = expert_of(a, i);
-        if (e >= 0) atomicAdd(&hist[e], 1u);
+    const uint32_t part = a.chunk / kSortWaves, begin = min(blockIdx.x * a.chunk + wave * part, a.n), end = min(begin + part, a.n);
+    for (uint32_t at = begin; at < end; at += 64 * kSortBatch) {
+        SlotBatch b;
+        b.load(a, at, end, lane);
+#pragma unroll
+        for (int r = 0; r < kSortBatch; ++r)
+            if (b.e[r] >= 0) atomicAdd(&hist[b.e[r]], 1u);
     }
     __syncthreads();
     for (int e = threadIdx.x; e < a.experts_n; e += kSortThreads)
@@ -63,14 +82,19 @@ __global__ void __launch_bounds__(kSortThreads) k_sort_place(SortArgs a, int wav
     uint32_t* base = lds + waves * E;
     uint32_t* slots = base + E;
     uint32_t* sums = slots + E;
+    const uint32_t part = a.chunk / waves;
+    const uint32_t begin = wave < waves ? min(blockIdx.x * a.chunk + wave * part, a.n) : a.n;
+    const uint32_t end = min(begin + part, a.n);
+    SlotBatch b;  // the first batch stays for the second pass
+    b.load(a, begin, end, lane);
     for (int i = threadIdx.x; i < waves * E; i += kSortThreads) hist[i] = 0;
     __syncthreads();
-    const uint32_t part = a.chunk / waves;
-    const uint32_t first = blockIdx.x * a.chunk + wave * part;
-    const uint32_t begin = wave < waves ? min(first, a.n) : a.n, end = wave < waves ? min(first + part, a.n) : a.n;
-    for (uint32_t i = begin + lane; i < end; i += 64) {
-        const int e = expert_of(a, i);
-        if (e >= 0) atomicAdd(&hist[wave * E + e], 1u);
+    for (uint32_t at = begin; at < end; at += 64 * kSortBatch) {
+        SlotBatch more = b;
+        if (at != begin) more.load(a, at, end, lane);
+#pragma unroll
+        for (int r = 0; r < kSortBatch; ++r)
+            if (more.e[r] >= 0) atomicAdd(&hist[wave * E + more.e[r]], 1u);
     }
     __syncthreads();
     // thread t scans experts [t per, (t + 1) per): their slots everywhere, and
@@ -81,10 +105,11 @@ __global__ void __launch_bounds__(kSortThreads) k_sort_place(SortArgs a, int wav
     for (int e = e0; e < e1; ++e) {
         uint32_t all = 0, before = 0;
         if (a.blocks > 1) {
-            for (uint32_t b = 0; b < a.blocks; ++b) {
-                const uint32_t c = a.counts[(int64_t)b * E + e];
-                all += c;
-                before += b < blockIdx.x ? c : 0;
+#pragma unroll 8
+            for (uint32_t c = 0; c < a.blocks; ++c) {
+                const uint32_t n = a.counts[(int64_t)c * E + e];
+                all += n;
+                before += c < blockIdx.x ? n : 0;
             }
         } else {
             for (int w = 0; w < waves; ++w) all += hist[w * E + e];
@@ -114,25 +139,30 @@ __global__ void __launch_bounds__(kSortThreads) k_sort_place(SortArgs a, int wav
     }
     if (blockIdx.x == 0 && threadIdx.x == 0) a.offsets[0] = 0;
     __syncthreads();
-    const int bits = 32 - __builtin_clz((unsigned)E);
-    for (uint32_t i0 = begin; i0 < end; i0 += 64) {
-        const uint32_t i = i0 + lane;
-        const int e = i < end ? expert_of(a, i) : -1;
-        uint64_t same = __ballot(e >= 0);
-        for (int b = 0; b < bits; ++b) {
-            const uint64_t set = __ballot((e >> b) & 1);
-            same &= (e >> b) & 1 ? set : ~set;
-        }
-        const uint64_t lower = same & ((1ull << lane) - 1);
-        uint32_t at = 0;
-        if (e >= 0) at = hist[wave * E + e];
-        __builtin_amdgcn_wave_barrier();
-        if (e >= 0 && lower == 0) hist[wave * E + e] = at + (uint32_t)__popcll(same);
-        __builtin_amdgcn_wave_barrier();
-        if (i < end) {
-            const int32_t p = e >= 0 ? (int32_t)(at + (uint32_t)__popcll(lower)) : -1;
-            a.position[i] = p;
-            if (e >= 0 && a.order) a.order[p] = (int32_t)i;
+    const int bits = E > 1 ? 32 - __builtin_clz((unsigned)E - 1) : 0;
+    for (uint32_t at = begin; at < end; at += 64 * kSortBatch) {
+        if (at != begin) b.load(a, at, end, lane);
+#pragma unroll
+        for (int r = 0; r < kSortBatch; ++r) {
+            const uint32_t i = at + 64 * r + lane;
+            const int e = b.e[r];
+            uint64_t same = __ballot(e >= 0);
+            if (at + 64 * r >= end) break;
+            for (int k = 0; k < bits; ++k) {
+                const uint64_t set = __ballot((e >> k) & 1);
+                same &= (e >> k) & 1 ? set : ~set;
+            }
+            const uint64_t lower = same & ((1ull << lane) - 1);
+            uint32_t to = 0;
+            if (e >= 0) to = hist[wave * E + e];
+            __builtin_amdgcn_wave_barrier();
+            if (e >= 0 && lower == 0) hist[wave * E + e] = to + (uint32_t)__popcll(same);
+            __builtin_amdgcn_wave_barrier();
+            if (i < end) {
+                const int32_t p = e >= 0 ? (int32_t)(to + (uint32_t)__popcll(lower)) : -1;
+                a.position[i] = p;
+                if (e >= 0 && a.order) a.order[p] = (int32_t)i;
+            }
         }
     }
 }
@@ -196,24 +226,58 @@ __global__ void __launch_bounds__(kRowThreads) k_gather8(ve_expert_gather_args a
     }
 }
 
+// A token's slots are taken 8 at a time, their rows' loads in flight together.
+constexpr int kSlotsAtOnce = 8;
+
+// Rows of slots [j0, j0 + 8) of a token: the place or -1, and the weight.
+struct SlotRows {
+    int64_t p[kSlotsAtOnce];
+    float w[kSlotsAtOnce];
+    __device__ __forceinline__ void load(const int32_t* pos, const float* weights, int j0, int slots, int64_t rows_len) {
+#pragma unroll
+        for (int j = 0; j < kSlotsAtOnce; ++j) {
+            const int at = min(j0 + j, slots - 1);
+            const int64_t q = pos[at];
+            p[j] = j0 + j < slots && q >= 0 && q < rows_len ? q : -1;
+            w[j] = weights ? weights[at] : 1.f;
+        }
+    }
+};
+
+// 8 columns of a row that is read once (4096 tokens of 7168, 8 slots: 106 us,
+// without the streaming hint 141).
+template <bool VEC>
+__device__ __forceinline__ u32x4 load_once(const uint16_t* p, int cnt) {
+    if (VEC && cnt >= 8) return ldv<true>((const VE_GLOBAL u32x4*)p);
+    return load_bf16x8(p, cnt, false);
+}
+
 template <bool VEC>
 __global__ void __launch_bounds__(kRowThreads) k_combine(ve_expert_combine_args a, int per) {
     const RowItem r = row_item((int)a.cols, per);
     if (r.cnt <= 0) return;
-    const int32_t* pos = a.position + r.t * a.slots;
+    u32x4 add = {0, 0, 0, 0};
+    if (a.residual) add = load_bf16x8(a.residual + r.t * a.ldr + r.col, r.cnt, VEC);
     float sum[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    for (int j = 0; j < a.slots; ++j) {
-        const int64_t p = pos[j];
-        if (p < 0 || p >= a.rows_len) continue;
-        float v[8];
-        widen8(load_bf16x8(a.rows + p * a.ld_rows + r.col, r.cnt, VEC), v);
-        const float w = a.weights ? a.weights[r.t * a.slots + j] : 1.f;
+    for (int j0 = 0; j0 < a.slots; j0 += kSlotsAtOnce) {
+        SlotRows s;
+        s.load(a.position + r.t * a.slots, a.weights ? a.weights + r.t * a.slots : nullptr, j0, a.slots, a.rows_len);
+        u32x4 h[kSlotsAtOnce];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) sum[i] = __builtin_fmaf(w, v[i], sum[i]);
+        for (int j = 0; j < kSlotsAtOnce; ++j)
+            if (s.p[j] >= 0) h[j] = load_once<VEC>(a.rows + s.p[j] * a.ld_rows + r.col, r.cnt);
+#pragma unroll
+        for (int j = 0; j < kSlotsAtOnce; ++j) {
+            if (s.p[j] < 0) continue;
+            float v[8];
+            widen8(h[j], v);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) sum[i] = __builtin_fmaf(s.w[j], v[i], sum[i]);
+        }
     }
     if (a.residual) {
         float v[8];
-        widen8(load_bf16x8(a.residual + r.t * a.ldr + r.col, r.cnt, VEC), v);
+        widen8(add, v);
 #pragma unroll
         for (int i = 0; i < 8; ++i) sum[i] += v[i];
     }
@@ -221,38 +285,42 @@ __global__ void __launch_bounds__(kRowThreads) k_combine(ve_expert_combine_args 
 }
 
 // A workgroup a token; dy is read again for every 8 slots (from the caches).
-constexpr int kSlotsAtOnce = 8;
 template <bool VEC>
 __global__ void __launch_bounds__(kRowThreads) k_combine_backward(ve_expert_combine_backward_args a) {
     __shared__ float sums[kRowThreads / 64][kSlotsAtOnce];
     const int64_t t = blockIdx.x;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, cols = (int)a.cols;
-    const int32_t* pos = a.position + t * a.slots;
     for (int j0 = 0; j0 < a.slots; j0 += kSlotsAtOnce) {
+        SlotRows s;
+        s.load(a.position + t * a.slots, a.weights && a.drows ? a.weights + t * a.slots : nullptr, j0, a.slots, a.rows_len);
         float dot[kSlotsAtOnce];
 #pragma unroll
         for (int j = 0; j < kSlotsAtOnce; ++j) dot[j] = 0.f;
         for (int col = (int)threadIdx.x * 8; col < cols; col += kRowThreads * 8) {
             const int cnt = min(cols - col, 8);
+            const u32x4 hg = load_bf16x8(a.dy + t * a.lddy + col, cnt, VEC);
+            u32x4 h[kSlotsAtOnce];
+            if (a.dweights) {
+#pragma unroll
+                for (int j = 0; j < kSlotsAtOnce; ++j)
+                    if (s.p[j] >= 0) h[j] = load_bf16x8(a.rows + s.p[j] * a.ld_rows + col, cnt, VEC);
+            }
             float g[8];
-            widen8(load_bf16x8(a.dy + t * a.lddy + col, cnt, VEC), g);
+            widen8(hg, g);
 #pragma unroll
             for (int j = 0; j < kSlotsAtOnce; ++j) {
-                if (j0 + j >= a.slots) break;
-                const int64_t p = pos[j0 + j];
-                if (p < 0 || p >= a.rows_len) continue;
+                if (s.p[j] < 0) continue;
+                if (a.drows) {
+                    float v[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) v[i] = s.w[j] * g[i];
+                    store_bf16x8(a.drows + s.p[j] * a.ld_drows + col, narrow8(v), cnt, VEC);
+                }
                 if (a.dweights) {
                     float v[8];
-                    widen8(load_bf16x8(a.rows + p * a.ld_rows + col, cnt, VEC), v);
+                    widen8(h[j], v);
 #pragma unroll
                     for (int i = 0; i < 8; ++i) dot[j] = __builtin_fmaf(g[i], v[i], dot[j]);
-                }
-                if (a.drows) {
-                    const float w = a.weights ? a.weights[t * a.slots + j0 + j] : 1.f;
-                    float s[8];
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) s[i] = w * g[i];
-                    store_bf16x8(a.drows + p * a.ld_drows + col, narrow8(s), cnt, VEC);
                 }
             }
         }
@@ -265,9 +333,9 @@ __global__ void __launch_bounds__(kRowThreads) k_combine_backward(ve_expert_comb
         }
         __syncthreads();
         if ((int)threadIdx.x < min(kSlotsAtOnce, a.slots - j0)) {
-            float s = 0.f;
-            for (int w = 0; w < kRowThreads / 64; ++w) s += sums[w][threadIdx.x];
-            a.dweights[t * a.slots + j0 + threadIdx.x] = s;
+            float v = 0.f;
+            for (int w = 0; w < kRowThreads / 64; ++w) v += sums[w][threadIdx.x];
+            a.dweights[t * a.slots + j0 + threadIdx.x] = v;
         }
         __syncthreads();
     }

@@ -897,13 +897,18 @@ hipError_t launch_exact(Fp8Args g, hipStream_t s) {
 // Microseconds of a product as `items` tiles (or slices) of `steps` steps, as
 // for the bf16 products.  Measured: a step of 256 x 256 takes 1.48 us and its
 // start and epilogue 5; of a pair of 128 x 128 tiles 1.06 and 4, of a single
-// one 0.8.
-double fp8_us(bool big, int64_t items, int64_t steps, int64_t bytes) {
+// one 0.8.  dw's starts and epilogues, which whole launches of short
+// contractions consist of, take 11 and 6.  Against measurements, 128^2 / 256^2
+// in us: 32 groups of 4096 rows 7168 -> 2048 146 / 204 (model 126 / 176), of
+// 16384 340 / 298; dw of 16 groups 4096 rows 2048 -> 4096 108 / 89, of 40
+// groups 2000 rows 1000 -> 1000 46 / 60.
+double fp8_us(LinKind kind, bool big, int64_t items, int64_t steps, int64_t bytes) {
     const double n = (double)((items + kCUs - 1) / kCUs), st = (double)steps;
     const double sums = bytes ? (double)bytes * 2 / 5e6 + 4 : 0;
-    if (big) return n * (1.48 * st + 5) + sums;
+    const double start = kind == kLinDw ? 6 : 4, start256 = kind == kLinDw ? 11 : 5;
+    if (big) return n * (1.48 * st + start256) + sums;
     const double pairs = (double)((int64_t)n / 2), one = n - 2 * pairs;
-    return pairs * (1.06 * st + 4) + one * (0.8 * st + 4) + sums;
+    return pairs * (1.06 * st + start) + one * (0.8 * st + start) + sums;
 }
 
 }  // namespace
@@ -925,11 +930,16 @@ LinPlan plan_fp8(const Fp8Args& g, LinKind kind) {
     double best = 0;
     for (int path : {(int)kPath128, (int)kPath256}) {
         if ((pin == kPath128 || pin == kPath256) && pin != path) continue;
-        const int64_t tiles = path == kPath256 ? tiles_of<Cfg256>(g, kind) : tiles_of<Cfg128>(g, kind);
+        int64_t tiles = path == kPath256 ? tiles_of<Cfg256>(g, kind) : tiles_of<Cfg128>(g, kind);
+        // (ragged rows: two thirds of a tile more a group, not the most any offsets could need)
+        if (kind == kLinFwd && g.offsets) {
+            const int64_t bm = path == kPath256 ? 256 : 128;
+            tiles = (g.T / bm + (2 * std::min<int64_t>(g.E, g.T) + 2) / 3) * ((g.N + bm - 1) / bm);
+        }
         const int64_t slots = kCUs * (path == kPath256 ? Cfg256::PER_CU : Cfg128::PER_CU), area = path == kPath256 ? 65536 : 16384;
         for (int64_t ks = 1; ks <= 32; ++ks) {
             if (ks > 1 && (!may_split || nk / ks < 4 || tiles * ks > slots)) break;
-            const double us = fp8_us(path == kPath256, tiles * ks, (nk + ks - 1) / ks, ks > 1 ? tiles * ks * area * 4 : 0);
+            const double us = fp8_us(kind, path == kPath256, tiles * ks, (nk + ks - 1) / ks, ks > 1 ? tiles * ks * area * 4 : 0);
             if (best == 0 || us < best) {
                 best = us;
                 p.us = us;

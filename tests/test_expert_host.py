@@ -33,8 +33,8 @@ def test_sort_sizes(tokens, slots, experts, rc):
 
 
 def test_sort_workspace_is_small():
-    assert _need(0, 8, 256) == (OK, 0) and _need(512, 8, 256) == (OK, 0)
-    assert _need(513, 8, 256) == (OK, 2 * 256 * 4)
+    assert _need(0, 8, 256) == (OK, 0)
+    assert _need(256, 8, 256) == (OK, 0) and _need(257, 8, 256) == (OK, 2 * 256 * 4)
     assert ve.expert_sort_workspace(1 << 20, 8, 256) == 256 * 256 * 4
     assert ve.lib().ve_expert_sort_workspace(8, 2, 4, None) == BAD
 
