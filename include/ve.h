@@ -235,7 +235,9 @@ ve_status ve_dbuffer_group_op(const ve_plan* plan, int32_t rank, int32_t op, flo
  *       products where it applies: 1 = register staged (any alignment), 2 /
  *       3 = direct-to-LDS tiles of 128 x 128 / 256 x 256 (rows that are not
  *       whole 16 bytes are laid out anew in the workspace), 4 = the forward
- *       form for few tokens; 0 = chosen by shape;
+ *       form for few tokens; 0 = chosen by shape (2, 3 and 4 pin those of
+ *       the products on matrices in 8-bit floating point too, except where
+ *       dw is fp32);
  *   "linear_split" (VE_LINEAR_SPLIT, 1): 0 = never cut their contraction
  *       into slices (the options must not change between a workspace query
  *       and the call it is for).

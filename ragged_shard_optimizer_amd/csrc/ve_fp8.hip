@@ -380,6 +380,62 @@ __device__ __forceinline__ void dw_epilogue(const Work& w, f32x16 (&acc)[CF::TM]
     }
 }
 
+// The same in fp32: exchanging q, q + 1 between the rows of 16 lanes, then both
+// pairs of q between lanes i and i + 8, a store covers 8 rows of the block's
+// 128 bytes.
+template <class CF, bool ADD>
+__device__ __forceinline__ void dw_epilogue_fp32(const Work& w, f32x16 (&acc)[CF::TM][CF::TN], int wr, int wc, int lane) {
+    constexpr int TM = CF::TM, TN = CF::TN;
+    const LinArgs g = args_again();
+    const int ld = (int)g.lddw, col0 = w.col0 + wc * CF::WN, r = lane & 7;
+    const bool low = (lane & 8) == 0;
+    const int sc = 4 * (lane >> 5) + 8 * ((lane >> 4) & 1) + 16 * ((lane >> 3) & 1);  // the lane's columns of a block
+    VE_GLOBAL char* out =
+        (VE_GLOBAL char*)((float*)g.dw + w.e * g.dw_group + (int64_t)(w.row0 + wr * CF::WM) * g.lddw + col0);
+    const int left = w.rows - wr * CF::WM - r;  // rows from the lane's first on
+#pragma unroll 1
+    for (int b = 0; b < TN; ++b) {
+        const bool in = col0 + 32 * b + sc < (int)g.N;
+        f32x4 held[ADD ? TM : 1][4];
+        if constexpr (ADD) {
+#pragma unroll
+            for (int a = 0; a < TM; ++a)
+#pragma unroll
+                for (int t = 0; t < 4; ++t) {
+                    held[a][t] = f32x4{0.f, 0.f, 0.f, 0.f};
+                    if (in && left > 32 * a + 8 * t)
+                        held[a][t] = *(const VE_GLOBAL f32x4*)(out + (uint32_t)((32 * a + 8 * t + r) * ld + 32 * b + sc) * 4);
+                }
+        }
+#pragma unroll
+        for (int a = 0; a < TM; ++a) {
+            uint32_t p[4][4];  // [q][column]; then the stores' rows 16 (q % 2) + 8 (q / 2)
+#pragma unroll
+            for (int e = 0; e < TN; ++e)
+                if (b == e) {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) p[i >> 2][i & 3] = __float_as_uint(acc[a][e][i]);
+                }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                swap_rows(p[0][i], p[1][i]);
+                swap_rows(p[2][i], p[3][i]);
+                swap_eights(p[0][i], p[2][i], low);
+                swap_eights(p[1][i], p[3][i], low);
+            }
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const int t = 2 * (q & 1) + (q >> 1);
+                if (in && left > 32 * a + 8 * t) {
+                    f32x4 v = {__uint_as_float(p[q][0]), __uint_as_float(p[q][1]), __uint_as_float(p[q][2]), __uint_as_float(p[q][3])};
+                    if constexpr (ADD) v += held[a][t];
+                    stv<true>((VE_GLOBAL f32x4*)(out + (uint32_t)((32 * a + 8 * t + r) * ld + 32 * b + sc) * 4), v);
+                }
+            }
+        }
+    }
+}
+
 template <class CF, int KIND>
 __device__ __forceinline__ void fp8_epilogue(int finish, const Work& w, f32x16 (&acc)[CF::TM][CF::TN], unsigned char* sw,
                                              int wr, int wc, int lane) {
@@ -750,7 +806,9 @@ __global__ void __launch_bounds__(CF::THREADS, CF::PER_CU) k_fp8_exact(Fp8Args g
         }
         __syncthreads();
     }
-    epilogue<CF, KIND>(g.finish, w, acc, smem + CF::STAGES_BYTES + wave * CF::OUT_BYTES, wr, wc, lane);
+    if (g.finish == kFinishWide) dw_epilogue_fp32<CF, false>(w, acc, wr, wc, lane);
+    else if (g.finish == kFinishWideAdd) dw_epilogue_fp32<CF, true>(w, acc, wr, wc, lane);
+    else epilogue_of<CF, KIND, kFinishAll>(w, acc, smem + CF::STAGES_BYTES + wave * CF::OUT_BYTES, wr, wc, lane);
 }
 
 // Few rows a group (forward and dx): bound by reading the weights.  A
@@ -881,16 +939,18 @@ hipError_t launch_kind(Fp8Args g, const LinPlan& p, hipStream_t s) {
     return hipGetLastError();
 }
 
-hipError_t launch_exact(Fp8Args g, hipStream_t s) {
+hipError_t launch_exact(Fp8Args g, const LinPlan& p, hipStream_t s) {
     typedef Cfg128 CF;
     g.tiles_n = (int)((g.N + CF::BN - 1) / CF::BN);
-    g.ksplit = 1;
+    g.ksplit = p.ksplit;
     g.tiles = tiles_of<CF>(g, kLinDw);
     if (g.tiles == 0) return hipSuccess;
     g.finish = finish_of(g, kLinDw);
     const dim3 grid((unsigned)items_of(g, kLinDw)), block(CF::THREADS);
     if (g.format == VE_E4M3) hipLaunchKernelGGL((k_fp8_exact<CF, VE_E4M3>), grid, block, 0, s, g);
     else hipLaunchKernelGGL((k_fp8_exact<CF, VE_E5M2>), grid, block, 0, s, g);
+    if (p.ksplit > 1)
+        hipLaunchKernelGGL((k_join<CF, kLinDw>), dim3((unsigned)(g.tiles * (CF::BM * (CF::BN / 8) / 256))), dim3(256), 0, s, g);
     return hipGetLastError();
 }
 
@@ -902,20 +962,22 @@ hipError_t launch_exact(Fp8Args g, hipStream_t s) {
 // in us: 32 groups of 4096 rows 7168 -> 2048 146 / 204 (model 126 / 176), of
 // 16384 340 / 298; dw of 16 groups 4096 rows 2048 -> 4096 108 / 89, of 40
 // groups 2000 rows 1000 -> 1000 46 / 60.
-double fp8_us(LinKind kind, bool big, int64_t items, int64_t steps, int64_t bytes) {
+// The exact form's steps take 1.8 and 1.2.
+double fp8_us(LinKind kind, bool exact, bool big, int64_t items, int64_t steps, int64_t bytes) {
     const double n = (double)((items + kCUs - 1) / kCUs), st = (double)steps;
+    const double pair = exact ? 1.8 : 1.06, single = exact ? 1.2 : 0.8;
     const double sums = bytes ? (double)bytes * 2 / 5e6 + 4 : 0;
     const double start = kind == kLinDw ? 6 : 4, start256 = kind == kLinDw ? 11 : 5;
     if (big) return n * (1.48 * st + start256) + sums;
     const double pairs = (double)((int64_t)n / 2), one = n - 2 * pairs;
-    return pairs * (1.06 * st + start) + one * (0.8 * st + start) + sums;
+    return pairs * (pair * st + start) + one * (single * st + start) + sums;
 }
 
 }  // namespace
 
 LinPlan plan_fp8(const Fp8Args& g, LinKind kind) {
     LinPlan p{kPath128, 1, 0, 0};
-    if (kind == kLinDw && g.wide) return p;
+    const bool exact = kind == kLinDw && g.wide;
     const int64_t pin = option(kOptLinearPath);
     // Few rows against the tiles, us a call: dense 8192 -> 8192 of 1 / 16 / 32
     // / 64 rows 14 / 19 / 26 / 47 against 33 / 34 / 34 / 30; 64 groups 7168 ->
@@ -929,7 +991,7 @@ LinPlan plan_fp8(const Fp8Args& g, LinKind kind) {
     const bool may_split = !g.offsets && option(kOptLinearSplit) != 0;
     double best = 0;
     for (int path : {(int)kPath128, (int)kPath256}) {
-        if ((pin == kPath128 || pin == kPath256) && pin != path) continue;
+        if (exact ? path != kPath128 : (pin == kPath128 || pin == kPath256) && pin != path) continue;
         int64_t tiles = path == kPath256 ? tiles_of<Cfg256>(g, kind) : tiles_of<Cfg128>(g, kind);
         // (ragged rows: two thirds of a tile more a group, not the most any offsets could need)
         if (kind == kLinFwd && g.offsets) {
@@ -939,7 +1001,7 @@ LinPlan plan_fp8(const Fp8Args& g, LinKind kind) {
         const int64_t slots = kCUs * (path == kPath256 ? Cfg256::PER_CU : Cfg128::PER_CU), area = path == kPath256 ? 65536 : 16384;
         for (int64_t ks = 1; ks <= 32; ++ks) {
             if (ks > 1 && (!may_split || nk / ks < 4 || tiles * ks > slots)) break;
-            const double us = fp8_us(kind, path == kPath256, tiles * ks, (nk + ks - 1) / ks, ks > 1 ? tiles * ks * area * 4 : 0);
+            const double us = fp8_us(kind, exact, path == kPath256, tiles * ks, (nk + ks - 1) / ks, ks > 1 ? tiles * ks * area * 4 : 0);
             if (best == 0 || us < best) {
                 best = us;
                 p.us = us;
@@ -953,7 +1015,7 @@ LinPlan plan_fp8(const Fp8Args& g, LinKind kind) {
 }
 
 hipError_t launch_fp8(Fp8Args g, LinKind kind, const LinPlan& p, hipStream_t s) {
-    if (kind == kLinDw && g.wide) return launch_exact(g, s);
+    if (kind == kLinDw && g.wide) return launch_exact(g, p, s);
     if (p.path == kPathFew) return g.offsets || g.T <= 16 ? launch_few<1, 8>(g, s) : launch_few<2, 4>(g, s);
     if (p.path == kPath256)
         return kind == kLinDw ? launch_kind<Cfg256, kLinDw>(g, p, s) : launch_kind<Cfg256, kLinFwd>(g, p, s);

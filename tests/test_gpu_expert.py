@@ -277,3 +277,136 @@ def test_infinities_and_nan_pass_through():
     ve.expert_combine(rows, pos, y, weights=torch.tensor([[2.0, 1.0], [1.0, float("nan")]], device=DEV))
     y = y.float().cpu()
     assert y[0, 0] == float("inf") and torch.isnan(y[0, 1]) and y[0, 3] == 3 and y[1, 2] == float("-inf") and y[1, 0] == 1
+
+
+def _calls(seed=0, T=700, k=4, E=20, C=264):
+    import torch
+    ve = _ve()
+    ids = torch.from_numpy(_ids(T, k, E, seed)).to(DEV)
+    x = _dev(_bits((T, C), seed))
+    g = torch.Generator(device=DEV)
+    g.manual_seed(seed)
+    w = torch.rand(T, k, generator=g, device=DEV)
+    off, pos = torch.zeros(E + 1, dtype=torch.int64, device=DEV), torch.zeros(T, k, dtype=torch.int32, device=DEV)
+    order = torch.zeros(T * k, dtype=torch.int32, device=DEV)
+    rows, y = torch.zeros(T * k, C, dtype=torch.bfloat16, device=DEV), torch.zeros(T, C, dtype=torch.bfloat16, device=DEV)
+    drows, dw, q = torch.zeros_like(rows), torch.zeros(T, k, device=DEV), ve.new_fp8(T * k, C, device=DEV)
+
+    def call(**kw):
+        ve.expert_sort(ids, off, pos, order=order, **kw)
+        ve.expert_gather(x, pos, rows, **kw)
+        ve.expert_gather(x, pos, q, **kw)
+        ve.expert_combine(rows, pos, y, weights=w, residual=x, **kw)
+        ve.expert_combine_backward(y, pos, rows=rows, weights=w, drows=drows, dweights=dw, **kw)
+
+    return call, [off, pos, order, rows, y, drows, dw, q.codes.view(torch.uint8), q.scales]
+
+
+def test_streams_and_captured_graphs():
+    import torch
+    call, outs = _calls()
+    call()
+    torch.cuda.synchronize()
+    want = [t.clone() for t in outs]
+    s = torch.cuda.Stream(DEV)
+    for stream in (None, s, s.cuda_stream):
+        for t in outs:
+            t.fill_(0)
+        s.wait_stream(torch.cuda.current_stream())
+        call(stream=stream)
+        torch.cuda.current_stream().wait_stream(s)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(outs, want))
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        call()
+    for _ in range(3):
+        for t in outs:
+            t.fill_(0)
+        g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(outs, want))
+        call()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(outs, want))
+
+
+def test_two_streams_at_once():
+    import torch
+    pairs = [_calls(seed=2) for _ in range(2)]
+    pairs[0][0]()
+    torch.cuda.synchronize()
+    want = [t.clone() for t in pairs[0][1]]
+    streams = [torch.cuda.Stream(DEV) for _ in range(2)]
+    for _ in range(5):
+        for (call, _), s in zip(pairs, streams):
+            call(stream=s)
+    torch.cuda.synchronize()
+    for _, outs in pairs:
+        assert all(torch.equal(a, b) for a, b in zip(outs, want))
+
+
+def test_sort_takes_its_workspace():
+    import torch
+    ve = _ve()
+    T, k, E = 3000, 4, 64
+    ids = torch.from_numpy(_ids(T, k, E, 1)).to(DEV)
+    off, pos = torch.zeros(E + 1, dtype=torch.int64, device=DEV), torch.zeros(T, k, dtype=torch.int32, device=DEV)
+    need = ve.expert_sort_workspace(T, k, E)
+    assert need > 0
+    with pytest.raises(ve.VeError, match="workspace"):
+        ve.expert_sort(ids, off, pos, workspace=torch.empty(need - 4, dtype=torch.uint8, device=DEV))
+    ve.expert_sort(ids, off, pos, workspace=torch.full((need,), 255, dtype=torch.uint8, device=DEV))
+    ref = expert.sort(ids.cpu().numpy(), E)
+    assert np.array_equal(off.cpu().numpy(), ref[0]) and np.array_equal(pos.cpu().numpy(), ref[1])
+
+
+def test_many_slots():
+    """A million slots: chunks of more than one batch a lane."""
+    import torch
+    ve = _ve()
+    T, k, E = 150000, 8, 256
+    g = torch.Generator(device=DEV)
+    g.manual_seed(0)
+    ids = torch.randint(-1, E, (T, k), generator=g, device=DEV, dtype=torch.int32)
+    off, pos = torch.zeros(E + 1, dtype=torch.int64, device=DEV), torch.zeros(T, k, dtype=torch.int32, device=DEV)
+    order = torch.full((T * k,), 77, dtype=torch.int32, device=DEV)
+    ve.expert_sort(ids, off, pos, order=order)
+    flat = ids.cpu().numpy().reshape(-1)
+    n = int((flat >= 0).sum())
+    key = np.where(flat >= 0, flat, E)
+    want = np.argsort(key, kind="stable")[:n]
+    assert np.array_equal(order[:n].cpu().numpy(), want) and bool((order[n:] == 77).all())
+    place = np.full(T * k, -1)
+    place[want] = np.arange(n)
+    assert np.array_equal(pos.cpu().numpy().reshape(-1), place)
+    assert np.array_equal(off.cpu().numpy(), np.concatenate([[0], np.cumsum(np.bincount(key, minlength=E + 1)[:E])]))
+
+
+def test_rows_beyond_32_bits():
+    """Rows past 4 GiB (and 2^31 elements): the last ones."""
+    import torch
+    ve = _ve()
+    T, k, C = 40000, 8, 7168
+    R = T * k                                              # 4.6 GB of rows
+    pos = torch.arange(R, dtype=torch.int32, device=DEV).flip(0).view(T, k).contiguous()
+    x = torch.arange(T, device=DEV).remainder(128).to(torch.bfloat16)[:, None].expand(T, C).contiguous()
+    rows = torch.zeros(R, C, dtype=torch.bfloat16, device=DEV)
+    ve.expert_gather(x, pos, rows)
+    want = torch.arange(T, device=DEV).remainder(128).flip(0).repeat_interleave(k).to(torch.bfloat16)
+    assert torch.equal(rows[:, 0], want) and torch.equal(rows[:, -1], want)
+    y = torch.empty_like(x)
+    ve.expert_combine(rows, pos, y)
+    assert torch.equal(y, (x.float() * k).to(torch.bfloat16))
+    dw = torch.empty(T, k, device=DEV)
+    ve.expert_combine_backward(torch.ones_like(x), pos, rows=rows, dweights=dw)
+    assert torch.equal(dw, x[:, :1].float() * C * torch.ones(1, k, device=DEV))
+    rows.zero_()
+    ve.expert_combine_backward(x, pos, drows=rows)
+    assert torch.equal(rows[:, 5], want)
+    del rows
+    q = ve.new_fp8(R, C, device=DEV)
+    ve.expert_gather(x, pos, q)
+    back = torch.empty(1000, C, dtype=torch.bfloat16, device=DEV)
+    ve.fp8_unpack(ve.Fp8(q.codes[-1000:], q.scales[:, -1000:]), back)
+    assert bool((back - want[-1000:, None]).abs().max() <= 8)  # half a step of a value below 128: 2^-4 of it

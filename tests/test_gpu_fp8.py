@@ -313,6 +313,19 @@ def test_forward(case):
     _forward(case)
 
 
+@pytest.mark.parametrize("path,split", [(2, 0), (2, 1), (3, 0), (3, 1), (4, 1)])
+@pytest.mark.parametrize("case", [
+    (70, 4096, 264, None, "silu", True, None, True, "e4m3", 0),
+    (300, 2056, 520, None, "none", True, "in place", False, "e5m2", 8),
+    (129, 1000, 257, None, "gelu", False, "apart", False, "e4m3", 1),
+    (700, 384, 136, 9, "relu", True, None, True, "e4m3", 0),
+    (900, 640, 264, 70, "none", True, "apart", False, "e4m3", 0),
+], ids=lambda c: "-".join(map(str, c)))
+def test_forward_forms(case, path, split):
+    with _ve().options(linear_path=path, linear_split=split):
+        _forward(case, seed=1)
+
+
 def _backward(case, seed=0, accumulate=False, dx=True, dw=True):
     import torch
     ve = _ve()
@@ -395,6 +408,21 @@ BACKWARD = [  # tokens, in, out, groups, dx_add, fp32 dw, format of dy, pad
 @pytest.mark.parametrize("accumulate", [False, True])
 def test_backward(case, accumulate):
     _backward(case, accumulate=accumulate)
+
+
+@pytest.mark.parametrize("path,split", [(2, 0), (2, 1), (3, 0), (3, 1)])
+@pytest.mark.parametrize("case", [
+    (4000, 136, 264, None, "apart", False, "e4m3", 0),
+    (3000, 72, 136, None, None, True, "e5m2", 8),
+    (2500, 129, 65, None, "in place", False, "e4m3", 1),
+    (700, 264, 392, 9, None, False, "e5m2", 0),
+    (900, 136, 264, 70, "apart", False, "e4m3", 0),
+    (800, 136, 264, 70, None, True, "e4m3", 0),
+], ids=lambda c: "-".join(map(str, c)))
+@pytest.mark.parametrize("accumulate", [False, True])
+def test_backward_forms(case, path, split, accumulate):
+    with _ve().options(linear_path=path, linear_split=split):
+        _backward(case, seed=1, accumulate=accumulate)
 
 
 def test_backward_outputs_are_optional():
@@ -519,3 +547,182 @@ def test_bad_offsets_stay_inside_the_buffers():
         ve.fp8_linear_backward(dy=dq, w_t=device(wtc, wte, 128), dx=dx[1:-1], dy_t=dt, x_t=xt, dw=dw[1:-1], offsets=off)
         torch.cuda.synchronize()
         assert all(bool((t[0] == 7).all()) and bool((t[-1] == 7).all()) for t in (y, dx, dw))
+
+
+# ---------------------------------------------------------------------------
+# how calls may be made
+
+def _layer(T=700, K=264, N=392, E=5, seed=0):
+    """A grouped layer's calls from bf16 on, and their outputs."""
+    import torch
+    ve = _ve()
+    rng = np.random.default_rng(seed)
+    off = _off(group_offsets(T, E, seed, first=1, spare=2))
+    x, dy, z = (_dev(_bits((T, n), seed + i)) for i, n in enumerate((K, N, N)))
+    w = _dev(_bits((E, N, K), seed + 9))
+    q = dict(x8=ve.new_fp8(T, K, device=DEV), dy8=ve.new_fp8(T, N, device=DEV), w8=ve.new_fp8(N, K, 128, groups=E, device=DEV),
+             w8t=ve.new_fp8(K, N, 128, groups=E, device=DEV), xt=ve.new_fp8(K, fp8.columns(T, E), device=DEV),
+             dyt=ve.new_fp8(N, fp8.columns(T, E), device=DEV))
+    y, dx = torch.zeros(T, N, dtype=torch.bfloat16, device=DEV), torch.zeros(T, K, dtype=torch.bfloat16, device=DEV)
+    dw, dw32 = torch.zeros(E, N, K, dtype=torch.bfloat16, device=DEV), torch.zeros(E, N, K, device=DEV)
+    back = torch.zeros(T, K, dtype=torch.bfloat16, device=DEV)
+
+    def call(**kw):
+        ve.fp8_pack(x, q["x8"], q["xt"], offsets=off, **kw)
+        ve.fp8_pack(dy, q["dy8"], q["dyt"], z=z, activation="silu", offsets=off, **kw)
+        ve.fp8_pack_weight(w, q["w8"], q["w8t"], **kw)
+        ve.fp8_unpack(q["x8"], back, **kw)
+        ve.fp8_linear_forward(q["x8"], q["w8"], y, activation="gelu", offsets=off, **kw)
+        for d in (dw, dw32):
+            ve.fp8_linear_backward(dy=q["dy8"], w_t=q["w8t"], dx=dx, dy_t=q["dyt"], x_t=q["xt"], dw=d, offsets=off, **kw)
+
+    outs = [y, dx, dw, dw32, back] + [t for v in q.values() for t in (v.codes.view(torch.uint8), v.scales)]
+    return call, outs
+
+
+def test_same_bits_every_call_and_on_other_streams():
+    import torch
+    call, outs = _layer()
+    call()
+    torch.cuda.synchronize()
+    want = [t.clone() for t in outs]
+    s = torch.cuda.Stream(DEV)
+    for stream in (None, s, s.cuda_stream):
+        for t in outs:
+            t.fill_(0)
+        s.wait_stream(torch.cuda.current_stream())
+        call(stream=stream)
+        torch.cuda.current_stream().wait_stream(s)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(outs, want))
+
+
+def test_two_streams_at_once():
+    import torch
+    pairs = [_layer(seed=3) for _ in range(2)]
+    pairs[0][0]()
+    torch.cuda.synchronize()
+    want = [t.clone() for t in pairs[0][1]]
+    streams = [torch.cuda.Stream(DEV) for _ in range(2)]
+    for t in pairs[0][1]:
+        t.fill_(0)
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for (call, _), s in zip(pairs, streams):
+            call(stream=s)
+    torch.cuda.synchronize()
+    for _, outs in pairs:
+        assert all(torch.equal(a, b) for a, b in zip(outs, want))
+
+
+def test_captured_graph_replays():
+    import torch
+    call, outs = _layer(seed=5)
+    call()
+    torch.cuda.synchronize()
+    want = [t.clone() for t in outs]
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        call()
+    for _ in range(3):
+        for t in outs:
+            t.fill_(0)
+        g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(outs, want))
+        call()                                             # eager work between the replays
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(outs, want))
+
+
+def test_split_products_need_and_take_their_workspace():
+    import torch
+    ve = _ve()
+    rng = np.random.default_rng(0)
+    T, K, N = 200, 8192, 264
+    xc, xe, x = packed_values(rng.standard_normal((T, K)), 1, "e4m3")
+    wc, we, w = packed_values(rng.standard_normal((N, K)), 128, "e4m3")
+    xq, wq = device(xc, xe), device(wc, we, 128)
+    y = torch.full((T, N), 5.0, dtype=torch.bfloat16, device=DEV)
+    need = ve.fp8_linear_forward_workspace(xq, wq, y)
+    assert need > 0
+    for ws in (torch.empty(need - 256, dtype=torch.uint8, device=DEV), torch.empty(need + 256, dtype=torch.uint8, device=DEV)[16:]):
+        with pytest.raises(ve.VeError, match="workspace"):
+            ve.fp8_linear_forward(xq, wq, y, workspace=ws)
+    torch.cuda.synchronize()
+    assert bool((y == 5).all())
+    ve.fp8_linear_forward(xq, wq, y, workspace=torch.empty(need, dtype=torch.uint8, device=DEV))
+    ref, z, mag = linear.forward(x, w)
+    _within(_host(y), ref, forward_bounds(ref, z, mag, cut(x, w), K, "none")[1], "y")
+    dw = torch.empty(40, 72, device=DEV)
+    assert ve.fp8_linear_backward_workspace(dy_t=ve.new_fp8(40, 8192, device=DEV), x_t=ve.new_fp8(72, 8192, device=DEV), dw=dw,
+                                            tokens=8192) > 0
+
+
+def test_offsets_beyond_32_bits():
+    """Codes, outputs and weights past 4 GiB: the last group's rows."""
+    import torch
+    ve = _ve()
+    rng = np.random.default_rng(0)
+    K, N, E = 8192, 8192, 66                               # 4.4 GB of weights
+    w8 = ve.new_fp8(N, K, 128, groups=E, device=DEV)
+    wc, we, w = packed_values(rng.standard_normal((N, 128)), 128, "e4m3")
+    w8.codes[E - 1].view(torch.uint8)[:, -128:] = torch.from_numpy(wc).to(DEV)
+    w8.scales[E - 1][-1, :] = torch.from_numpy(we[0]).to(DEV)
+    for T in (20, 700):                                    # few rows, and tiles
+        off = torch.zeros(E + 1, dtype=torch.int64, device=DEV)
+        off[E] = T
+        xc, xe, x = packed_values(rng.standard_normal((T, K)), 1, "e4m3")
+        y = torch.empty(T, N, dtype=torch.bfloat16, device=DEV)
+        ve.fp8_linear_forward(device(xc, xe), w8, y, offsets=off)
+        ref, z, mag = linear.forward(x[:, -128:], w)
+        _within(_host(y), ref, forward_bounds(ref, z, mag, cut(x[:, -128:], w), 128, "none")[1], T)
+    back = torch.empty(E, 512, K, dtype=torch.bfloat16, device=DEV)
+    ve.fp8_unpack(ve.Fp8(w8.codes[:, -512:], w8.scales[..., -4:], 128), back)
+    assert np.array_equal(_host(back[-1, :, -128:]), w[-512:])
+    del back
+    # dw of the last group, 4.4 G elements of 2 bytes from the first one's
+    dw = torch.zeros(E, N, K, dtype=torch.bfloat16, device=DEV)
+    off = torch.zeros(E + 1, dtype=torch.int64, device=DEV)
+    off[E] = 40
+    dy, xx = rng.standard_normal((40, N)), rng.standard_normal((40, K))
+    dyc, dye, dyv = packed_values(fp8.transposed(dy, off.cpu().numpy())[0], 1, "e4m3")
+    xtc, xte, xv = packed_values(fp8.transposed(xx, off.cpu().numpy())[0], 1, "e4m3")
+    ve.fp8_linear_backward(dy_t=device(dyc, dye), x_t=device(xtc, xte), dw=dw, offsets=off, tokens=40)
+    ref, mag = dyv[:64, :128] @ xv[:, :128].T, np.abs(dyv[:64, :128]) @ np.abs(xv[:, :128]).T
+    _within(_host(dw[-1, :64]), ref, rounded(gamma(170) * mag + cut(dyv[:64], xv) + TINY, ref), "dw")
+    assert bool((dw[:-1:13] == 0).all())
+    del dw, w8
+    # rows of 4.8 GB
+    T, K, N = 600000, 8192, 72
+    x8, y = ve.new_fp8(T, K, device=DEV), torch.empty(T, N, dtype=torch.bfloat16, device=DEV)
+    xb, wb = _bits((300, K), 1), _bits((N, K), 2)
+    big = torch.zeros(T, K, dtype=torch.bfloat16, device=DEV)
+    big[-300:] = _dev(xb)
+    ve.fp8_pack(big, x8)
+    del big
+    w8 = ve.new_fp8(N, K, 128, device=DEV)
+    ve.fp8_pack_weight(_dev(wb), w8)
+    ve.fp8_linear_forward(x8, w8, y)
+    xv, wv = packed_values(_up(xb), 1, "e4m3")[2], packed_values(_up(wb), 128, "e4m3")[2]
+    ref, z, mag = linear.forward(xv, wv)
+    _within(_host(y[-300:]), ref, forward_bounds(ref, z, mag, cut(xv, wv), K, "none")[1], "rows")
+    assert bool((y[:-300:997] == 0).all())
+
+
+def test_binding_refuses_rows_without_room():
+    """The last row's memory has to go on to whole 16 bytes (scales: 4)."""
+    import torch
+    ve = _ve()
+    c = torch.zeros(4 * 112, dtype=torch.uint8, device=DEV)[:3 * 112 + 100].view(torch.float8_e4m3fn)
+    short = torch.empty(3 * 112 + 100, dtype=torch.uint8, device=DEV)
+    good = ve.new_fp8(4, 100, device=DEV)
+    out = torch.empty(4, 100, dtype=torch.bfloat16, device=DEV)
+    ve.fp8_unpack(good, out)
+    short = torch.as_strided(short.view(torch.float8_e4m3fn), (4, 100), (112, 1))
+    with pytest.raises(ValueError, match="memory"):
+        ve.fp8_unpack(ve.Fp8(short, good.scales), out)
+    with pytest.raises(ve.VeError, match="16 bytes"):
+        ve.fp8_unpack(ve.Fp8(torch.zeros(4, 100, dtype=torch.uint8, device=DEV).view(torch.float8_e4m3fn)[:, :96],
+                             ve.new_fp8(4, 96, device=DEV).scales), out[:, :96])
+    del c
