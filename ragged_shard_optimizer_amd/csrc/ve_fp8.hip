@@ -739,10 +739,10 @@ __global__ void __launch_bounds__(CF::THREADS, CF::PER_CU) k_fp8(Fp8Args g) {
 // dw in fp32: one item a workgroup, codes turned to bf16 between LDS and the
 // MFMAs.
 template <class CF, int FORMAT>
-__global__ void __launch_bounds__(CF::THREADS, CF::PER_CU) k_fp8_exact(Fp8Args g) {
+__global__ void __launch_bounds__(CF::THREADS, 3) k_fp8_exact(Fp8Args g) {
     constexpr int KIND = kLinDw;
     constexpr int TM = CF::TM, TN = CF::TN, WM = CF::WM, WN = CF::WN;
-    __shared__ __attribute__((aligned(1024))) unsigned char smem[CF::SMEM];
+    __shared__ __attribute__((aligned(1024))) unsigned char smem[CF::STAGE_ELEMS * 2 + CF::WAVES * CF::OUT_BYTES];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
     const int wr = wave / CF::WAVES_N, wc = wave % CF::WAVES_N;
     Work w;
@@ -808,7 +808,7 @@ __global__ void __launch_bounds__(CF::THREADS, CF::PER_CU) k_fp8_exact(Fp8Args g
     }
     if (g.finish == kFinishWide) dw_epilogue_fp32<CF, false>(w, acc, wr, wc, lane);
     else if (g.finish == kFinishWideAdd) dw_epilogue_fp32<CF, true>(w, acc, wr, wc, lane);
-    else epilogue_of<CF, KIND, kFinishAll>(w, acc, smem + CF::STAGES_BYTES + wave * CF::OUT_BYTES, wr, wc, lane);
+    else epilogue_of<CF, KIND, kFinishAll>(w, acc, smem + CF::STAGE_ELEMS * 2 + wave * CF::OUT_BYTES, wr, wc, lane);
 }
 
 // Few rows a group (forward and dx): bound by reading the weights.  A
