@@ -17,7 +17,10 @@
  * and the DBuffer's other group operations (zero, scale, accumulate) over a
  * rank chunk or a whole bucket, the structure-aware planner that produces
  * bucket layouts (host only), and Muon's Newton-Schulz iteration on one
- * gathered matrix (MFMA).
+ * gathered matrix (MFMA).  Next to the optimizer stand the operators that make
+ * its gradients: a linear layer's products, dense or grouped by expert, in bf16
+ * or on matrices in 8-bit floating point, saved activations, and rows sorted
+ * by expert.
  *
  * Conventions shared by every entry point
  * ---------------------------------------

@@ -9,10 +9,14 @@
 // pass takes 64 slots at a time: ballots over the bits of the expert find the
 // lanes that share it, and a slot's rank among them is the number of lower
 // ones, so that equal experts keep the order of their slots and every call
-// gives the same places.
+// gives the same places.  The ballots cost 0.3 us for 64 slots of a wave, so
+// that chunks are short:
+// 32,768 slots over 256 experts 5 + 7 us in 16 workgroups, 11 + 22 in two.
 //
 // Gather, combine and its gradients go by token: a token's row is read (or
-// written) once, and each of its slots' rows once.  They are bound by HBM.
+// written) once, and each of its slots' rows once.  They are bound by HBM: 4096
+// tokens of 7168, 8 slots, gather 99 to 116 us (4.6 to 5.3 TB/s), combine 91 to
+// 106 (5.0 to 5.8), both gradients 187 to 208 (4.8 to 5.4).
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>
