@@ -631,7 +631,7 @@ ve_status ve_expert_sort(const void* experts, int32_t index_bytes, int64_t token
  * block_rows 1, no weights) on the way.  One pass: x is read once.  rows_len
  * rows are there; a slot whose position is not in [0, rows_len) is left out,
  * and rows without a slot are left as they are.  Two slots with one position
- * leave either's value.  Exactly one of rows and rows8->codes. */
+ * leave a mix of both rows (a sort gives no such positions).  Exactly one of rows and rows8->codes. */
 typedef struct {
     int64_t tokens, cols;
     int32_t slots;                              /* 1 .. 64 */
@@ -661,7 +661,8 @@ typedef struct {
 ve_status ve_expert_combine(const ve_expert_combine_args* a, void* stream);
 
 /* The gradients of ve_expert_combine (the residual's is dy itself):
- *   drows[position[t,j]] = bf16(weights[t,j] dy[t])   (rows without a slot are left as they are)
+ *   drows[position[t,j]] = bf16(weights[t,j] dy[t])   (rows without a slot are left as they are;
+ *                                                      two slots with one position: as for the gather)
  *   dweights[t,j] = sum_c dy[t,c] rows[position[t,j],c]   (fp32; 0 for slots left out)
  * Either may be NULL; rows is read for dweights only. */
 typedef struct {

@@ -916,19 +916,29 @@ __global__ void __launch_bounds__(64 * kFewWaves) k_fp8_few(Fp8Args g, int col_b
     finish8<kLinFwd>(g, e, row0 + row, n0 + c8, cnt, v, 0);
 }
 
-template <int MT, int U>
-hipError_t launch_few(Fp8Args g, hipStream_t s) {
-    const int64_t tiles = g.offsets ? std::min<int64_t>(g.T, g.T / (16 * MT) + g.E) : (g.T + 16 * MT - 1) / (16 * MT);
+// Workgroups of the few-row form: row tiles (with offsets the most that any
+// could need) and columns of each.
+struct FewGrid { int64_t tiles; int col_blocks, per; };
+FewGrid few_grid(const Fp8Args& g, int mt) {
+    FewGrid f;
+    f.tiles = g.offsets ? std::min<int64_t>(g.T, g.T / (16 * mt) + g.E) : (g.T + 16 * mt - 1) / (16 * mt);
     // Fewer columns a workgroup where 16 leave CUs without work (one token 8192
     // -> 1024: 7.7 us, with 16 columns 8.5), but not where that reads x of many
     // rows more often (32 rows 2880 -> 2880: 10.4 against 7.8).
-    const int per = MT == 1 && tiles * ((g.N + 15) / 16) < 2 * kCUs ? 8 : 16;
-    const int col_blocks = (int)((g.N + per - 1) / per);
+    f.per = mt == 1 && f.tiles * ((g.N + 15) / 16) < 2 * kCUs ? 8 : 16;
+    f.col_blocks = (int)((g.N + f.per - 1) / f.per);
+    return f;
+}
+int few_mt(const Fp8Args& g) { return g.offsets || g.T <= 16 ? 1 : 2; }
+
+template <int MT, int U>
+hipError_t launch_few(Fp8Args g, hipStream_t s) {
+    const FewGrid f = few_grid(g, MT);
     g.tiles_n = 1;
-    g.tiles = tiles;
-    const dim3 grid((unsigned)(tiles * col_blocks)), block(64 * kFewWaves);
-    if (g.format == VE_E4M3) hipLaunchKernelGGL((k_fp8_few<MT, U, VE_E4M3>), grid, block, 0, s, g, col_blocks, per);
-    else hipLaunchKernelGGL((k_fp8_few<MT, U, VE_E5M2>), grid, block, 0, s, g, col_blocks, per);
+    g.tiles = f.tiles;
+    const dim3 grid((unsigned)(f.tiles * f.col_blocks)), block(64 * kFewWaves);
+    if (g.format == VE_E4M3) hipLaunchKernelGGL((k_fp8_few<MT, U, VE_E4M3>), grid, block, 0, s, g, f.col_blocks, f.per);
+    else hipLaunchKernelGGL((k_fp8_few<MT, U, VE_E5M2>), grid, block, 0, s, g, f.col_blocks, f.per);
     return hipGetLastError();
 }
 
@@ -992,8 +1002,11 @@ LinPlan plan_fp8(const Fp8Args& g, LinKind kind) {
     // / 64 rows 14 / 19 / 26 / 47 against 33 / 34 / 34 / 30; 64 groups 7168 ->
     // 2048 of 1 / 4 / 8 rows on average 119 / 165 / 192 against 142 / 163 / 160.
     if (kind == kLinFwd && (pin == kPathFew || (pin == kPathAuto && g.T <= (g.offsets ? 4 * (int64_t)g.E : 32)))) {
-        p.path = kPathFew;
-        return p;
+        const FewGrid f = few_grid(g, few_mt(g));
+        if (f.tiles <= kMaxGridItems / (64 * kFewWaves) / f.col_blocks) {  // (else the tiles, which fit)
+            p.path = kPathFew;
+            return p;
+        }
     }
     const int64_t K = kind != kLinDw ? g.K : g.offsets ? (g.T / g.E + 127) / 128 * 64 : g.T;
     const int64_t nk = std::max<int64_t>(1, (K + BK - 1) / BK);
@@ -1025,7 +1038,7 @@ LinPlan plan_fp8(const Fp8Args& g, LinKind kind) {
 
 hipError_t launch_fp8(Fp8Args g, LinKind kind, const LinPlan& p, hipStream_t s) {
     if (kind == kLinDw && g.wide) return launch_exact(g, p, s);
-    if (p.path == kPathFew) return g.offsets || g.T <= 16 ? launch_few<1, 8>(g, s) : launch_few<2, 4>(g, s);
+    if (p.path == kPathFew) return few_mt(g) == 1 ? launch_few<1, 8>(g, s) : launch_few<2, 4>(g, s);
     if (p.path == kPath256)
         return kind == kLinDw ? launch_kind<Cfg256, kLinDw>(g, p, s) : launch_kind<Cfg256, kLinFwd>(g, p, s);
     return kind == kLinDw ? launch_kind<Cfg128, kLinDw>(g, p, s) : launch_kind<Cfg128, kLinFwd>(g, p, s);

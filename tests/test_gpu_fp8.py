@@ -726,3 +726,19 @@ def test_binding_refuses_rows_without_room():
         ve.fp8_unpack(ve.Fp8(torch.zeros(4, 100, dtype=torch.uint8, device=DEV).view(torch.float8_e4m3fn)[:, :96],
                              ve.new_fp8(4, 96, device=DEV).scales), out[:, :96])
     del c
+
+
+def test_more_workgroups_than_the_few_row_form_may_have():
+    """40,000 groups of one row each and 4,096 columns: 10 million workgroups of
+    512 threads would pass a grid's 2^32 threads, so the tiles take it."""
+    import torch
+    ve = _ve()
+    E, N, K = 40000, 4096, 16
+    w8 = ve.new_fp8(N, K, 128, groups=E, device=DEV)
+    w8.codes.view(torch.uint8).fill_(0x38)                 # 1.0
+    w8.scales.fill_(127)
+    x = torch.arange(E, device=DEV).remainder(16).to(torch.bfloat16)[:, None].expand(E, K).contiguous()
+    x8, y = ve.new_fp8(E, K, device=DEV), torch.zeros(E, N, dtype=torch.bfloat16, device=DEV)
+    ve.fp8_pack(x, x8)
+    ve.fp8_linear_forward(x8, w8, y, offsets=torch.arange(E + 1, device=DEV))
+    assert torch.equal(y, (x[:, :1] * K).expand(E, N))
