@@ -20,6 +20,7 @@ matrices packed in 8-bit floating point.
 from __future__ import annotations
 
 import ctypes as C
+import functools
 import os
 import weakref
 
@@ -460,15 +461,17 @@ def gemm_bf16_nt(P, Q, C=None, CT=None, D=None, alpha: float = 1.0, beta: float 
 _TYPES = None  # element types by size, and torch, once a call has needed them
 _torch = None
 _raw_stream = None  # torch's handle-only query of the current stream, where it has one (3 us less than the object)
+_get_device = None  # and of the current device
 
 
 def _types():
-    global _TYPES, _torch, _raw_stream
+    global _TYPES, _torch, _raw_stream, _get_device
     if _TYPES is None:
         import torch
         _TYPES = {1: (torch.int8, torch.uint8), 2: (torch.bfloat16, torch.int16, torch.uint16), 4: (torch.float32,)}
         _torch = torch
         _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        _get_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
     return _TYPES
 
 
@@ -560,8 +563,9 @@ def _scratch(need, device, stream):
 
 def _call(device, fn, *args):
     """A launching entry point with the tensors' device current."""
-    if _torch.cuda.current_device() == device.index:
-        return _check(fn(*args))
+    if _get_device() == device.index:
+        rc = fn(*args)
+        return _check(rc) if rc else None
     with _torch.cuda.device(device):
         return _check(fn(*args))
 
@@ -979,13 +983,18 @@ def _fp8_backward(dy, w_t, dx, dx_add, dy_t, x_t, dw, accumulate, offsets, token
 
 def _slots(t, shape, dtypes, name, device):
     """Pointer of a contiguous device tensor of [tokens, slots] values."""
-    if t.dtype not in dtypes:
-        raise ValueError(f"{name}: need {' or '.join(str(d) for d in dtypes)} elements")
     if t.device != device or not t.is_cuda or not t.is_contiguous():
         raise ValueError(f"{name}: must be a contiguous device tensor on {device}")
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name}: need {' or '.join(str(d) for d in dtypes)} elements")
     if shape is not None and t.shape != shape:
         raise ValueError(f"{name}: shape {tuple(t.shape)} != {tuple(shape)}")
     return t.data_ptr()
+
+
+@functools.lru_cache(maxsize=256)
+def _sort_scratch(tokens, slots, groups):
+    return expert_sort_workspace(tokens, slots, groups)
 
 
 def expert_sort(experts, offsets, position, order=None, workspace=None, stream=None):
@@ -1009,16 +1018,14 @@ def expert_sort(experts, offsets, position, order=None, workspace=None, stream=N
     L, handle = lib(), _stream_on(dev, stream)
     n = offsets.shape[0] - 1
     if workspace is None:
-        need = C.c_int64()
-        _check(L.ve_expert_sort_workspace(T, k, n, C.byref(need)))
-        ws, size = (_scratch(need.value, dev, stream), need.value) if need.value else (None, 0)
+        size = _sort_scratch(T, k, n)
+        ws = _scratch(size, dev, stream) if size else None
     else:
         if workspace.device != dev:
             raise ValueError("workspace: must be on the tensors' device")
         _require_buffer(workspace, 0, 1, "workspace")
         ws, size = workspace, workspace.numel()
-    _call(dev, L.ve_expert_sort, e, experts.element_size(), T, k, n, o, p, r, 0 if ws is None else ws.data_ptr(), size,
-          handle)
+    _call(dev, L.ve_expert_sort, e, experts.itemsize, T, k, n, o, p, r, 0 if ws is None else ws.data_ptr(), size, handle)
 
 
 def expert_sort_workspace(tokens: int, slots: int, groups: int) -> int:
