@@ -775,35 +775,38 @@ class Fp8:
         """(record, group strides of codes and of scales)"""
         _types()
         c, s, b = self.codes, self.scales, self.block_rows
-        if b not in (1, 128):
-            raise ValueError(f"{name}: {b} rows share a scale, not 1 or 128")
-        if c.dtype == _torch.float8_e4m3fn:
-            fmt = 0
-        elif c.dtype == _torch.float8_e5m2:
-            fmt = 1
+        if b == 1:
+            n = rows
+        elif b == 128:
+            n = -(-rows // 128)
         else:
+            raise ValueError(f"{name}: {b} rows share a scale, not 1 or 128")
+        dtype = c.dtype
+        if dtype != _torch.float8_e4m3fn and dtype != _torch.float8_e5m2:
             raise ValueError(f"{name}.codes: need a float8_e4m3fn or float8_e5m2 tensor")
-        ptr, ld, cg = _rows8(c, groups, rows, cols, 16, f"{name}.codes", device)
         if s.dtype != _torch.uint8:
             raise ValueError(f"{name}.scales: need uint8 elements")
-        sptr, lds, sg = _rows8(s, groups, -(-cols // 128), -(-rows // b), 4, f"{name}.scales", device)
-        return _Fp8(ptr, ld, sptr, lds, fmt, b), cg, sg
+        ptr, ld, cg = _rows8(c, groups, rows, cols, 16, name, device)
+        sptr, lds, sg = _rows8(s, groups, -(-cols // 128), n, 4, name, device)
+        return _Fp8(ptr, ld, sptr, lds, 0 if dtype == _torch.float8_e4m3fn else 1, b), cg, sg
 
 
 def _rows8(t, groups, rows, cols, unit, name, device):
     """(pointer, leading dimension, group stride) of a tensor of bytes whose
-    rows start on `unit` bytes and have memory up to the next multiple."""
-    shape = (rows, cols) if groups is None else (groups, rows, cols)
-    if t.shape != shape:
-        raise ValueError(f"{name}: shape {tuple(t.shape)} != {shape}")
-    if t.device != device or not t.is_cuda:
-        raise ValueError(f"{name}: must be a device tensor on {device}")
+    rows start on `unit` bytes (codes 16, scales 4) and have memory up to the
+    next multiple."""
     st = t.stride()
-    if st[-1] != 1 and cols > 1:
-        raise ValueError(f"{name}: rows must be contiguous")
+    if (t.shape != ((rows, cols) if groups is None else (groups, rows, cols)) or t.device != device or not t.is_cuda
+            or (st[-1] != 1 and cols > 1)):
+        what = f"{name}.{'codes' if unit == 16 else 'scales'}"
+        if t.device != device or not t.is_cuda:
+            raise ValueError(f"{what}: must be a device tensor on {device}")
+        if st and st[-1] != 1 and cols > 1:
+            raise ValueError(f"{what}: rows must be contiguous")
+        raise ValueError(f"{what}: shape {tuple(t.shape)} != {(rows, cols) if groups is None else (groups, rows, cols)}")
     whole = -(-cols // unit) * unit
     ld = st[-2] if rows > 1 else whole
-    group = st[0] if groups is not None else 0
+    group = 0 if groups is None else st[0]
     if whole != cols and t.numel():
         end = t.storage_offset() + ((groups or 1) - 1) * group + (rows - 1) * ld + whole
         if end > t.untyped_storage().nbytes():
