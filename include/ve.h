@@ -491,8 +491,8 @@ ve_status ve_linear_backward(const ve_linear_backward_args* a, void* workspace, 
  *
  * Layout.  A row of codes starts on 16 bytes and is followed by zeros up to
  * the next multiple of 16 (the products read them); long rows are read faster
- * where they start on 128 bytes (8192 tokens, 8192 -> 28672: 1,417 us, with rows
- * 16 or 64 bytes longer 1,763 and 1,684).  The scales are stored
+ * where they start on 128 bytes (8192 tokens, 8192 -> 28672: 1,447 us, with rows
+ * 16 or 64 bytes longer 1,780 and 1,716).  The scales are stored
  * with the rows' index along memory, so that a tile's scales of one
  * contraction step are one short run of bytes: row j holds those of columns
  * [128 j, 128 (j + 1)), starts on 4 bytes and may be read up to the next
