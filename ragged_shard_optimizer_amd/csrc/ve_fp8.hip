@@ -46,8 +46,10 @@ __device__ __forceinline__ f32x16 mfma_fp8(i32x8 b, i32x8 a, f32x16 c, int eb, i
                              : __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(b, a, c, 0, 1, 0, eb, 0, ea);
 }
 
-// 32 codes times a power of two, as bf16: exact (values below 2^-126 may
-// become 0).
+// 32 codes times a power of two, as bf16: exact where no value leaves bf16's
+// normal numbers (bf16_exponent), which a block's largest may by rounding up to
+// 2^128 when it was packed, and any may where the other operand's scale brings
+// the product back.
 struct Wide { bf16x8 v[4]; };
 __device__ __forceinline__ Wide widen(i32x8 c, int e, int format) {
     typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
@@ -65,6 +67,21 @@ __device__ __forceinline__ Wide widen(i32x8 c, int e, int format) {
         w.v[i >> 1][4 * (i & 1) + 3] = hi[1];
     }
     return w;
+}
+
+// Every code under this exponent is a normal number of bf16: the smallest, 2^-9
+// (E4M3) or 2^-16 (E5M2), is at least 2^-126, and the largest, below 2^9 or
+// 2^16, below 2^128.
+__device__ __forceinline__ bool bf16_exponent(int e, int format) {
+    return (uint32_t)((e & 255) - (format == VE_E4M3 ? 10 : 17)) <= (format == VE_E4M3 ? 236u : 222u);
+}
+
+// ... under all four of a dword.
+__device__ __forceinline__ bool bf16_exponents(uint32_t e, int format) {
+    bool all = true;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) all &= bf16_exponent((int)(e >> (8 * i)), format);
+    return all;
 }
 
 // A lane's 32 codes of row r0 + lane % 32, half kk of the block.
@@ -91,6 +108,8 @@ struct Exponents {
         const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc((void*)p, (short)0, live ? all : 0, 0x00020000);
         return (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(rs, lane <= 32 ? (row & ~3) + 4 * lane : (int)0x80000000, 0, 0);
     }
+    // whether a lane's dword has some of the wave's first n rows
+    __device__ __forceinline__ bool holds(int lane, int n) const { return 4 * lane < (row & 3) + n; }
     __device__ __forceinline__ void next() { p += ld; }
     __device__ __forceinline__ void stash(uint32_t& keep, int at) const {
         put_lane(keep, at, (uint32_t)(uintptr_t)p);
@@ -744,10 +763,27 @@ __global__ void __launch_bounds__(CF::THREADS, CF::PER_CU) k_fp8(Fp8Args g) {
     __builtin_amdgcn_s_waitcnt(kWaitAll);
 }
 
+// Whether a lane's half of row 32 f + lane % 32, of `rows` from r0 on, holds what
+// bf16 cannot under exponent e: a code other than 0, or a NaN scale.
+template <class Op>
+__device__ __forceinline__ bool leaves_bf16(const uint16_t* st, int r0, int f, int lane, int rows, int e, int format) {
+    if (32 * f + (lane & 31) >= rows || bf16_exponent(e, format)) return false;
+    uint32_t any = (e & 255) == 255;
+#pragma unroll
+    for (int kk = 0; kk < 2; ++kk) {
+        const i32x8 c = fragment<Op>(st, r0 + 32 * f, kk, lane);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) any |= (uint32_t)c[i] & 0x7f7f7f7fu;
+    }
+    return any != 0;
+}
+
 // dw in fp32: one item a workgroup, codes turned to bf16 between LDS and the
 // MFMAs.  One stage of LDS and three workgroups a CU, which load and compute in
-// turn: 927 us at 8192^3 (1,186 TFLOP/s; two workgroups 963), and 16 groups of
-// 777 rows 2880 -> 2880, whose 0.53 GB of results bind, 109 us (4.9 TB/s; 132).
+// turn: 887 us at 8192^3 (1,240 TFLOP/s; with two workgroups 4% longer), and 16
+// groups of 777 rows 2880 -> 2880, whose 0.53 GB of results bind, 113 us (4.7
+// TB/s; with two 122).  Looking for what bf16 cannot hold takes 3% of the first
+// (860 us without), 10% where blocks of zeros make it look at codes.
 template <class CF, int FORMAT>
 __global__ void __launch_bounds__(CF::THREADS, 3) k_fp8_exact(Fp8Args g) {
     constexpr int KIND = kLinDw;
@@ -767,33 +803,56 @@ __global__ void __launch_bounds__(CF::THREADS, 3) k_fp8_exact(Fp8Args g) {
     A.init(g.A + w.row0 * g.lda + w.begin, g.lda, w.rows, w.len, lane, wave);
     B.init(g.B + w.col0 * g.ldb + w.begin, g.ldb, cols, w.len, lane, wave);
     Exponents XA, XB;
-    XA.init(g.sa + (w.begin / BK + w.kbeg) * g.ld_sa, g.ld_sa, w.row0 + wr * WM, g.sa_rows);
-    XB.init(g.sb + (w.begin / BK + w.kbeg) * g.ld_sb, g.ld_sb, w.col0 + wc * WN, g.sb_rows);
-    f32x16 acc[TM][TN];
-#pragma unroll
-    for (int a = 0; a < TM; ++a)
-#pragma unroll
-        for (int b = 0; b < TN; ++b)
-#pragma unroll
-            for (int r = 0; r < 16; ++r) acc[a][b][r] = 0.f;
     uint16_t* st = (uint16_t*)smem;
-    for (int kt = w.kbeg; kt < w.kbeg + w.nk; ++kt) {
+    f32x16 acc[TM][TN];
+    uint32_t raw_a, raw_b;
+    auto start = [&]() {
+        XA.init(g.sa + (w.begin / BK + w.kbeg) * g.ld_sa, g.ld_sa, w.row0 + wr * WM, g.sa_rows);
+        XB.init(g.sb + (w.begin / BK + w.kbeg) * g.ld_sb, g.ld_sb, w.col0 + wc * WN, g.sb_rows);
+#pragma unroll
+        for (int a = 0; a < TM; ++a)
+#pragma unroll
+            for (int b = 0; b < TN; ++b)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) acc[a][b][r] = 0.f;
+    };
+    auto load = [&](int kt) {
         A.begin(kt, true);
         B.begin(kt, true);
 #pragma unroll
         for (int q = 0; q < OpA::PIECES; ++q) A.piece(st, q);
 #pragma unroll
         for (int q = 0; q < OpB::PIECES; ++q) B.piece(st + CF::A_ELEMS, q);
-        const uint32_t raw_a = XA.load(lane, true), raw_b = XB.load(lane, true);
+        raw_a = XA.load(lane, true);
+        raw_b = XB.load(lane, true);
         XA.next();
         XB.next();
         __builtin_amdgcn_s_waitcnt(kWaitAll);
-        __syncthreads();
-        int ea[TM], eb[TN];
+    };
+    int ea[TM], eb[TN];
+    auto exponents = [&]() {
 #pragma unroll
         for (int a = 0; a < TM; ++a) ea[a] = spread(raw_a, XA.row, a, lane);
 #pragma unroll
         for (int b = 0; b < TN; ++b) eb[b] = spread(raw_b, XB.row, b, lane);
+    };
+    start();
+    const int rows_in = w.rows - wr * WM, cols_in = cols - wc * WN;  // the wave's rows and columns that exist
+    const bool dword_a = XA.holds(lane, min(WM, rows_in)), dword_b = XB.holds(lane, min(WN, cols_in));
+    bool past = false;
+    for (int kt = w.kbeg; kt < w.kbeg + w.nk; ++kt) {
+        load(kt);
+        // Exponents past bf16's are seldom, but for blocks of zeros, which have
+        // 0: looked for in the dwords, while the others' loads land.
+        const bool seldom = __any((dword_a && !bf16_exponents(raw_a, FORMAT)) || (dword_b && !bf16_exponents(raw_b, VE_E4M3)));
+        __syncthreads();
+        exponents();
+        if (seldom) {
+#pragma unroll
+            for (int a = 0; a < TM; ++a) past |= leaves_bf16<OpA>(st, wr * WM, a, lane, rows_in, ea[a], FORMAT);
+#pragma unroll
+            for (int b = 0; b < TN; ++b) past |= leaves_bf16<OpB>(st + CF::A_ELEMS, wc * WN, b, lane, cols_in, eb[b], VE_E4M3);
+        }
 #pragma unroll
         for (int kk = 0; kk < 2; ++kk) {
             i32x8 fa[TM], fb[TN];
@@ -815,6 +874,45 @@ __global__ void __launch_bounds__(CF::THREADS, 3) k_fp8_exact(Fp8Args g) {
                         acc[a][b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(wb[b].v[q], wa[a].v[q], acc[a][b], 0, 0, 0);
         }
         __syncthreads();
+    }
+    // Where any wave met such values, all take the item again with the 8-bit
+    // MFMAs, which take every scale and cut nothing where only one of 8
+    // consecutive products is not 0: 8 passes over each half of a block.  (In
+    // the loop above a second way to the sums would cost it 14%.)
+    uint32_t* met = (uint32_t*)smem;
+    if (lane == 0) met[wave] = 0;
+    if (past) met[wave] = 1;
+    __syncthreads();
+    bool again = false;
+#pragma unroll
+    for (int v = 0; v < CF::WAVES; ++v) again |= __builtin_amdgcn_readfirstlane((int)met[v]) != 0;
+    __syncthreads();
+    if (again) {
+        start();
+        for (int kt = w.kbeg; kt < w.kbeg + w.nk; ++kt) {
+            load(kt);
+            __syncthreads();
+            exponents();
+#pragma unroll 1
+            for (int pass = 0; pass < 16; ++pass) {
+                const int kk = pass & 1, at = pass >> 1;
+                const uint32_t keep = 255u << (8 * (at & 3));
+                i32x8 fa[TM], fb[TN];
+#pragma unroll
+                for (int a = 0; a < TM; ++a) {
+                    fa[a] = fragment<OpA>(st, wr * WM + a * 32, kk, lane);
+#pragma unroll
+                    for (int c = 0; c < 8; ++c) fa[a][c] &= (c & 1) == at >> 2 ? (int)keep : 0;
+                }
+#pragma unroll
+                for (int b = 0; b < TN; ++b) fb[b] = fragment<OpB>(st + CF::A_ELEMS, wc * WN + b * 32, kk, lane);
+#pragma unroll
+                for (int a = 0; a < TM; ++a)
+#pragma unroll
+                    for (int b = 0; b < TN; ++b) acc[a][b] = mfma_fp8(fb[b], fa[a], acc[a][b], eb[b], ea[a], FORMAT);
+            }
+            __syncthreads();
+        }
     }
     if (g.finish == kFinishWide) dw_epilogue_fp32<CF, false>(w, acc, wr, wc, lane);
     else if (g.finish == kFinishWideAdd) dw_epilogue_fp32<CF, true>(w, acc, wr, wc, lane);
