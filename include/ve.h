@@ -609,7 +609,10 @@ typedef struct {
 } ve_fp8_linear_backward_args;
 /* Workspaces and errors are as for ve_linear_forward and ve_linear_backward;
  * beyond those, a misaligned matrix, an unknown format or one the operand may
- * not have, and a block_rows other than the operand's are VE_ERR_INVALID_ARG. */
+ * not have, and a block_rows other than the operand's are VE_ERR_INVALID_ARG;
+ * rows of codes (ld_codes) more than 2^22 bytes apart, for dy_t and x_t 2^24
+ * bytes or more, are VE_ERR_UNSUPPORTED (so dw takes fewer than 2^24 columns:
+ * 65,536 groups of 8.4 million tokens, or 16.7 million tokens of one group). */
 ve_status ve_fp8_linear_forward_workspace(const ve_fp8_linear_forward_args* a, int64_t* bytes);
 ve_status ve_fp8_linear_forward(const ve_fp8_linear_forward_args* a, void* workspace, int64_t workspace_bytes, void* stream);
 ve_status ve_fp8_linear_backward_workspace(const ve_fp8_linear_backward_args* a, int64_t* bytes);

@@ -927,7 +927,7 @@ def fp8_linear_backward(dy: Fp8 = None, w_t: Fp8 = None, dx=None, dx_add=None, d
     """``ve_fp8_linear_backward``: ``dx`` (bf16, plus ``dx_add``) from ``dy``
     [tokens, out] and ``w_t`` ([groups,] in, out), and ``dw`` (bf16 or fp32,
     added to what it holds with ``accumulate``) from ``dy_t`` [out, columns]
-    and ``x_t`` [in, columns], columns = fp8_columns(tokens, groups), as
+    and ``x_t`` [in, columns], columns = fp8_columns(tokens, groups) < 2^24, as
     :func:`fp8_pack` and :func:`fp8_pack_weight` transpose them.  Either
     gradient may be None; ``tokens`` is needed where ``dx`` is."""
     _fp8_backward(dy, w_t, dx, dx_add, dy_t, x_t, dw, accumulate, offsets, tokens, workspace, stream, False)

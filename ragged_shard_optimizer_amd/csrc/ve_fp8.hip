@@ -1110,9 +1110,10 @@ LinPlan plan_fp8(const Fp8Args& g, LinKind kind) {
     const int64_t K = kind != kLinDw ? g.K : g.offsets ? (g.T / g.E + 127) / 128 * 64 : g.T;
     const int64_t nk = std::max<int64_t>(1, (K + BK - 1) / BK);
     const bool may_split = !g.offsets && option(kOptLinearSplit) != 0;
+    const bool far = 2 * std::max(g.lda, g.ldb) >= kFp8Pitch256;  // (lda, ldb: of 2 bytes)
     double best = 0;
     for (int path : {(int)kPath128, (int)kPath256}) {
-        if (exact ? path != kPath128 : (pin == kPath128 || pin == kPath256) && pin != path) continue;
+        if (exact || far ? path != kPath128 : (pin == kPath128 || pin == kPath256) && pin != path) continue;
         int64_t tiles = path == kPath256 ? tiles_of<Cfg256>(g, kind) : tiles_of<Cfg128>(g, kind);
         // (ragged rows: two thirds of a tile more a group, not the most any offsets could need)
         if (kind == kLinFwd && g.offsets) {

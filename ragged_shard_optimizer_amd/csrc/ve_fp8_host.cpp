@@ -46,10 +46,17 @@ ve_status check_e4m3(const ve_fp8& q, const char* name) {
     return q.format == VE_E4M3 ? VE_OK : fail(VE_ERR_INVALID_ARG, "%s: must be E4M3", name);
 }
 
-// Rows of codes within 32-bit byte offsets of a tile's first.
 ve_status check_pitch(const ve_fp8& q, const char* name) {
     if (q.ld_codes > int64_t(1) << 22 || q.ld_scales > kMaxDim)
         return fail(VE_ERR_UNSUPPORTED, "%s: rows more than 2^22 bytes apart", name);
+    return VE_OK;
+}
+
+// dw's operands, whose rows are as long as the groups' runs together: the rows
+// of a tile within 32-bit byte offsets of its first.
+ve_status check_pitch_t(const ve_fp8& q, const char* name) {
+    if (q.ld_codes >= kFp8Pitch128 || q.ld_scales > kMaxDim)
+        return fail(VE_ERR_UNSUPPORTED, "%s: rows 2^24 bytes apart or more", name);
     return VE_OK;
 }
 
@@ -113,8 +120,8 @@ ve_status check_backward(const ve_fp8_linear_backward_args& a) {
     }
     if (a.dw) {
         if (T > 0 && ((st = check_fp8(a.dy_t, N, C, 1, "dy_t")) != VE_OK || (st = check_fp8(a.x_t, K, C, 1, "x_t")) != VE_OK ||
-                      (st = check_e4m3(a.x_t, "x_t")) != VE_OK || (st = check_pitch(a.dy_t, "dy_t")) != VE_OK ||
-                      (st = check_pitch(a.x_t, "x_t")) != VE_OK))
+                      (st = check_e4m3(a.x_t, "x_t")) != VE_OK || (st = check_pitch_t(a.dy_t, "dy_t")) != VE_OK ||
+                      (st = check_pitch_t(a.x_t, "x_t")) != VE_OK))
             return st;
         if (a.lddw < K) return fail(VE_ERR_INVALID_ARG, "leading dimension smaller than the row");
         if (a.groups > 1 && a.dw_group < (N - 1) * a.lddw + K)

@@ -19,6 +19,9 @@ struct Fp8Args : LinArgs {
     int32_t format;                              // of A (B is E4M3)
     int64_t sa_rows, sb_rows;                    // exponents in a row, up to a multiple of 4
 };
+// Operands' rows are less than this many bytes apart, so that all of a tile's
+// lie within 2^31 bytes of its first: of 128 x 128 and of 256 x 256 tiles.
+constexpr int64_t kFp8Pitch128 = int64_t(1) << 24, kFp8Pitch256 = int64_t(1) << 23;
 LinPlan plan_fp8(const Fp8Args& g, LinKind kind);
 hipError_t launch_fp8(Fp8Args g, LinKind kind, const LinPlan& p, hipStream_t s);
 
