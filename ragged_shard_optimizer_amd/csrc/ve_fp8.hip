@@ -16,11 +16,16 @@
 // How exact the sums are: the unit aligns the products of 8 consecutive codes
 // to the largest of them, cuts each 13 bits below it, and adds the sums of
 // eight in fp32 (measured: 2^16 + 7 times 2^2 comes back as 2^16, with the
-// products 8 apart exactly).  On normal values the error is 2^-16.2 of the
-// result's rms, far below the 2^-9 of a bf16 result's rounding and the 2^-4 of
-// the codes.  For dw in fp32 the codes are turned to bf16 on the way to the
-// bf16 MFMAs, whose sums are exact to fp32 (2^-27.6), at half the rate; the
-// unscaled 8-bit MFMA 32x32x16 cuts products the same way, and is no faster.
+// products 8 apart exactly), so that each of 8 loses up to 2^-13 of the largest.
+// On normal values the error is 2^-16.2 of the result's rms, far below the 2^-8
+// of a bf16 result's rounding and the 2^-4 of the codes, and bf16 results take
+// it.  Beside what is left where large products cancel it is not small: columns
+// 2^9 times the rest, in pairs that cancel, leave errors of up to 10% of the
+// rms.  For dw in fp32 the codes are turned to bf16 on the way to the bf16
+// MFMAs, whose sums are exact to fp32 (2^-27.6), at half the rate; tiles with
+// values that bf16 cannot hold take the scaled MFMAs, one of 8 consecutive
+// products at a time, which are not cut.  The unscaled 8-bit MFMA 32x32x16 cuts
+// products the same way, and is no faster.
 //
 // MFMA 32x32x64, operands swapped (output columns as the first operand): the
 // accumulator's layout is that of ve_linear.hip.  A lane gives 32 codes of one
