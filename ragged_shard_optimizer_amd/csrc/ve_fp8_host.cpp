@@ -127,7 +127,7 @@ ve_status check_backward(const ve_fp8_linear_backward_args& a) {
         if (a.groups > 1 && a.dw_group < (N - 1) * a.lddw + K)
             return fail(VE_ERR_INVALID_ARG, "group stride smaller than a group");
     }
-    if (!launchable(T, K, a.groups, 1) || !launchable(N, K, 0, a.groups))
+    if ((a.dx && !launchable(T, K, a.groups, 1)) || (a.dw && !launchable(N, K, 0, a.groups)))
         return fail(VE_ERR_UNSUPPORTED, "product too large for one launch");
     return VE_OK;
 }

@@ -55,3 +55,20 @@ def test_rows_of_the_other_operands(ld, rc):
         a = ve._Fp8Backward(tokens=300, in_features=200, out_features=100, groups=1, dx=3 * P, lddx=200,
                             dy=_q(1, 300, 100, ld=ld if which == "x" else None), w_t=_q(2, 200, 100, 128, ld if which == "w" else None))
         assert L.ve_fp8_linear_backward_workspace(C.byref(a), C.byref(n)) == rc
+
+
+def test_one_gradient_is_not_refused_for_the_other_ones_size():
+    """16 million tokens of 8192 features are too many tiles of dx, 65,536 weights
+    of 1024 x 1024 too many of dw."""
+    L, n, T, E = ve.lib(), C.c_int64(-1), 1 << 20, 65536
+    a = ve._Fp8Backward(tokens=T * 15, in_features=8192, out_features=8192, groups=1, dy_t=_q(2, 8192, T * 15), x_t=_q(3, 8192, T * 15),
+                        dw=4 * P, lddw=8192)
+    assert L.ve_fp8_linear_backward_workspace(C.byref(a), C.byref(n)) == OK
+    a.dx, a.lddx, a.dy, a.w_t = 5 * P, 8192, _q(6, T * 15, 8192), _q(7, 8192, 8192, 128)
+    assert L.ve_fp8_linear_backward_workspace(C.byref(a), C.byref(n)) == UNSUP
+    a = ve._Fp8Backward(tokens=300, in_features=1024, out_features=1024, groups=E, offsets=P, dx=5 * P, lddx=1024,
+                        dy=_q(6, 300, 1024), w_t=_q(7, 1024, 1024, 128), w_codes_group=1 << 20, w_scales_group=64)
+    assert L.ve_fp8_linear_backward_workspace(C.byref(a), C.byref(n)) == OK
+    cols = ve.fp8_columns(300, E)
+    a.dw, a.lddw, a.dw_group, a.dy_t, a.x_t = 4 * P, 1024, 1 << 20, _q(2, 1024, cols), _q(3, 1024, cols)
+    assert L.ve_fp8_linear_backward_workspace(C.byref(a), C.byref(n)) == UNSUP
