@@ -240,7 +240,7 @@ ve_status ve_dbuffer_group_op(const ve_plan* plan, int32_t rank, int32_t op, flo
  *       whole 16 bytes are laid out anew in the workspace), 4 = the forward
  *       form for few tokens; 0 = chosen by shape (2, 3 and 4 pin those of
  *       the products on matrices in 8-bit floating point too, except where
- *       dw is fp32);
+ *       dw is fp32 or its operands' rows are 2^23 bytes apart or more);
  *   "linear_split" (VE_LINEAR_SPLIT, 1): 0 = never cut their contraction
  *       into slices (the options must not change between a workspace query
  *       and the call it is for).

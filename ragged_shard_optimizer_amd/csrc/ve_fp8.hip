@@ -492,9 +492,9 @@ __device__ __forceinline__ Fp8Args fp8_args_again() {
 // The exponents of a step are two loads of a dword a lane, two steps ahead,
 // which the lanes exchange once the step's tile is there.
 //
-// 8192 tokens, 8192 -> 28672: 1,399 to 1,440 us (2,670 to 2,750 TFLOP/s; the
-// library's product with one scale a matrix 3,000 to 3,160), with SiLU and z
-// 1,570 to 1,590; dw at 8192^3 2,550 to 2,820 TFLOP/s.  By the counters the
+// 8192 tokens, 8192 -> 28672: 1,440 to 1,515 us once warm (2,540 to 2,670
+// TFLOP/s; the library's product with one scale a matrix 3,000 to 3,160), with
+// SiLU and z 1,560 to 1,600; dw at 8192^3 2,520 to 2,760 TFLOP/s.  By the counters the
 // MFMAs are busy 66% of the cycles at 1.93 GHz: the rest of a step waits for
 // its loads, which have half a step to land.  Barriers and loads at other
 // places of the step were within 1%.
@@ -785,9 +785,9 @@ __device__ __forceinline__ bool leaves_bf16(const uint16_t* st, int r0, int f, i
 
 // dw in fp32: one item a workgroup, codes turned to bf16 between LDS and the
 // MFMAs.  One stage of LDS and three workgroups a CU, which load and compute in
-// turn: 887 us at 8192^3 (1,240 TFLOP/s; with two workgroups 4% longer), and 16
-// groups of 777 rows 2880 -> 2880, whose 0.53 GB of results bind, 113 us (4.7
-// TB/s; with two 122).  Looking for what bf16 cannot hold takes 3% of the first
+// turn: 887 to 922 us at 8192^3 (1,190 to 1,240 TFLOP/s; with two workgroups 4%
+// longer), and 16 groups of 777 rows in all, 2880 -> 2880, whose 0.53 GB of
+// results bind, 113 us (4.7 TB/s; with two 122).  Looking for what bf16 cannot hold takes 3% of the first
 // (860 us without), 10% where blocks of zeros make it look at codes.
 template <class CF, int FORMAT>
 __global__ void __launch_bounds__(CF::THREADS, 3) k_fp8_exact(Fp8Args g) {

@@ -8,11 +8,13 @@
 // LDS).  The transposed codes are turned 8 x 8 in registers and go through
 // 16 KB of LDS, 8-byte pieces permuted by XOR so that writes and reads touch
 // distinct banks, so that memory sees whole 128-byte lines both ways.  Bound by
-// HBM: 16 weights of 2048 x 7168 both ways 167 us (5.6 TB/s; with 4 rows a
-// thread in twice the threads 173), 16000 x 7168 rows both ways 91 us (5.1
-// TB/s), rows only 67 (5.1); restoring 16 x 2048 x 7168 138 to 141 us (5.0 to
-// 5.1 TB/s).  A short batch is bound by latency: 500 x 2880 both ways 6 us, in
-// 16 groups, whose tiles are searched first, 9.
+// HBM: 16 weights of 2048 x 7168 both ways 167 to 182 us (5.2 to 5.6 TB/s; with
+// 4 rows a thread in twice the threads 173 beside 167), 16000 x 7168 rows both
+// ways 91 to 98 us (4.7 to 5.1 TB/s), rows only 67 (5.1); restoring 16 x 2048 x
+// 7168 137 to 141 us (5.0 to 5.1 TB/s).  Through an activation's slope (whose z
+// is loaded row by row, where it is needed) 267 us with SiLU, 278 with GELU (2.5
+// TB/s).  A short batch is bound by latency: 500 x 2880 in 16 groups, whose tiles
+// are searched first, 11.4 to 12.4 us in a trace.
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>
