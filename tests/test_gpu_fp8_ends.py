@@ -203,3 +203,41 @@ def test_forward_and_dx(T, K, N, sign, fmt):
             _within(_host(y), ref, bound, ("y", path))
             ve.fp8_linear_backward(dy=xq, w_t=wq, dx=y.zero_())
             _within(_host(y), ref, bound, ("dx", path))
+
+
+@pytest.mark.parametrize("sign", [0, 1])
+def test_infinities_of_e5m2(sign):
+    """An infinity times a value is one, times 0 NaN, and two of opposite sign
+    NaN, in every product; elements without one are as ever.  sign 1: beside
+    scales at the ends."""
+    import torch
+    ve = _ve()
+    T, K, N = 70, 640, 140
+    x, w = _operand(T, K, 1, "e5m2", sign, 12), _operand(N, K, 128, "e4m3", -sign, 13)
+    x[0][3, 5], x[0][3, 300], x[0][9, 639], x[0][11, 0], x[0][11, 64] = 0x7C, 0x7C, 0xFC, 0x7C, 0xFC
+    w[0][7, 5] = w[0][8, 639] = 0
+    x, w = (*x[:2], fp8.unpack(*x[:2], 1, "e5m2")), (*w[:2], fp8.unpack(*w[:2], 128))
+    with np.errstate(invalid="ignore"):
+        prod = [[x[2][t] * w[2][n] for n in range(N)] for t in (3, 9, 11)]
+        want = np.array([[p.sum() for p in row] for row in prod])
+    assert np.isinf(want).any() and np.isnan(want).any()
+    fine = np.ones(T, bool)
+    fine[[3, 9, 11]] = False
+    ref, z, mag = linear.forward(x[2][fine], w[2])
+    lost = cut(x[2][fine], w[2])
+    bound = forward_bounds(ref, z, mag, lost, K, "none")[1]
+    exact = gamma(K + 130) * mag + TINY
+    xq, wq = device(*x[:2], fmt="e5m2"), device(*w[:2], 128)
+    rows = device(w[0], np.repeat(w[1], 128, 1)[:, :N])
+    for path in (0, 2, 3, 4):
+        with ve.options(linear_path=path):
+            out = {k: torch.empty(T, N, dtype=d, device=DEV) for k, d in
+                   (("y", torch.bfloat16), ("dx", torch.bfloat16), ("dw", torch.bfloat16), ("dw32", torch.float32))}
+            ve.fp8_linear_forward(xq, wq, out["y"])
+            ve.fp8_linear_backward(dy=xq, w_t=wq, dx=out["dx"])
+            for k in ("dw", "dw32"):
+                ve.fp8_linear_backward(dy_t=xq, x_t=rows, dw=out[k], tokens=K)
+        for k, t in out.items():
+            got = _host(t)
+            assert np.array_equal(got[[3, 9, 11]], want, equal_nan=True), (k, path)
+            _within(got[fine], ref, exact if k == "dw32" else rounded(exact + lost, ref) if k == "dw" else bound, (k, path))
